@@ -406,6 +406,241 @@ pb_status pb_gemm_bf16_static(int32_t M, int32_t N, int32_t K, const void* A, co
 pb_status pb_swa_attention(const pb_dims* dims, const void* qk, const void* vt, void* act,
                            int64_t act_ld, int* status, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Positions: the norm of every query and key head and its rotation, in one pass between a
+ * projection and pb_swa_attention, and its backward pass. For a head x of head_dim values,
+ *   n = x / sqrt(mean x^2 + eps) * gamma               (skipped where gamma is NULL)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t)   for every rotated pair of n,
+ * t = position on the pair's axis x the pair's frequency. Computed in fp32, rounded once to
+ * bf16; the angle's place in its turn is exact to 2^-33 at any position.
+ * ---------------------------------------------------------------------------------- */
+
+#define PB_ROPE_MAX_AXES 4
+
+/* Pair i of the rot_dim / 2: values (i, i + rot_dim / 2), or (2i, 2i + 1). */
+typedef enum pb_rope_pairing { PB_ROPE_HALVES = 0, PB_ROPE_ADJACENT = 1 } pb_rope_pairing;
+/* Frequency of pair i: theta^(-2i / rot_dim) over all pairs, or on each axis from 1 on,
+ * theta^(-j / n) for pair j of the axis's n. */
+typedef enum pb_rope_ladder { PB_ROPE_SHARED = 0, PB_ROPE_PER_AXIS = 1 } pb_rope_ladder;
+
+/* A rotation's plan, filled by pb_rope_init and only read by the calls: a plain value in
+ * host memory that may be copied and shared between threads. */
+typedef struct pb_rope {
+  uint32_t magic;
+  int32_t head_dim;
+  int32_t rot_dim;
+  int32_t pairing;
+  int32_t axes;
+  int32_t section_end[PB_ROPE_MAX_AXES];
+  uint64_t turns[128]; /* frequency of each pair, 2^-64 turns a position */
+} pb_rope;
+
+/* head_dim: a multiple of 16, 16 to 256 (else PB_ERR_UNSUPPORTED). rot_dim: how many leading
+ * values of a head are rotated, a multiple of 16, 0 to head_dim; the others only take the
+ * norm. axes: 1 to 4; the first sections[0] pairs turn with the position on axis 0, the next
+ * sections[1] with axis 1, ... (their sum is rot_dim / 2; NULL for one axis). inv_freq: host
+ * array of rot_dim / 2 frequencies (radians a position), or NULL for theta's ladder. */
+pb_status pb_rope_init(int32_t head_dim, int32_t rot_dim, int32_t pairing, int32_t axes,
+                       const int32_t* sections, int32_t ladder, double theta,
+                       const double* inv_freq, pb_rope* out);
+
+/* The heads of every token, bf16: value d of head h at (b, s) is ptr[b batch_stride + s
+ * seq_stride + h head_stride + d]. Strides in elements, multiples of 8, >= 0; ptr 16-byte
+ * aligned. [B, S, heads, dh], [B, heads, S, dh] and the q or k columns of a [q | k | v] or
+ * of the scratch layout's [q | k] buffer are such views. */
+typedef struct pb_heads {
+  void* ptr;
+  int32_t heads;
+  int64_t batch_stride;
+  int64_t seq_stride;
+  int64_t head_stride;
+} pb_heads;
+
+/* q_out = R(norm(q)), k_out = R(norm(k)). Either may be left out (input and result NULL).
+ * gamma_q, gamma_k: [head_dim] bf16, or NULL for no norm. positions: int32 [axes, batch,
+ * seq], any value (negative ones turn backwards); NULL is position s of each sequence, for
+ * one axis. A result may be its own input (in place); otherwise results overlap neither
+ * inputs nor one another (PB_ERR_INVALID_ARG where the strides do not show that). batch or
+ * seq 0 does nothing; batch * seq < 2^31. */
+pb_status pb_qk_norm_rope(const pb_rope* rope, int32_t batch, int32_t seq, const pb_heads* q,
+                          const pb_heads* k, const void* gamma_q, const void* gamma_k, float eps,
+                          const int32_t* positions, const pb_heads* q_out,
+                          const pb_heads* k_out, void* stream);
+
+/* Backward: from the inputs q, k of the forward call (read only where there is a gamma, else
+ * they may be NULL) and the gradients dq, dk of its results, the gradients dq_out, dk_out of
+ * its inputs (bf16) and of gamma_q, gamma_k (fp32 [head_dim]; NULL skips one; accumulate != 0
+ * adds to what is there). A result may be its own dq (dk) or q (k). `scratch` (device,
+ * 256-byte aligned, >= pb_qk_norm_rope_scratch_bytes) is needed where there is a gamma and
+ * must not be used by another call that may run concurrently. Sums over tokens and heads are
+ * taken in a fixed order. batch or seq 0 gives zero sums. */
+pb_status pb_qk_norm_rope_scratch_bytes(size_t* bytes);
+pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t seq,
+                                   const pb_heads* q, const pb_heads* k, const void* gamma_q,
+                                   const void* gamma_k, float eps, const int32_t* positions,
+                                   const pb_heads* dq, const pb_heads* dk,
+                                   const pb_heads* dq_out, const pb_heads* dk_out,
+                                   float* dgamma_q, float* dgamma_k, int32_t accumulate,
+                                   void* scratch, size_t scratch_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * A linear layer outside the block (an embedding's or a head's projection, an adapter, a
+ * projection around pb_qk_norm_rope): bias, activation and residual in the product's epilogue,
+ * any number of tokens from one on, and its backward pass.
+ * ---------------------------------------------------------------------------------- */
+
+typedef enum pb_dtype { PB_DTYPE_BF16 = 0, PB_DTYPE_FP16 = 1, PB_DTYPE_FP32 = 2 } pb_dtype;
+
+/* w as [k, n] (the pages' Y = X W, as in pb_weights) or as [n, k]. */
+typedef enum pb_weight_layout { PB_WEIGHT_IN_OUT = 0, PB_WEIGHT_OUT_IN = 1 } pb_weight_layout;
+
+/* GELU: z Phi(z). GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. SILU: z / (1 +
+ * e^-z). RELU: max(z, 0), with derivative 0 at 0. */
+typedef enum pb_activation {
+  PB_ACT_NONE = 0,
+  PB_ACT_GELU = 1,
+  PB_ACT_GELU_TANH = 2,
+  PB_ACT_SILU = 3,
+  PB_ACT_RELU = 4
+} pb_activation;
+
+/* pre = x w + bias, y = activation(pre) + residual: x [m, k], w [k, n] or [n, k], bias [n],
+ * residual and y [m, n]. x, w, bias and pre have dtype (PB_DTYPE_BF16 or _FP16), residual and
+ * y either dtype or PB_DTYPE_FP32. Sums in fp32; pre (optional, for the backward pass) and y
+ * are each rounded once from the fp32 value. bias, residual and pre may be NULL. Any m >= 0
+ * (0 does nothing), n and k >= 1; ld*: row strides in elements, at least the row's length, a
+ * multiple of 8 (of 4 for an fp32 matrix); pointers 16-byte aligned. Bytes between the rows are
+ * neither used nor written. y may be the residual (same pointer, stride and type); no other
+ * overlap of y or pre. */
+typedef struct pb_linear_args {
+  int32_t m, n, k;
+  int32_t dtype;
+  int32_t w_layout;
+  int32_t activation;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  int32_t residual_dtype;
+  void* pre;
+  int64_t ldp;
+  void* y;
+  int64_t ldy;
+  int32_t y_dtype;
+} pb_linear_args;
+
+/* `scratch` (device, 256-byte aligned, >= pb_linear_scratch_bytes, or NULL) lets products be
+ * split along k where their tiles do not fill the GPU; with NULL every tile is computed whole.
+ * It needs no preparation. Calls that share one must not overlap on the GPU. `status` as in
+ * pb_gemm_bf16. */
+pb_status pb_linear_scratch_bytes(size_t* bytes);
+pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_bytes, int* status,
+                    void* stream);
+
+/* Backward of y = x w + bias for dy [m, n], the gradient of x w + bias: dx = dy w^T [m, k]
+ * (dtype), dw = x^T dy in w's layout (fp32), db [n] = the sum of dy's rows (fp32, in a fixed
+ * order); NULL skips one. Where x is activation(pre) of the layer before, give its pre [m, k]:
+ * dx is then the gradient of pre, dy w^T * activation'(pre), ready as that layer's dy.
+ * accumulate != 0 adds dw and db to what is there (dx is always overwritten); with m = 0 they
+ * are zero. The gradient of the residual is dy itself. ld*, pointers, scratch and status as
+ * in pb_linear; scratch is needed where db is wanted. Results overlap nothing else. */
+typedef struct pb_linear_grads {
+  int32_t m, n, k;
+  int32_t dtype;
+  int32_t w_layout;
+  int32_t activation; /* of pre; PB_ACT_NONE: pre is not read */
+  int32_t accumulate;
+  const void* dy;
+  int64_t lddy;
+  const void* x; /* read for dw */
+  int64_t ldx;
+  const void* w; /* read for dx */
+  int64_t ldw;
+  const void* pre;
+  int64_t ldp;
+  void* dx;
+  int64_t lddx;
+  float* dw;
+  int64_t lddw;
+  float* db;
+} pb_linear_grads;
+pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t scratch_bytes,
+                             int* status, void* stream);
+
+/* out = dy * activation'(pre), [rows, cols] of dtype (PB_DTYPE_BF16 or _FP16), for an
+ * activation whose result goes elsewhere than into a pb_linear. Row strides in elements,
+ * multiples of 8; pointers 16-byte aligned; out may be dy or pre (same stride). */
+pb_status pb_activation_backward(int64_t rows, int64_t cols, int32_t dtype, int32_t activation,
+                                 const void* dy, int64_t lddy, const void* pre, int64_t ldp,
+                                 void* out, int64_t ldo, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Optimiser: what follows pb_backward in a training step.
+ * ---------------------------------------------------------------------------------- */
+
+/* Values of a tensor that share a scale in an 8-bit state. */
+#define PB_ADAMW_BLOCK 256
+
+/* One tensor of n values (contiguous; n = 0 is skipped), device pointers, 16-byte aligned:
+ *   param       updated in place (pb_adamw_args.param_dtype)
+ *   param_copy  bf16 copy of an fp32 param, written with it (pb_weights' type), or NULL
+ *   grad        read (pb_adamw_args.grad_dtype)
+ *   m, v        states, zero before the first step. 32 bits: fp32 m and v. 8 bits: E4M3 codes
+ *               of m and of sqrt(v); value = code x scale of its PB_ADAMW_BLOCK values
+ *   m_scale, v_scale  8 bits: fp32 [ceil(n / PB_ADAMW_BLOCK)], zero before the first step;
+ *               32 bits: NULL */
+typedef struct pb_adamw_tensor {
+  int64_t n;
+  void* param;
+  void* param_copy;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float weight_decay;
+} pb_adamw_tensor;
+
+/* d_lr, d_step, d_grad_scale: device scalars read when the step runs, or NULL. d_lr and
+ * d_step stand in for lr and step (a captured graph is replayed with other values);
+ * every gradient is multiplied by *d_grad_scale, and where that is not finite the step
+ * changes nothing. */
+typedef struct pb_adamw_args {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  int64_t step; /* counts from 1 */
+  int32_t param_dtype; /* PB_DTYPE_FP32 or PB_DTYPE_BF16 */
+  int32_t grad_dtype;  /* PB_DTYPE_FP32 or PB_DTYPE_BF16 */
+  int32_t state_bits;  /* 32 or 8 */
+  const float* d_lr;
+  const int32_t* d_step;
+  const float* d_grad_scale;
+} pb_adamw_args;
+
+/* One AdamW step over all tensors (host array, read before the call returns):
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   param -= lr (weight_decay param + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
+ * in fp32, with m and v unrounded in the step that computes them. No buffer that is written
+ * may overlap another one (PB_ERR_INVALID_ARG: a tensor listed twice, too). */
+pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_tensor* tensors,
+                   void* stream);
+
+/* The 2-norm of all tensors' gradients together (n and grad of each are read): out (device
+ * fp32 [2]) = {norm, min(1, max_norm / (norm + 1e-6))}; the second is NaN where the norm is
+ * not finite, so that as d_grad_scale it clips the step, or leaves it out. Squares are taken
+ * in fp32 (gradients beyond 1e19 give an infinite norm), sums in a fixed order. `scratch`:
+ * device, 256-byte aligned, >= pb_grad_norm_scratch_bytes, not shared with a call that may
+ * run concurrently. */
+pb_status pb_grad_norm_scratch_bytes(int32_t n_tensors, size_t* bytes);
+pb_status pb_grad_norm(int32_t n_tensors, const pb_adamw_tensor* tensors, int32_t grad_dtype,
+                       float max_norm, float* out, void* scratch, size_t scratch_bytes,
+                       void* stream);
+
 /* Failure-detection self-test: one thread waits, with the kernels' bounded-wait
  * routine, on an mbarrier that nothing arrives at. After `limit_ns` it records
  * PB_ERR_DEVICE_TIMEOUT in *status (a device int) and the kernel returns; no copy, MMA

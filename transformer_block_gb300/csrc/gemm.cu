@@ -507,6 +507,239 @@ __device__ __forceinline__ void epilogue32(const EpiParams& ep, int row, int col
   }
 }
 
+// ---------------------------------------------------------------- kEpiLinear
+// Beyond |z| = kActFar every activation and derivative here equals its limit in fp32 (GeLU's
+// tails end at 13, the tanh form's at 9; SiLU's is 1e-33 there): z is held at that bound, so
+// an infinite z meets no infinity times zero. NaN stays NaN.
+constexpr float kActFar = 80.f;
+__device__ __forceinline__ float act_held(float z) {
+  return fabsf(z) > kActFar ? copysignf(kActFar, z) : z;
+}
+// 1 / (1 + exp(-z)) from the approximate exponential and reciprocal (2^-22 relative).
+__device__ __forceinline__ float sigmoid_approx(float z) {
+  return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * z));
+}
+// GeLU's tanh form is z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
+constexpr float kTanh2C = 1.5957691216057308f, kTanhA = 0.044715f;
+
+__device__ __forceinline__ void act_apply(int act, float (&v)[32]) {
+  if (act == kActNone) return;
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float a = act_held(v[i]), b = act_held(v[i + 1]);
+      gelu_pair(a, b);
+      v[i] = v[i] > kActFar ? v[i] : a;
+      v[i + 1] = v[i + 1] > kActFar ? v[i + 1] : b;
+    }
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float z = act_held(v[i]);
+      const float a = z * sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
+      v[i] = v[i] > kActFar ? v[i] : a;
+    }
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float z = act_held(v[i]);
+      const float a = z * sigmoid_approx(z);
+      v[i] = v[i] > kActFar ? v[i] : a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+  }
+}
+
+// d *= act'(z)
+__device__ __forceinline__ void act_grad_apply(int act, float (&d)[32], const float (&zs)[32]) {
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      gelu_grad_pair(d[i], d[i + 1], act_held(zs[i]), act_held(zs[i + 1]));
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float z = act_held(zs[i]);
+      const float s = sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
+      d[i] *= s + z * s * (1.f - s) * kTanh2C * (1.f + 3.f * kTanhA * z * z);
+    }
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float z = act_held(zs[i]), s = sigmoid_approx(z);
+      d[i] *= s * (1.f + z * (1.f - s));
+    }
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) d[i] = zs[i] > 0.f ? d[i] : zs[i] <= 0.f ? 0.f : zs[i];
+  }
+}
+
+// 32 values of 16 bits from src (64 bytes, 16-byte aligned) or the first n of them.
+template <bool F16>
+__device__ __forceinline__ void load_row16(const void* src, int n, float (&v)[32]) {
+  const uint16_t* s = static_cast<const uint16_t*>(src);
+  uint32_t w[16];
+  if (n >= 32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 u = reinterpret_cast<const uint4*>(s)[q];
+      w[4 * q] = u.x;
+      w[4 * q + 1] = u.y;
+      w[4 * q + 2] = u.z;
+      w[4 * q + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = (2 * i < n ? uint32_t(s[2 * i]) : 0u) |
+             (2 * i + 1 < n ? uint32_t(s[2 * i + 1]) << 16 : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// fp32 result of a warp's 32 x 32 chunk: through shared memory, so that a store instruction
+// writes whole 128-byte rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q
+// of row r sits at piece q ^ (r & 7), so neither the rows' writes nor the reads meet a bank
+// twice.
+__device__ __forceinline__ void linear_store_f32(const EpiParams& ep, int row0, int col0,
+                                                 const float (&v)[32], uint32_t stage) {
+  const int lane = int(threadIdx.x & 31);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     stage + uint32_t(lane * 128 + ((q ^ (lane & 7)) << 4))),
+                 "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                 : "memory");
+  __syncwarp();
+  const int cq = (lane & 7) * 4;
+  const int n = ep.N - (col0 + cq);  // columns left from this lane's first on
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int r = 4 * it + (lane >> 3);
+    if (row0 + r < ep.M && n > 0) {
+      float sr[4];
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(sr[0]), "=f"(sr[1]), "=f"(sr[2]), "=f"(sr[3])
+                   : "r"(stage + uint32_t(r * 128 + (((lane & 7) ^ (r & 7)) << 4)))
+                   : "memory");
+      float* dst = ep.lin.y32 + int64_t(row0 + r) * ep.lin.ldy + col0 + cq;
+      if (n >= 4) {
+        float4 o = make_float4(sr[0], sr[1], sr[2], sr[3]);
+        if (ep.lin.accumulate) {
+          const float4 a = *reinterpret_cast<const float4*>(dst);
+          o.x += a.x;
+          o.y += a.y;
+          o.z += a.z;
+          o.w += a.w;
+        }
+        *reinterpret_cast<float4*>(dst) = o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < n) dst[e] = ep.lin.accumulate ? dst[e] + sr[e] : sr[e];
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// 16-bit result of a warp's 32 rows x 32 columns, n of them inside the matrix. A TMA store
+// cuts a box off at the last column only to 16 bytes: where the columns end inside those, the
+// last chunk is stored by its lanes.
+template <bool F16>
+__device__ __forceinline__ void linear_store16(StoreStage& ss, const CUtensorMap* tm, void* dst,
+                                               int64_t ld, int row0, int col0, int M, int n,
+                                               const float (&v)[32]) {
+  uint32_t w[16];
+  pack_words16<F16>(v, w);
+  if (n >= 32 || n % 8 == 0) {
+    tma_store_rows32(ss, tm, row0, col0, M, w);
+    return;
+  }
+  const int row = row0 + int(threadIdx.x & 31);
+  if (row < M) {
+    uint16_t* d = static_cast<uint16_t*>(dst) + int64_t(row) * ld + col0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) d[i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
+  }
+}
+
+// Warp-wide, lane l holding row `row` = the warp's first row + l of columns [col0, col0 + 32).
+template <bool F16>
+__device__ __forceinline__ void linear_epilogue32(const EpiParams& ep, int row, int col0,
+                                                  float (&v)[32], StoreStage& ss) {
+  const LinearEpi& e = ep.lin;
+  const int row0 = row - int(threadIdx.x & 31);
+  if (row0 >= ep.M) return;
+  const bool live = row < ep.M;
+  const int n = ep.N - col0;
+  if (e.bias != nullptr) {
+    float b[32];
+    load_row16<F16>(static_cast<const uint16_t*>(e.bias) + col0, n, b);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += b[i];
+  }
+  if (e.pre != nullptr)
+    linear_store16<F16>(ss, &ep.tm_out1, e.pre, e.ld_pre, row0, col0, ep.M, n, v);
+  if (e.mul != nullptr) {
+    if (live) {
+      float z[32];
+      load_row16<F16>(static_cast<const uint16_t*>(e.mul) + int64_t(row) * e.ld_mul + col0, n, z);
+      act_grad_apply(e.act, v, z);
+    }
+  } else {
+    act_apply(e.act, v);
+  }
+  if (e.resid != nullptr && live) {
+    if (e.resid_f32) {
+      const float* r = static_cast<const float*>(e.resid) + int64_t(row) * e.ld_resid + col0;
+      if (n >= 32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 f = reinterpret_cast<const float4*>(r)[q];
+          v[4 * q] += f.x;
+          v[4 * q + 1] += f.y;
+          v[4 * q + 2] += f.z;
+          v[4 * q + 3] += f.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < n) v[i] += r[i];
+      }
+    } else {
+      float r[32];
+      load_row16<F16>(static_cast<const uint16_t*>(e.resid) + int64_t(row) * e.ld_resid + col0, n,
+                      r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += r[i];
+    }
+  }
+  if (e.y32 != nullptr) {
+    if (ss.n > 0) {  // the pre-activation's TMA store reads the same shared memory
+      if ((threadIdx.x & 31) == 0) bulk_wait_read();
+      __syncwarp();
+    }
+    linear_store_f32(ep, row0, col0, v, ss.base);
+  } else {
+    linear_store16<F16>(ss, &ep.tm_out0, e.y16, e.ldy, row0, col0, ep.M, n, v);
+  }
+}
+
 // Destination of columns [col0 + cq, col0 + cq + 4) of gradient row `row` (kEpiGrad).
 __device__ __forceinline__ float* grad_dst(const EpiParams& ep, int row, int col0, int cq) {
   if (row >= ep.split_row) return ep.g1 + int64_t(row - ep.split_row) * ep.ld1 + col0 + cq;
@@ -564,9 +797,10 @@ struct Sched {
 
 struct SkParams {
   int dp_tiles, sk_tiles, W;
-  float* partials;  // [kSkMaxClusters][2][128][256]
-  uint64_t* flags;  // [kSkMaxClusters][2][4]
+  float* partials;  // [kSkMaxClusters][2][128][256]; kEpiLinear: [.. clusters][2 slots] of it
+  uint64_t* flags;  // [kSkMaxClusters][2][4]; kEpiLinear: a tile's counters [tiles][2][4]
   uint64_t epoch;
+  int seg;          // kEpiLinear, one M tile: k-blocks summed at a time in one accumulator
 };
 
 struct Unit {
@@ -625,6 +859,25 @@ __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
 }
 __device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
   asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
+// One of n arrivals at a counter word of a launch: whether it is the last one, which leaves
+// the word at zero. Whatever another launch left in the word does not count: the upper 48
+// bits are the launch's epoch. Nobody waits; an exchange fails only where another succeeded.
+__device__ __forceinline__ bool arrive_is_last(uint64_t* word, uint64_t epoch, int n) {
+  auto* w = reinterpret_cast<unsigned long long*>(word);
+  const unsigned long long mine = (static_cast<unsigned long long>(epoch) << 16);
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
+  for (;;) {
+    const unsigned long long count = (old & ~0xffffull) == mine ? (old & 0xffffull) : 0ull;
+    const unsigned long long seen = atomicCAS(w, old, mine | (count + 1));
+    if (seen == old) {
+      const bool last = int(count) + 1 == n;
+      if (last) *reinterpret_cast<volatile unsigned long long*>(w) = 0ull;
+      return last;
+    }
+    old = seen;
+  }
 }
 
 template <int KIND, int OP, int LAYOUT, int MT>
@@ -773,7 +1026,47 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       UnitIter ui(sc);
       Unit u;
+      uint32_t uses = 0;  // kEpiLinear: parity of each accumulator's uses so far
       while (ok && ui.next(sc, u)) {
+        if (KIND == kEpiLinear && MT == 1) {
+          // The unit's first sk.seg k-blocks go to accumulator acc, each further segment to
+          // the other one, from which the epilogue warps add it to the first; the next unit
+          // starts in the other one.
+          for (int ks = u.kb0; ok && ks < u.kb1; ks += sk.seg) {
+            const int a = ks == u.kb0 ? acc : acc ^ 1;
+            const int ke = min(u.kb1, ks + sk.seg);
+            if (!mbar_wait(tempty0 + 8 * a, ((uses >> a) & 1u) ^ 1u, wc, 2)) {
+              ok = false;
+              break;
+            }
+            uses ^= 1u << a;
+            tc_fence_after();
+            for (int kb = ks; kb < ke; ++kb) {
+              if (!mbar_wait(full0 + 8 * stage, phase, wc, 3)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(smem + size_t(stage) * STAGE_BYTES);
+              const uint64_t da =
+                  AMN ? sdesc_mnmajor_sw128(sa, A_BYTES / 2) : sdesc_kmajor_sw128(sa);
+              const uint64_t db = BMN ? sdesc_mnmajor_sw128(sa + A_BYTES, B_BYTES / 2)
+                                      : sdesc_kmajor_sw128(sa + A_BYTES);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f16kind_ss_pair(tmem_base + uint32_t(a * BN), da + kStepA * k,
+                                    db + kStepB * k, idesc, (kb > ks) || k > 0);
+              mma_commit_pair(empty0 + 8 * stage, 0x3);
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            if (ok) mma_commit_pair(tfull0 + 8 * a, 0x3);
+          }
+          acc ^= 1;
+          continue;
+        }
         if (!mbar_wait(tempty0 + 8 * acc, acc_par ^ 1, wc, 2)) break;
         tc_fence_after();
         // MT = 1: accumulator acc of two; MT = 2: M tile g in columns [g * BN, (g + 1) * BN)
@@ -837,7 +1130,133 @@ __global__ void __launch_bounds__(THREADS, 1)
     UnitIter ui(sc);
     Unit u;
     bool ok = true;
+    uint32_t uses = 0;  // kEpiLinear, MT = 1: parity of each accumulator's uses so far
+    const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
+    auto release = [&](int a) {  // warp-wide: accumulator a may be written again
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(tempty0 + 8 * a);
+        else
+          mbar_arrive_remote(mapa_shared(tempty0 + 8 * a, 0));
+      }
+    };
     while (ok && ui.next(sc, u)) {
+      if (KIND == kEpiLinear) {
+        if (!mbar_wait_warp(tfull0 + 8 * acc, MT == 1 ? (uses >> acc) & 1u : acc_par, wc, 4)) break;
+        uses ^= 1u << acc;
+        tc_fence_after();
+        const int n0 = u.tn * BN;
+        if (MT == 1) {
+          for (int ks = u.kb0 + sk.seg; ks < u.kb1; ks += sk.seg) {
+            const int a = acc ^ 1;
+            if (!mbar_wait_warp(tfull0 + 8 * a, (uses >> a) & 1u, wc, 4)) {
+              ok = false;
+              break;
+            }
+            uses ^= 1u << a;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              if (n0 + c * 32 >= ep.N) break;
+              uint32_t r[32], t[32];
+              tmem_ld32(lane_base + uint32_t(a * BN + c * 32), t);
+              tmem_ld32(lane_base + uint32_t(acc * BN + c * 32), r);
+              tmem_ld_wait(r);
+              tmem_ld_wait_regs(t);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(t[i]));
+              tmem_st32(lane_base + uint32_t(acc * BN + c * 32), r);
+            }
+            tmem_st_wait();
+            release(a);
+          }
+          if (!ok) break;
+        }
+        for (int g = 0; g < u.mt; ++g) {
+          const int row = u.row0 + g * PM + int(rank) * BM + int(quad * 32 + lane);
+          const uint32_t taddr = lane_base + uint32_t((MT == 2 ? g : acc) * BN);
+          const size_t part_off = (size_t(rank) * 128 + quad * 32 + lane) * BN;
+          // the pairs that hold part of this tile: first (its last share) to last
+          int first = sc.cluster, last = sc.cluster;
+          bool mine = true;
+          if (u.ts >= 0 && (u.kb0 > 0 || u.kb1 < sc.num_kb)) {
+            const int64_t it0 = int64_t(u.ts) * sc.num_kb;
+            first = int(it0 / sc.W);
+            last = int((it0 + sc.num_kb - 1) / sc.W);
+            float* dst = sk.partials +
+                         (size_t(sc.cluster) * 2 + (sc.cluster == first ? 1 : 0)) * (2 * 128 * BN) +
+                         part_off;
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              if (n0 + c * 32 >= ep.N) break;
+              __syncwarp();
+              uint32_t r[32];
+              tmem_ld32(taddr + uint32_t(c * 32), r);
+              tmem_ld_wait(r);
+              if (row < ep.M) {
+                float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  __stcg(d4 + q,
+                         make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                     __uint_as_float(r[4 * q + 2]),
+                                     __uint_as_float(r[4 * q + 3])));
+              }
+            }
+            __threadfence();
+            __syncwarp();
+            int is_last = 0;
+            if (lane == 0)
+              is_last = arrive_is_last(sk.flags + (size_t(u.ts) * 2 + rank) * 4 + quad, sk.epoch,
+                                       last - first + 1);
+            mine = __shfl_sync(0xffffffffu, is_last, 0) != 0;
+            __threadfence();
+          }
+          if (!mine) continue;
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            const int col0 = n0 + c * 32;
+            if (col0 >= ep.N) break;
+            __syncwarp();
+            float v[32];
+            if (first == last) {
+              uint32_t r[32];
+              tmem_ld32(taddr + uint32_t(c * 32), r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              for (int c2 = first; c2 <= last; ++c2) {
+                const float4* p4 = reinterpret_cast<const float4*>(
+                    sk.partials + (size_t(c2) * 2 + (c2 == first ? 1 : 0)) * (2 * 128 * BN) +
+                    part_off + c * 32);
+                if (row < ep.M) {
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) {
+                    const float4 pv = __ldcg(p4 + q);
+                    v[4 * q] += pv.x;
+                    v[4 * q + 1] += pv.y;
+                    v[4 * q + 2] += pv.z;
+                    v[4 * q + 3] += pv.w;
+                  }
+                }
+              }
+            }
+            linear_epilogue32<OP == kOpF16>(ep, row, col0, v, ss);
+          }
+        }
+        release(acc);
+        if (MT == 1)
+          acc ^= 1;
+        else
+          acc_par ^= 1;
+        continue;
+      }
       if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
       tc_fence_after();
       for (int g = 0; g < u.mt; ++g) {  // MT = 2: the unit's two M tiles, one after the other
@@ -969,6 +1388,14 @@ uint64_t next_epoch() {
   return e == 0 ? ++counter : e;
 }
 
+// kEpiLinear: k-blocks (of 64) that one accumulator sums where the result is fp32, before the
+// sum goes on in fp32 additions that round to nearest. The tensor core cuts its sums off
+// instead of rounding them, which leaves 1.0e-6 of relative error at K = 1024 and, growing
+// with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6 of a chain of fp32 fused multiply-adds.
+// A 16-bit result rounds at 2^-9 and needs none of that.
+constexpr int kLinearSegment = 16;
+// kEpiLinear: k-blocks that a share of a split tile has at least.
+constexpr int kLinearMinBlocks = 4;
 // Stream-K tiles of a two-M-tile launch: at most this many pairs share one tile along K.
 constexpr int kSkMaxSplit = 16;
 
@@ -1010,7 +1437,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   if (attr_err != cudaSuccess) return attr_err;
   if (max_clusters <= 0) return cudaErrorLaunchOutOfResources;
   const int units = ((M + MT * PM - 1) / (MT * PM)) * ((N + BN - 1) / BN);
-  const int clusters = units < max_clusters ? units : max_clusters;
+  int clusters = units < max_clusters ? units : max_clusters;
   const int bke = OP == kOpE4m3 ? kGemmBK8 : BK;
   const int num_kb = (K + bke - 1) / bke;
   // Stream-K for the last waves when they would leave pairs idle. MT = 1: every full wave
@@ -1038,6 +1465,25 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
     sk.flags = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(sk_scratch) +
                                            size_t(kSkMaxClusters) * kSkPartialBytes);
     sk.epoch = next_epoch();
+  }
+  if (KIND == kEpiLinear) {
+    // Fewer tiles than pairs: all of them are split along K, over as many pairs as have at
+    // least kLinearMinBlocks k-blocks each.
+    if (sk_scratch != nullptr && MT == 1 && units < max_clusters && max_clusters <= kSkMaxClusters) {
+      const int64_t iters = int64_t(units) * num_kb;
+      int64_t w = (iters + max_clusters - 1) / max_clusters;
+      if (w < kLinearMinBlocks) w = kLinearMinBlocks;
+      if (w < num_kb) {
+        sk.W = int(w);
+        sk.sk_tiles = units;
+        sk.dp_tiles = 0;
+        clusters = int((iters + w - 1) / w);
+      }
+    }
+    sk.partials = static_cast<float*>(sk_scratch);
+    sk.flags = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(sk_scratch) + kLinearPartialBytes);
+    if (sk.sk_tiles > 0) sk.epoch = next_epoch();
+    sk.seg = ep.lin.y32 != nullptr ? kLinearSegment : num_kb;
   }
   EpiParams e = ep;
   e.M = M;
@@ -1109,6 +1555,39 @@ cudaError_t launch_gemm(EpiKind kind, OpType op, const CUtensorMap& tmA, const C
   }
 #undef PB_GEMM_CASE
 #undef PB_GEMM_OP
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& tmA,
+                               const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
+                               int* status, uint64_t limit_ns, void* scratch,
+                               cudaStream_t stream) {
+  if (M <= 0 || N <= 0 || K <= 0) return cudaSuccess;
+  // two M tiles a unit: where the units still fill the pairs (see two_m_tiles), and not for
+  // fp32 results, whose segments need both accumulators for one tile
+  const int64_t units2 = int64_t((M + 2 * PM - 1) / (2 * PM)) * ((N + BN - 1) / BN);
+  const bool two = layout == kKK && two_m_tiles(M, K) && ep.lin.y32 == nullptr &&
+                   units2 >= kSkMaxClusters;
+#define PB_GEMM_LINEAR(OP_)                                                                     \
+  switch (layout) {                                                                             \
+    case kKK:                                                                                   \
+      if (two)                                                                                  \
+        return launch_kind<kEpiLinear, OP_, kKK, 2>(tmA, tmB, M, N, K, ep, 0, status, limit_ns, \
+                                                    scratch, stream);                           \
+      return launch_kind<kEpiLinear, OP_, kKK>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
+                                               scratch, stream);                                \
+    case kKM:                                                                                   \
+      return launch_kind<kEpiLinear, OP_, kKM>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
+                                               scratch, stream);                                \
+    case kMM:                                                                                   \
+      return launch_kind<kEpiLinear, OP_, kMM>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
+                                               scratch, stream);                                \
+    default:                                                                                    \
+      return cudaErrorInvalidValue;                                                             \
+  }
+  if (op == kOpF16) PB_GEMM_LINEAR(kOpF16);
+  if (op == kOpBf16) PB_GEMM_LINEAR(kOpBf16);
+#undef PB_GEMM_LINEAR
   return cudaErrorInvalidValue;
 }
 

@@ -63,6 +63,29 @@ enum EpiKind : int {
   kEpiResidual = 2,  // y = bf16(D + bias + x)
   kEpiBwdAct = 3,    // D = dy [Wo ; W2]^T: d_attn (bf16), and dh = D * act'(h) into dz
   kEpiGrad = 4,      // fp32 gradient store (or accumulate), split by rows or columns
+  kEpiLinear = 5,    // y = resid + act(D + bias), or D * act'(mul): any M, N and K
+};
+
+// Activations of kEpiLinear (== pb_activation).
+enum Act : int { kActNone = 0, kActGelu = 1, kActGeluTanh = 2, kActSilu = 3, kActRelu = 4 };
+
+// kEpiLinear. 16-bit tensors have the operands' type. Row strides in elements, 16-byte rows
+// (any N: the last columns are handled one by one). The GEMM's y16 and pre leave by TMA stores
+// through tm_out0 and tm_out1.
+struct LinearEpi {
+  int act;
+  const void* bias;   // [N] 16-bit, or null
+  const void* mul;    // backward: D is multiplied by act'(mul), 16-bit [M, N], or null
+  int64_t ld_mul;
+  const void* resid;  // 16-bit or fp32 [M, N], or null
+  int64_t ld_resid;
+  bool resid_f32;
+  void* pre;          // D + bias is also stored here (16-bit), or null
+  int64_t ld_pre;
+  void* y16;          // 16-bit result, or
+  float* y32;         // fp32 result
+  int64_t ldy;
+  bool accumulate;    // y32 is added to
 };
 
 // Operand layouts: bit 0 set = A is MN-major (stored [K, M], M contiguous), bit 1 = B is
@@ -126,6 +149,7 @@ struct EpiParams {
   int64_t ld0, ld1;
   int split_row, split_col;
   bool accumulate;
+  LinearEpi lin;  // kEpiLinear
 };
 
 // Stream-K work space: the tiles of the last waves are split along K across all CTA
@@ -136,6 +160,15 @@ constexpr int kSkMaxClusters = 96;
 constexpr size_t kSkPartialBytes = size_t(2) * 128 * 256 * 4;  // one pair tile, fp32
 constexpr size_t kSkFlagBytes = size_t(2) * 4 * 8;             // 2 CTAs x 4 warps x u64
 constexpr size_t kSkScratchBytes = size_t(kSkMaxClusters) * (kSkPartialBytes + kSkFlagBytes);
+
+// kEpiLinear's work space. Here no pair waits for another one: every pair that computed part
+// of a tile along K leaves its partial sums, and whichever arrives last adds them up in the
+// pairs' order and finishes the tile. A pair's share of the iterations has two partial tiles
+// at most (its first and its last). A tile's counter words hold the launch's epoch and the
+// arrivals, and the last to arrive clears its word, so the words need no preparation.
+constexpr size_t kLinearPartialBytes = size_t(kSkMaxClusters) * 2 * kSkPartialBytes;
+constexpr size_t kLinearCounterBytes = size_t(kSkMaxClusters) * 2 * 8 * 8;  // 8 warps a tile
+constexpr size_t kLinearScratchBytes = kLinearPartialBytes + kLinearCounterBytes;
 
 size_t gemm_smem_bytes();
 // op: the type of A and B (K % 64 == 0, K % 128 == 0 for kOpE4m3). sk_scratch
@@ -151,6 +184,34 @@ cudaError_t launch_gemm_layout(EpiKind kind, GemmLayout layout, const CUtensorMa
                                const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
                                int num_sms, int* status, uint64_t limit_ns, void* sk_scratch,
                                cudaStream_t stream);
+
+// kEpiLinear with bf16 or fp16 operands (kKK, kKM or kMM; any M, N, K). scratch:
+// kLinearScratchBytes, 256-byte aligned, or null: every tile is computed whole.
+cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& tmA,
+                               const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
+                               int* status, uint64_t limit_ns, void* scratch,
+                               cudaStream_t stream);
+
+// ---------------------------------------------------------------- linear (linear.cu)
+// Few rows of A: y as kEpiLinear's, D = A * B^T with B [N, K] (ldb) or, b_mn, stored [K, N].
+constexpr int kFewRows = 32;
+struct FewParams {
+  int M, N, K;
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;
+  LinearEpi epi;
+};
+cudaError_t launch_linear_few(OpType op, bool b_mn, const FewParams& p, cudaStream_t stream);
+// out = dy * act'(pre), rows of cols 16-bit values.
+cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,
+                                int64_t ld_dy, const void* pre, int64_t ld_pre, void* out,
+                                int64_t ld_out, cudaStream_t stream);
+// out[c] (+)= sum over rows of m[r, c] (16-bit values, 16-byte rows, any cols), through
+// partials [kSumBlocks][cols] fp32, in a fixed order.
+constexpr int kSumBlocks = 64;
+cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols, int64_t ld,
+                            float* partials, float* out, bool accumulate, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention (swa.cu)
 struct SwaParams {

@@ -796,6 +796,57 @@ pb_status check_stack(pb_handle* const* layers, int32_t n_layers, const void* sc
   return PB_OK;
 }
 
+// A row-major matrix argument: its bytes from the first to the last value.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld, esz;
+  size_t bytes() const { return size_t(((rows - 1) * ld + cols) * esz); }
+};
+
+pb_status check_matrix(const Matrix& m, const char* name) {
+  if (m.p == nullptr || !aligned(m.p, 16))
+    return fail(PB_ERR_INVALID_ARG, "%s must be a 16-byte aligned device pointer", name);
+  if (m.ld < m.cols || m.ld % (16 / m.esz) != 0)
+    return fail(PB_ERR_INVALID_ARG, "%s: the row stride must be >= %lld and a multiple of %lld",
+                name, (long long)m.cols, (long long)(16 / m.esz));
+  if (m.ld > (int64_t(1) << 34))  // a tensor map's stride has 40 bits
+    return fail(PB_ERR_UNSUPPORTED, "%s: the row stride is beyond 2^34", name);
+  return PB_OK;
+}
+
+pb_status check_apart(const Matrix& out, const char* name, const Matrix& other) {
+  if (other.p != nullptr && overlap(out.p, out.bytes(), other.p, other.bytes()))
+    return fail(PB_ERR_INVALID_ARG, "%s overlaps another argument", name);
+  return PB_OK;
+}
+
+pb_status check_linear_sizes(int32_t m, int32_t n, int32_t k, int32_t dtype, int32_t layout,
+                             int32_t act) {
+  if (m < 0 || n < 1 || k < 1) return fail(PB_ERR_INVALID_ARG, "need m >= 0, n >= 1, k >= 1");
+  if (dtype != PB_DTYPE_BF16 && dtype != PB_DTYPE_FP16)
+    return fail(PB_ERR_UNSUPPORTED, "dtype must be PB_DTYPE_BF16 or PB_DTYPE_FP16");
+  if (layout != PB_WEIGHT_IN_OUT && layout != PB_WEIGHT_OUT_IN)
+    return fail(PB_ERR_INVALID_ARG, "w_layout %d is not a pb_weight_layout", layout);
+  if (act < PB_ACT_NONE || act > PB_ACT_RELU)
+    return fail(PB_ERR_INVALID_ARG, "activation %d is not a pb_activation", act);
+  // the GEMM counts its 256 x 256 tiles in 32 bits
+  const int64_t big = (int64_t(1) << 30) * 65536;
+  if (int64_t(m) * n > big || int64_t(m) * k > big || int64_t(n) * k > big)
+    return fail(PB_ERR_UNSUPPORTED, "a matrix has more than 2^46 values");
+  return PB_OK;
+}
+
+pb_status check_linear_scratch(const void* scratch, size_t bytes) {
+  if (scratch != nullptr && (!aligned(scratch, 256) || bytes < pb::kLinearScratchBytes))
+    return fail(PB_ERR_WORKSPACE, "scratch must be NULL or 256-byte aligned with >= %zu bytes",
+                pb::kLinearScratchBytes);
+  return PB_OK;
+}
+
+// Columns whose row sums are taken at once: their partial sums fit the partial tiles' region.
+constexpr int64_t kSumCols = 131072;
+static_assert(size_t(kSumCols) * pb::kSumBlocks * 4 <= pb::kLinearPartialBytes, "row sums");
+
 // Layer 0 reads bf16 x, the last layer writes y (bf16, or fp32 when y_f32); in between
 // the residual stream alternates between the fp32 buffers res0 and res1.
 pb_status run_stack(pb_handle* const* layers, int32_t n, const void* x, void* y,
@@ -1414,6 +1465,215 @@ pb_status pb_gemm_bf16_layout(int32_t M, int32_t N, int32_t K, const void* A, in
   PB_CUDA(pb::launch_gemm_layout(pb::kEpiStore, layout, ta, tb, M, N, K, ep, sms, status,
                                  kDefaultLimitNs, scratch, static_cast<cudaStream_t>(stream)),
           "gemm launch");
+  return PB_OK;
+}
+
+pb_status pb_linear_scratch_bytes(size_t* bytes) {
+  if (bytes == nullptr) return fail(PB_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = pb::kLinearScratchBytes;
+  return PB_OK;
+}
+
+pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_bytes, int* status,
+                    void* stream) {
+  if (args == nullptr) return fail(PB_ERR_INVALID_ARG, "args is NULL");
+  const pb_linear_args& a = *args;
+  pb_status s = check_linear_sizes(a.m, a.n, a.k, a.dtype, a.w_layout, a.activation);
+  if (s == PB_OK) s = check_linear_scratch(scratch, scratch_bytes);
+  if (s != PB_OK) return s;
+  if (a.y_dtype != a.dtype && a.y_dtype != PB_DTYPE_FP32)
+    return fail(PB_ERR_UNSUPPORTED, "y_dtype must be dtype or PB_DTYPE_FP32");
+  if (a.residual != nullptr && a.residual_dtype != a.dtype && a.residual_dtype != PB_DTYPE_FP32)
+    return fail(PB_ERR_UNSUPPORTED, "residual_dtype must be dtype or PB_DTYPE_FP32");
+  if (a.m == 0) return PB_OK;
+  const bool in_out = a.w_layout == PB_WEIGHT_IN_OUT;
+  const Matrix x{a.x, a.m, a.k, a.ldx, 2};
+  const Matrix w{a.w, in_out ? a.k : a.n, in_out ? a.n : a.k, a.ldw, 2};
+  const Matrix y{a.y, a.m, a.n, a.ldy, a.y_dtype == PB_DTYPE_FP32 ? 4 : 2};
+  const Matrix r{a.residual, a.m, a.n, a.ldr, a.residual_dtype == PB_DTYPE_FP32 ? 4 : 2};
+  const Matrix pre{a.pre, a.m, a.n, a.ldp, 2};
+  const Matrix bias{a.bias, 1, a.n, a.n, 2};
+  const Matrix work{scratch, 1, int64_t(pb::kLinearScratchBytes), 0, 1};
+  s = check_matrix(x, "x");
+  if (s == PB_OK) s = check_matrix(w, "w");
+  if (s == PB_OK) s = check_matrix(y, "y");
+  if (s == PB_OK && r.p != nullptr) s = check_matrix(r, "residual");
+  if (s == PB_OK && pre.p != nullptr) s = check_matrix(pre, "pre");
+  if (s != PB_OK) return s;
+  if (!aligned(a.bias, 16)) return fail(PB_ERR_INVALID_ARG, "bias must be 16-byte aligned");
+  const bool in_place = r.p == y.p && r.ld == y.ld && r.esz == y.esz;
+  const Matrix* others[5] = {&x, &w, &bias, &pre, &work};
+  for (const Matrix* o : others) {
+    s = check_apart(y, "y", *o);
+    if (s != PB_OK) return s;
+    if (pre.p != nullptr && o != &pre) s = check_apart(pre, "pre", *o);
+    if (s != PB_OK) return s;
+  }
+  if (!in_place) s = check_apart(y, "y", r);
+  if (s == PB_OK && pre.p != nullptr) s = check_apart(pre, "pre", r);
+  if (s != PB_OK) return s;
+
+  const pb::OpType op = a.dtype == PB_DTYPE_FP16 ? pb::kOpF16 : pb::kOpBf16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  EpiParams ep{};
+  ep.lin.act = a.activation;
+  ep.lin.bias = a.bias;
+  ep.lin.resid = a.residual;
+  ep.lin.ld_resid = a.ldr;
+  ep.lin.resid_f32 = r.esz == 4;
+  ep.lin.pre = a.pre;
+  ep.lin.ld_pre = a.ldp;
+  if (y.esz == 4)
+    ep.lin.y32 = static_cast<float*>(a.y);
+  else
+    ep.lin.y16 = a.y;
+  ep.lin.ldy = a.ldy;
+  if (a.m <= pb::kFewRows) {
+    pb::FewParams f{a.m, a.n, a.k, a.x, a.w, a.ldx, a.ldw, ep.lin};
+    PB_CUDA(pb::launch_linear_few(op, in_out, f, st), "linear launch");
+    return PB_OK;
+  }
+  CUtensorMap tx, tw;
+  s = make_map_2d(&tx, a.x, x.rows, x.cols, x.ld, pb::kGemmBoxRows, op);
+  if (s == PB_OK)
+    s = make_map_2d(&tw, a.w, w.rows, w.cols, w.ld, in_out ? 64 : pb::kGemmBoxRows, op);
+  if (s == PB_OK && y.esz == 2)
+    s = make_store_map(&ep.tm_out0, a.y, y.rows, y.cols, y.ld, op == pb::kOpF16);
+  if (s == PB_OK && a.pre != nullptr)
+    s = make_store_map(&ep.tm_out1, a.pre, pre.rows, pre.cols, pre.ld, op == pb::kOpF16);
+  if (s != PB_OK) return s;
+  PB_CUDA(pb::launch_gemm_linear(op, in_out ? pb::kKM : pb::kKK, tx, tw, a.m, a.n, a.k, ep,
+                                 status, kDefaultLimitNs, scratch, st),
+          "linear launch");
+  return PB_OK;
+}
+
+pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t scratch_bytes,
+                             int* status, void* stream) {
+  if (args == nullptr) return fail(PB_ERR_INVALID_ARG, "args is NULL");
+  const pb_linear_grads& a = *args;
+  pb_status s = check_linear_sizes(a.m, a.n, a.k, a.dtype, a.w_layout, a.activation);
+  if (s == PB_OK) s = check_linear_scratch(scratch, scratch_bytes);
+  if (s != PB_OK) return s;
+  const bool in_out = a.w_layout == PB_WEIGHT_IN_OUT;
+  const bool mul = a.activation != PB_ACT_NONE && a.dx != nullptr;
+  const int64_t wr = in_out ? a.k : a.n, wc = in_out ? a.n : a.k;
+  const Matrix dy{a.dy, a.m, a.n, a.lddy, 2};
+  const Matrix x{a.dw != nullptr ? a.x : nullptr, a.m, a.k, a.ldx, 2};
+  const Matrix w{a.dx != nullptr ? a.w : nullptr, wr, wc, a.ldw, 2};
+  const Matrix pre{mul ? a.pre : nullptr, a.m, a.k, a.ldp, 2};
+  const Matrix dx{a.dx, a.m, a.k, a.lddx, 2};
+  const Matrix dw{a.dw, wr, wc, a.lddw, 4};
+  const Matrix db{a.db, 1, a.n, a.n, 4};
+  const Matrix work{scratch, 1, int64_t(pb::kLinearScratchBytes), 0, 1};
+  if (a.m > 0) {
+    s = check_matrix(dy, "dy");
+    if (s == PB_OK && a.dx != nullptr) s = check_matrix(dx, "dx");
+    if (s == PB_OK && a.dx != nullptr) s = check_matrix(w, "w");
+    if (s == PB_OK && mul) s = check_matrix(pre, "pre");
+    if (s == PB_OK && a.dw != nullptr) s = check_matrix(x, "x");
+    if (s != PB_OK) return s;
+  }
+  if (a.dw != nullptr) s = check_matrix(dw, "dw");
+  if (s != PB_OK) return s;
+  if (!aligned(a.db, 4)) return fail(PB_ERR_INVALID_ARG, "db must be 4-byte aligned");
+  if (a.db != nullptr && a.m > 0 && scratch == nullptr)
+    return fail(PB_ERR_WORKSPACE, "db needs scratch");
+  const Matrix* outs[3] = {&dx, &dw, &db};
+  const char* const names[3] = {"dx", "dw", "db"};
+  const Matrix* all[8] = {&dy, &x, &w, &pre, &dx, &dw, &db, &work};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i]->p == nullptr || (i == 0 && a.m == 0)) continue;
+    for (const Matrix* o : all) {
+      if (o == outs[i] || o->rows == 0) continue;
+      s = check_apart(*outs[i], names[i], *o);
+      if (s != PB_OK) return s;
+    }
+  }
+  const pb::OpType op = a.dtype == PB_DTYPE_FP16 ? pb::kOpF16 : pb::kOpBf16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.m == 0) {  // no tokens: the sums over them are zero
+    if (!a.accumulate) {
+      if (a.dw != nullptr)
+        PB_CUDA(cudaMemset2DAsync(a.dw, size_t(a.lddw) * 4, 0, size_t(wc) * 4, size_t(wr), st),
+                "cudaMemset2DAsync(dw)");
+      if (a.db != nullptr)
+        PB_CUDA(cudaMemsetAsync(a.db, 0, size_t(a.n) * 4, st), "cudaMemsetAsync(db)");
+    }
+    return PB_OK;
+  }
+  for (int64_t c = 0; a.db != nullptr && c < a.n; c += kSumCols) {
+    const int64_t cols = a.n - c < kSumCols ? a.n - c : kSumCols;
+    PB_CUDA(pb::launch_row_sums(op, static_cast<const uint16_t*>(a.dy) + c, a.m, cols, a.lddy,
+                                static_cast<float*>(scratch), a.db + c, a.accumulate != 0, st),
+            "bias gradient launch");
+  }
+  if (a.dx != nullptr) {
+    // the contraction runs over n: dy and an [k, n] w are K-major
+    EpiParams ep{};
+    ep.lin.act = a.activation;
+    ep.lin.mul = mul ? a.pre : nullptr;
+    if (!mul) ep.lin.act = PB_ACT_NONE;
+    ep.lin.ld_mul = a.ldp;
+    ep.lin.y16 = a.dx;
+    ep.lin.ldy = a.lddx;
+    if (a.m <= pb::kFewRows) {
+      pb::FewParams f{a.m, a.k, a.n, a.dy, a.w, a.lddy, a.ldw, ep.lin};
+      PB_CUDA(pb::launch_linear_few(op, !in_out, f, st), "linear backward (dx) launch");
+    } else {
+      CUtensorMap ta, tb;
+      s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::kGemmBoxRows, op);
+      if (s == PB_OK)
+        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, in_out ? pb::kGemmBoxRows : 64, op);
+      if (s == PB_OK)
+        s = make_store_map(&ep.tm_out0, a.dx, dx.rows, dx.cols, dx.ld, op == pb::kOpF16);
+      if (s != PB_OK) return s;
+      PB_CUDA(pb::launch_gemm_linear(op, in_out ? pb::kKK : pb::kKM, ta, tb, a.m, a.k, a.n, ep,
+                                     status, kDefaultLimitNs, scratch, st),
+              "linear backward (dx) launch");
+    }
+  }
+  if (a.dw != nullptr) {
+    // the contraction runs over the tokens: both operands are MN-major
+    const Matrix& ra = in_out ? x : dy;
+    const Matrix& rb = in_out ? dy : x;
+    CUtensorMap ta, tb;
+    s = make_map_2d(&ta, ra.p, ra.rows, ra.cols, ra.ld, 64, op);
+    if (s == PB_OK) s = make_map_2d(&tb, rb.p, rb.rows, rb.cols, rb.ld, 64, op);
+    if (s != PB_OK) return s;
+    EpiParams ep{};
+    ep.lin.y32 = a.dw;
+    ep.lin.ldy = a.lddw;
+    ep.lin.accumulate = a.accumulate != 0;
+    PB_CUDA(pb::launch_gemm_linear(op, pb::kMM, ta, tb, int(wr), int(wc), a.m, ep, status,
+                                   kDefaultLimitNs, scratch, st),
+            "linear backward (dw) launch");
+  }
+  return PB_OK;
+}
+
+pb_status pb_activation_backward(int64_t rows, int64_t cols, int32_t dtype, int32_t activation,
+                                 const void* dy, int64_t lddy, const void* pre, int64_t ldp,
+                                 void* out, int64_t ldo, void* stream) {
+  if (rows < 0 || cols < 1) return fail(PB_ERR_INVALID_ARG, "need rows >= 0 and cols >= 1");
+  if (rows >= (int64_t(1) << 40) || cols >= (int64_t(1) << 40))
+    return fail(PB_ERR_UNSUPPORTED, "rows or cols >= 2^40");
+  if (dtype != PB_DTYPE_BF16 && dtype != PB_DTYPE_FP16)
+    return fail(PB_ERR_UNSUPPORTED, "dtype must be PB_DTYPE_BF16 or PB_DTYPE_FP16");
+  if (activation < PB_ACT_NONE || activation > PB_ACT_RELU)
+    return fail(PB_ERR_INVALID_ARG, "activation %d is not a pb_activation", activation);
+  if (rows == 0) return PB_OK;
+  const Matrix d{dy, rows, cols, lddy, 2}, z{pre, rows, cols, ldp, 2}, o{out, rows, cols, ldo, 2};
+  pb_status s = check_matrix(d, "dy");
+  if (s == PB_OK) s = check_matrix(z, "pre");
+  if (s == PB_OK) s = check_matrix(o, "out");
+  if (s == PB_OK && !(out == dy && ldo == lddy)) s = check_apart(o, "out", d);
+  if (s == PB_OK && !(out == pre && ldo == ldp)) s = check_apart(o, "out", z);
+  if (s != PB_OK) return s;
+  PB_CUDA(pb::launch_act_backward(dtype == PB_DTYPE_FP16 ? pb::kOpF16 : pb::kOpBf16, activation,
+                                  rows, cols, dy, lddy, pre, ldp, out, ldo,
+                                  static_cast<cudaStream_t>(stream)),
+          "activation backward launch");
   return PB_OK;
 }
 

@@ -22,6 +22,15 @@ STATUS_NAMES = {0: "PB_OK", 1: "PB_ERR_INVALID_ARG", 2: "PB_ERR_UNSUPPORTED",
                 3: "PB_ERR_WORKSPACE", 4: "PB_ERR_CUDA", 5: "PB_ERR_DEVICE_TIMEOUT",
                 6: "PB_ERR_BAD_HANDLE", 7: "PB_ERR_RANGE"}
 PB_OPERANDS_BF16, PB_OPERANDS_FP16, PB_OPERANDS_FP8 = 0, 1, 2
+PB_DTYPE_BF16, PB_DTYPE_FP16, PB_DTYPE_FP32 = 0, 1, 2
+PB_WEIGHT_IN_OUT, PB_WEIGHT_OUT_IN = 0, 1
+PB_ADAMW_BLOCK = 256
+PB_ROPE_MAX_AXES = 4
+ACTIVATIONS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
+ROPE_PAIRINGS = {"halves": 0, "adjacent": 1}
+ROPE_LADDERS = {"shared": 0, "per_axis": 1}
+_DTYPES = {torch.bfloat16: PB_DTYPE_BF16, torch.float16: PB_DTYPE_FP16,
+           torch.float32: PB_DTYPE_FP32}
 
 
 class PbError(RuntimeError):
@@ -61,6 +70,52 @@ class pb_grads(ctypes.Structure):
 
 class pb_options(ctypes.Structure):
     _fields_ = [("operand_precision", ctypes.c_int32), ("wait_limit_ns", ctypes.c_uint64)]
+
+
+class pb_rope(ctypes.Structure):
+    _fields_ = [("magic", ctypes.c_uint32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("pairing", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("section_end", ctypes.c_int32 * PB_ROPE_MAX_AXES),
+                ("turns", ctypes.c_uint64 * 128)]
+
+
+class pb_heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("batch_stride", ctypes.c_int64), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class pb_linear_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("m", "n", "k", "dtype", "w_layout", "activation")] + [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p),
+        ("ldw", ctypes.c_int64), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+        ("ldr", ctypes.c_int64), ("residual_dtype", ctypes.c_int32), ("pre", ctypes.c_void_p),
+        ("ldp", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("y_dtype", ctypes.c_int32)]
+
+
+class pb_linear_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("m", "n", "k", "dtype", "w_layout", "activation", "accumulate")] + [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("x", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+        ("pre", ctypes.c_void_p), ("ldp", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+        ("db", ctypes.c_void_p)]
+
+
+class pb_adamw_tensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("param", "param_copy", "grad", "m", "v", "m_scale",
+                                       "v_scale")] + [("weight_decay", ctypes.c_float)]
+
+
+class pb_adamw_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+        ("d_lr", ctypes.c_void_p), ("d_step", ctypes.c_void_p),
+        ("d_grad_scale", ctypes.c_void_p)]
 
 
 # name -> (restype, argtypes); every function of include/pb.h
@@ -103,6 +158,20 @@ SIGNATURES = {
     "pb_gemm_bf16_static": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pb_set_guard_bytes": (ctypes.c_int, [_S]),
     "pb_get_guard_bytes": (ctypes.c_int, [ctypes.POINTER(_S)]),
+    "pb_rope_init": (ctypes.c_int, [_I32, _I32, _I32, _I32, _P, _I32, ctypes.c_double, _P, _P]),
+    "pb_qk_norm_rope": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P,
+                                       _P]),
+    "pb_qk_norm_rope_scratch_bytes": (ctypes.c_int, [ctypes.POINTER(_S)]),
+    "pb_qk_norm_rope_backward": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float,
+                                                _P, _P, _P, _P, _P, _P, _P, _I32, _P, _S, _P]),
+    "pb_linear_scratch_bytes": (ctypes.c_int, [ctypes.POINTER(_S)]),
+    "pb_linear": (ctypes.c_int, [_P, _P, _S, _P, _P]),
+    "pb_linear_backward": (ctypes.c_int, [_P, _P, _S, _P, _P]),
+    "pb_activation_backward": (ctypes.c_int, [_I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _P,
+                                              _I64, _P]),
+    "pb_adamw": (ctypes.c_int, [_P, _I32, _P, _P]),
+    "pb_grad_norm_scratch_bytes": (ctypes.c_int, [_I32, ctypes.POINTER(_S)]),
+    "pb_grad_norm": (ctypes.c_int, [_I32, _P, _I32, ctypes.c_float, _P, _P, _S, _P]),
 }
 
 _lib = None
@@ -477,3 +546,345 @@ def swa_attention(dims: pb_dims, qk, vt, act, status=None, stream=None):
 def wait_probe(limit_ns: int, status: torch.Tensor, stream=None):
     """Runs the bounded-wait self-test kernel; ``status`` is a 1-element int32 CUDA tensor."""
     _check("pb_wait_probe", lib().pb_wait_probe(int(limit_ns), _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------------------------- arguments of the steps
+# below: the library sees pointers and strides only, so what a tensor knows is checked here.
+
+def _here(*tensors):
+    """Every given tensor is a CUDA tensor on the current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _is(cond: bool, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def _rows(t: torch.Tensor, shape, dtype, what: str):
+    """A [rows, cols] tensor with contiguous rows; returns its row stride."""
+    _is(t.dim() == 2 and tuple(t.shape) == tuple(shape), f"{what} must be {tuple(shape)}")
+    _is(t.dtype == dtype, f"{what} must be {dtype}")
+    s0, s1 = t.stride()
+    _is(s1 == 1 or t.shape[1] == 1, f"{what}: the values of a row must be contiguous")
+    return s0 if t.shape[0] > 1 else t.shape[1] + (-t.shape[1]) % 8
+
+
+def _new_rows(rows: int, cols: int, dtype, device, zero: bool = False) -> torch.Tensor:
+    """A new [rows, cols] tensor whose rows start on 16-byte boundaries."""
+    new = torch.zeros if zero else torch.empty
+    return new((rows, cols + (-cols) % 8), dtype=dtype, device=device)[:, :cols] if cols % 8 else \
+        new((rows, cols), dtype=dtype, device=device)
+
+
+def _flat(t, n: int, dtype, what: str):
+    """A contiguous tensor of n values, or None; returns its address."""
+    if t is None:
+        return None
+    _is(t.dtype == dtype and t.numel() == n and t.is_contiguous(),
+        f"{what} must be {n} contiguous values of {dtype}")
+    return t.data_ptr()
+
+
+# ------------------------------------------------------------------- query/key norm, rotation
+
+class Rope:
+    """The plan of a rotation (``pb_rope_init``): ``sections`` are the pairs of each axis
+    (their sum is ``rot_dim / 2``; default one axis), ``inv_freq`` radians a position of every
+    pair instead of ``theta``'s ladder. Host memory only; may be shared."""
+
+    def __init__(self, head_dim: int, rot_dim: int | None = None, theta: float = 10000.0,
+                 pairing: str = "halves", sections=None, ladder: str = "shared", inv_freq=None):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        n = 1 if sections is None else len(sections)
+        sec = None if sections is None else (ctypes.c_int32 * n)(*sections)
+        freq = None
+        if inv_freq is not None:
+            _is(len(inv_freq) == rot_dim // 2, "inv_freq must have rot_dim / 2 values")
+            freq = (ctypes.c_double * max(1, len(inv_freq)))(*[float(f) for f in inv_freq])
+        self.plan = pb_rope()
+        self.head_dim, self.axes = head_dim, n
+        _check("pb_rope_init", lib().pb_rope_init(
+            head_dim, rot_dim, ROPE_PAIRINGS[pairing], n, sec, ROPE_LADDERS[ladder],
+            float(theta), freq, ctypes.byref(self.plan)))
+
+
+def _heads(t, head_dim: int, tokens, what: str):
+    """``pb_heads`` of a [batch, seq, heads, head_dim] bf16 view."""
+    if t is None:
+        return None
+    _is(t.dim() == 4 and t.shape[3] == head_dim and tuple(t.shape[:2]) == tokens,
+        f"{what} must be [batch, seq, heads, head_dim], head_dim {head_dim}")
+    _is(t.dtype == torch.bfloat16, f"{what} must be torch.bfloat16")
+    b, s, h, d = t.stride()
+    _is(d == 1, f"{what}: the values of a head must be contiguous")
+    return pb_heads(t.data_ptr(), t.shape[2], b if t.shape[0] > 1 else 0,
+                    s if t.shape[1] > 1 else 0, h if t.shape[2] > 1 else 0)
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _rope_common(rope, first, positions, gamma_q, gamma_k):
+    b, s = first.shape[0], first.shape[1]
+    if positions is not None:
+        _is(positions.dtype == torch.int32 and positions.is_contiguous()
+            and positions.numel() == rope.axes * b * s,
+            "positions must be contiguous int32 [axes, batch, seq]")
+    return (b, s), None if positions is None else positions.data_ptr()
+
+
+def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, eps: float = 1e-6,
+                 out_q=None, out_k=None, stream=None):
+    """``pb_qk_norm_rope``: norm (where there is a gamma) and rotation of ``q`` and ``k``
+    ([batch, seq, heads, head_dim] bf16 views, either may be None) at ``positions`` (int32
+    [axes, batch, seq]; None: 0, 1, ... in each sequence). ``out_q=q`` works in place."""
+    first = q if q is not None else k
+    _is(first is not None, "q and k are both None")
+    tokens, pos = _rope_common(rope, first, positions, gamma_q, gamma_k)
+    if q is not None and out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and out_k is None:
+        out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _here(q, k, positions, gamma_q, gamma_k, out_q, out_k)
+    d = rope.head_dim
+    _check("pb_qk_norm_rope", lib().pb_qk_norm_rope(
+        ctypes.byref(rope.plan), tokens[0], tokens[1], _ref(_heads(q, d, tokens, "q")),
+        _ref(_heads(k, d, tokens, "k")), _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
+        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, pos,
+        _ref(_heads(out_q, d, tokens, "out_q")), _ref(_heads(out_k, d, tokens, "out_k")),
+        _stream(stream)))
+    return out_q, out_k
+
+
+def qk_norm_rope_scratch_bytes() -> int:
+    n = ctypes.c_size_t()
+    _check("pb_qk_norm_rope_scratch_bytes", lib().pb_qk_norm_rope_scratch_bytes(ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_backward(rope: Rope, q, k, positions, dq, dk, gamma_q=None, gamma_k=None,
+                          eps: float = 1e-6, out_dq=None, out_dk=None, dgamma_q=None,
+                          dgamma_k=None, accumulate: bool = False, scratch=None, stream=None):
+    """``pb_qk_norm_rope_backward``: ``(dq, dk, dgamma_q, dgamma_k)`` of the forward call's
+    inputs, from the gradients ``dq``, ``dk`` of its results. ``q`` and ``k`` are the forward's
+    inputs (None where there is no gamma); a gamma's gradient is fp32 [head_dim], None without
+    that gamma, and added to with ``accumulate`` (give the buffer)."""
+    first = dq if dq is not None else dk
+    _is(first is not None, "dq and dk are both None")
+    tokens, pos = _rope_common(rope, first, positions, gamma_q, gamma_k)
+    d, dev = rope.head_dim, first.device
+    if dq is not None and out_dq is None:
+        out_dq = torch.empty(dq.shape, dtype=dq.dtype, device=dev)
+    if dk is not None and out_dk is None:
+        out_dk = torch.empty(dk.shape, dtype=dk.dtype, device=dev)
+    new = torch.zeros if accumulate else torch.empty
+    if gamma_q is not None and dq is not None and dgamma_q is None:
+        dgamma_q = new(d, dtype=torch.float32, device=dev)
+    if gamma_k is not None and dk is not None and dgamma_k is None:
+        dgamma_k = new(d, dtype=torch.float32, device=dev)
+    if scratch is None and (gamma_q is not None or gamma_k is not None):
+        scratch = torch.empty(qk_norm_rope_scratch_bytes(), dtype=torch.uint8, device=dev)
+    _here(q, k, positions, dq, dk, gamma_q, gamma_k, out_dq, out_dk, dgamma_q, dgamma_k, scratch)
+    _check("pb_qk_norm_rope_backward", lib().pb_qk_norm_rope_backward(
+        ctypes.byref(rope.plan), tokens[0], tokens[1], _ref(_heads(q, d, tokens, "q")),
+        _ref(_heads(k, d, tokens, "k")), _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
+        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, pos,
+        _ref(_heads(dq, d, tokens, "dq")), _ref(_heads(dk, d, tokens, "dk")),
+        _ref(_heads(out_dq, d, tokens, "out_dq")), _ref(_heads(out_dk, d, tokens, "out_dk")),
+        _flat(dgamma_q, d, torch.float32, "dgamma_q"),
+        _flat(dgamma_k, d, torch.float32, "dgamma_k"), int(accumulate), _ptr(scratch),
+        0 if scratch is None else scratch.numel(), _stream(stream)))
+    return out_dq, out_dk, dgamma_q, dgamma_k
+
+
+# ------------------------------------------------------------------- linear
+
+def linear_scratch_bytes() -> int:
+    n = ctypes.c_size_t()
+    _check("pb_linear_scratch_bytes", lib().pb_linear_scratch_bytes(ctypes.byref(n)))
+    return n.value
+
+
+def linear(x, w, bias=None, residual=None, activation: str = "none",
+           layout: int = PB_WEIGHT_IN_OUT, out=None, out_dtype=None, pre=None, scratch=None,
+           status=None, stream=None):
+    """``pb_linear``: ``activation(x @ w + bias) + residual`` for ``x`` [m, k] and ``w`` [k, n]
+    (or [n, k], ``PB_WEIGHT_OUT_IN``), bf16 or fp16; ``out_dtype`` (or ``out``'s) is theirs or
+    fp32. ``pre`` (a [m, n] tensor of their type) receives ``x @ w + bias``. ``scratch`` (a
+    uint8 CUDA tensor of ``linear_scratch_bytes()``) lets the product be split along k."""
+    m, k = x.shape
+    n = w.shape[1 if layout == PB_WEIGHT_IN_OUT else 0]
+    dt = x.dtype
+    _is(dt in (torch.bfloat16, torch.float16), "x must be torch.bfloat16 or torch.float16")
+    if out is None:
+        out = _new_rows(m, n, out_dtype or dt, x.device)
+    _is(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    _is(out.dtype in (dt, torch.float32), f"out must be {dt} or torch.float32")
+    _here(x, w, bias, residual, out, pre, scratch, status)
+    a = pb_linear_args(m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], x.data_ptr(),
+                       _rows(x, (m, k), dt, "x"), w.data_ptr(),
+                       _rows(w, (k, n) if layout == PB_WEIGHT_IN_OUT else (n, k), dt, "w"),
+                       _flat(bias, n, dt, "bias"))
+    if residual is not None:
+        _is(residual.dtype in (dt, torch.float32), f"residual must be {dt} or torch.float32")
+        a.residual, a.residual_dtype = residual.data_ptr(), _DTYPES[residual.dtype]
+        a.ldr = _rows(residual, (m, n), residual.dtype, "residual")
+    if pre is not None:
+        a.pre, a.ldp = pre.data_ptr(), _rows(pre, (m, n), dt, "pre")
+    a.y, a.ldy, a.y_dtype = out.data_ptr(), _rows(out, (m, n), out.dtype, "out"), \
+        _DTYPES[out.dtype]
+    _check("pb_linear", lib().pb_linear(ctypes.byref(a), _ptr(scratch),
+                                        0 if scratch is None else scratch.numel(), _ptr(status),
+                                        _stream(stream)))
+    return out
+
+
+def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = PB_WEIGHT_IN_OUT,
+                    need_dx: bool = True, need_dw: bool = True, bias: bool = False, dx=None,
+                    dw=None, db=None, accumulate: bool = False, scratch=None, status=None,
+                    stream=None):
+    """``pb_linear_backward``: ``(dx, dw, db)`` of ``x @ w + bias`` for ``dy`` [m, n]; dx in the
+    operands' type, dw (``w``'s layout) and db fp32, None where not wanted. ``pre`` and
+    ``activation``: ``x`` is ``activation(pre)``, and dx is the gradient of ``pre``.
+    ``accumulate`` adds to the given ``dw`` and ``db``."""
+    m, n = dy.shape
+    in_out = layout == PB_WEIGHT_IN_OUT
+    k = (x if x is not None else w).shape[1 if x is not None or not in_out else 0]
+    dt, dev = dy.dtype, dy.device
+    _is(dt in (torch.bfloat16, torch.float16), "dy must be torch.bfloat16 or torch.float16")
+    w_shape = (k, n) if in_out else (n, k)
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    if need_dx and dx is None:
+        dx = _new_rows(m, k, dt, dev)
+    if need_dw and dw is None:
+        dw = _new_rows(*w_shape, torch.float32, dev, zero=accumulate)
+    if bias and db is None:
+        db = (torch.zeros if accumulate else torch.empty)(n, dtype=torch.float32, device=dev)
+    if db is not None and scratch is None:
+        scratch = torch.empty(linear_scratch_bytes(), dtype=torch.uint8, device=dev)
+    _here(dy, x, w, pre, dx, dw, db, scratch, status)
+    _is((pre is not None) == (ACTIVATIONS[activation] != 0), "pre goes with an activation")
+    a = pb_linear_grads(m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], int(accumulate),
+                        dy.data_ptr(), _rows(dy, (m, n), dt, "dy"))
+    if need_dw:
+        _is(x is not None, "dw needs x")
+        a.x, a.ldx = x.data_ptr(), _rows(x, (m, k), dt, "x")
+        a.dw, a.lddw = dw.data_ptr(), _rows(dw, w_shape, torch.float32, "dw")
+    if need_dx:
+        _is(w is not None, "dx needs w")
+        a.w, a.ldw = w.data_ptr(), _rows(w, w_shape, dt, "w")
+        a.dx, a.lddx = dx.data_ptr(), _rows(dx, (m, k), dt, "dx")
+        if pre is not None:
+            a.pre, a.ldp = pre.data_ptr(), _rows(pre, (m, k), dt, "pre")
+    a.db = _flat(db, n, torch.float32, "db")
+    _check("pb_linear_backward", lib().pb_linear_backward(
+        ctypes.byref(a), _ptr(scratch), 0 if scratch is None else scratch.numel(), _ptr(status),
+        _stream(stream)))
+    return dx if need_dx else None, dw if need_dw else None, db
+
+
+def activation_backward(dy, pre, activation: str, out=None, stream=None):
+    """``pb_activation_backward``: ``dy * activation'(pre)``, [rows, cols] bf16 or fp16."""
+    rows, cols = dy.shape
+    _is(dy.dtype in (torch.bfloat16, torch.float16), "dy must be torch.bfloat16 or torch.float16")
+    if out is None:
+        out = _new_rows(rows, cols, dy.dtype, dy.device)
+    _here(dy, pre, out)
+    _check("pb_activation_backward", lib().pb_activation_backward(
+        rows, cols, _DTYPES[dy.dtype], ACTIVATIONS[activation], _ptr(dy),
+        _rows(dy, (rows, cols), dy.dtype, "dy"), _ptr(pre),
+        _rows(pre, (rows, cols), dy.dtype, "pre"), _ptr(out),
+        _rows(out, (rows, cols), dy.dtype, "out"), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------- AdamW
+
+class AdamW:
+    """The tensors of an AdamW step (``pb_adamw``). Each is a dict: ``param`` (fp32 or bf16,
+    updated in place), ``copy`` (a bf16 copy of fp32 parameters, or None), ``grad`` (fp32 or
+    bf16), the states ``m`` and ``v`` (fp32, or ``torch.float8_e4m3fn`` with fp32 ``m_scale``
+    and ``v_scale``, one per 256 values), ``weight_decay`` (default 0). States start at zero:
+    ``adamw_states`` makes them. Types are the same for all tensors of a step."""
+
+    def __init__(self, tensors, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8):
+        self.tensors = [dict(t) for t in tensors]
+        self.beta1, self.beta2, self.eps = float(beta1), float(beta2), float(eps)
+        n = len(self.tensors)
+        _is(n > 0, "no tensors")
+        t0 = self.tensors[0]
+        self.device = t0["param"].device
+        ptype, gtype, eight = t0["param"].dtype, t0["grad"].dtype, t0.get("m_scale") is not None
+        _is(ptype in (torch.float32, torch.bfloat16), "param must be fp32 or bf16")
+        _is(gtype in (torch.float32, torch.bfloat16), "grad must be fp32 or bf16")
+        self.param_dtype, self.grad_dtype = _DTYPES[ptype], _DTYPES[gtype]
+        self.state_bits = 8 if eight else 32
+        stype = torch.float8_e4m3fn if eight else torch.float32
+        self.array = (pb_adamw_tensor * n)()
+        for i, t in enumerate(self.tensors):
+            size = t["param"].numel()
+            blocks = -(-size // PB_ADAMW_BLOCK)
+            for name in ("param", "copy", "grad", "m", "v", "m_scale", "v_scale"):
+                x = t.get(name)
+                _is(x is None or x.device == self.device, f"tensor {i}: {name} is elsewhere")
+            _is((t.get("m_scale") is not None) == eight == (t.get("v_scale") is not None),
+                f"tensor {i}: m_scale and v_scale go with 8-bit states, for all tensors")
+            a = self.array[i]
+            a.n = size
+            a.param = _flat(t["param"], size, ptype, f"tensor {i}: param")
+            a.param_copy = _flat(t.get("copy"), size, torch.bfloat16, f"tensor {i}: copy")
+            a.grad = _flat(t["grad"], size, gtype, f"tensor {i}: grad")
+            a.m = _flat(t["m"], size, stype, f"tensor {i}: m")
+            a.v = _flat(t["v"], size, stype, f"tensor {i}: v")
+            a.m_scale = _flat(t.get("m_scale"), blocks, torch.float32, f"tensor {i}: m_scale")
+            a.v_scale = _flat(t.get("v_scale"), blocks, torch.float32, f"tensor {i}: v_scale")
+            a.weight_decay = float(t.get("weight_decay", 0.0))
+        b = ctypes.c_size_t()
+        _check("pb_grad_norm_scratch_bytes", lib().pb_grad_norm_scratch_bytes(n, ctypes.byref(b)))
+        self.scratch_bytes = b.value
+
+    def grad_norm(self, max_norm: float, out=None, scratch=None, stream=None) -> torch.Tensor:
+        """``pb_grad_norm``: fp32 [2], the norm of all gradients and the factor that clips them
+        to ``max_norm`` (``step(grad_scale=out[1:])``)."""
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+        if scratch is None:
+            scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=self.device)
+        _here(out, scratch, self.tensors[0]["param"])
+        _check("pb_grad_norm", lib().pb_grad_norm(
+            len(self.tensors), self.array, self.grad_dtype, max_norm,
+            _flat(out, 2, torch.float32, "out"), _ptr(scratch), scratch.numel(),
+            _stream(stream)))
+        return out
+
+    def step(self, lr: float, step: int = 0, grad_scale=None, d_lr=None, d_step=None,
+             stream=None):
+        """``pb_adamw``, in place: step number ``step`` (from 1 on). ``d_lr`` (fp32), ``d_step``
+        (int32) and ``grad_scale`` (fp32): one-element CUDA tensors read when the step runs."""
+        _here(grad_scale, d_lr, d_step, self.tensors[0]["param"])
+        a = pb_adamw_args(lr, self.beta1, self.beta2, self.eps, step, self.param_dtype,
+                          self.grad_dtype, self.state_bits,
+                          _flat(d_lr, 1, torch.float32, "d_lr"),
+                          _flat(d_step, 1, torch.int32, "d_step"),
+                          _flat(grad_scale, 1, torch.float32, "grad_scale"))
+        _check("pb_adamw", lib().pb_adamw(ctypes.byref(a), len(self.tensors), self.array,
+                                          _stream(stream)))
+
+
+def adamw_states(param: torch.Tensor, bits: int = 32) -> dict:
+    """The states of one tensor before its first step: ``m`` and ``v``, with ``bits=8`` their
+    scales too."""
+    _is(bits in (8, 32), "bits must be 8 or 32")
+    n = param.numel()
+    if bits == 32:
+        return {k: torch.zeros(n, dtype=torch.float32, device=param.device) for k in ("m", "v")}
+    st = {k: torch.zeros(n, dtype=torch.uint8, device=param.device).view(torch.float8_e4m3fn)
+          for k in ("m", "v")}
+    for k in ("m_scale", "v_scale"):
+        st[k] = torch.zeros(-(-n // PB_ADAMW_BLOCK), dtype=torch.float32, device=param.device)
+    return st
