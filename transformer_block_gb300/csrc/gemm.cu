@@ -1178,7 +1178,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int g = 0; g < u.mt; ++g) {
           const int row = u.row0 + g * PM + int(rank) * BM + int(quad * 32 + lane);
           const uint32_t taddr = lane_base + uint32_t((MT == 2 ? g : acc) * BN);
-          const size_t part_off = (size_t(rank) * 128 + quad * 32 + lane) * BN;
+          // this warp's 32 x 256 of a partial tile: 16-byte pieces in the order [piece of a
+          // row][row], so a warp's accesses are whole 512-byte runs
+          const size_t part_off = (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
           // the pairs that hold part of this tile: first (its last share) to last
           int first = sc.cluster, last = sc.cluster;
           bool mine = true;
@@ -1197,10 +1199,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               tmem_ld32(taddr + uint32_t(c * 32), r);
               tmem_ld_wait(r);
               if (row < ep.M) {
-                float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
+                float4* d4 = reinterpret_cast<float4*>(dst + c * 1024);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                  __stcg(d4 + q,
+                  __stcg(d4 + 32 * q,
                          make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
                                      __uint_as_float(r[4 * q + 2]),
                                      __uint_as_float(r[4 * q + 3])));
@@ -1231,14 +1233,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
               for (int c2 = first; c2 <= last; ++c2) {
                 const float4* p4 = reinterpret_cast<const float4*>(
                     sk.partials + (size_t(c2) * 2 + (c2 == first ? 1 : 0)) * (2 * 128 * BN) +
-                    part_off + c * 32);
+                    part_off + c * 1024);
                 if (row < ep.M) {
 #pragma unroll
                   for (int q = 0; q < 8; ++q) {
-                    const float4 pv = __ldcg(p4 + q);
+                    const float4 pv = __ldcg(p4 + 32 * q);
                     v[4 * q] += pv.x;
                     v[4 * q + 1] += pv.y;
                     v[4 * q + 2] += pv.z;

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -209,8 +210,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: no Stream object for every call
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -564,13 +565,14 @@ def _is(cond: bool, what: str):
         raise ValueError(what)
 
 
-def _rows(t: torch.Tensor, shape, dtype, what: str):
+def _rows(t: torch.Tensor, rows: int, cols: int, dtype, what: str) -> int:
     """A [rows, cols] tensor with contiguous rows; returns its row stride."""
-    _is(t.dim() == 2 and tuple(t.shape) == tuple(shape), f"{what} must be {tuple(shape)}")
-    _is(t.dtype == dtype, f"{what} must be {dtype}")
+    if t.dtype is not dtype or t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{what} must be [{rows}, {cols}] {dtype}")
     s0, s1 = t.stride()
-    _is(s1 == 1 or t.shape[1] == 1, f"{what}: the values of a row must be contiguous")
-    return s0 if t.shape[0] > 1 else t.shape[1] + (-t.shape[1]) % 8
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{what}: the values of a row must be contiguous")
+    return s0 if rows > 1 else cols + (-cols) % 8
 
 
 def _new_rows(rows: int, cols: int, dtype, device, zero: bool = False) -> torch.Tensor:
@@ -584,8 +586,8 @@ def _flat(t, n: int, dtype, what: str):
     """A contiguous tensor of n values, or None; returns its address."""
     if t is None:
         return None
-    _is(t.dtype == dtype and t.numel() == n and t.is_contiguous(),
-        f"{what} must be {n} contiguous values of {dtype}")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be {n} contiguous values of {dtype}")
     return t.data_ptr()
 
 
@@ -612,30 +614,30 @@ class Rope:
             float(theta), freq, ctypes.byref(self.plan)))
 
 
-def _heads(t, head_dim: int, tokens, what: str):
+# pb_heads as bytes: cheaper to make for every call than a ctypes structure
+_pack_heads = struct.Struct("@Piqqq").pack
+assert struct.calcsize("@Piqqq") == ctypes.sizeof(pb_heads)
+
+
+def _heads(t, head_dim: int, b: int, s: int, what: str):
     """``pb_heads`` of a [batch, seq, heads, head_dim] bf16 view."""
     if t is None:
         return None
-    _is(t.dim() == 4 and t.shape[3] == head_dim and tuple(t.shape[:2]) == tokens,
-        f"{what} must be [batch, seq, heads, head_dim], head_dim {head_dim}")
-    _is(t.dtype == torch.bfloat16, f"{what} must be torch.bfloat16")
-    b, s, h, d = t.stride()
-    _is(d == 1, f"{what}: the values of a head must be contiguous")
-    return pb_heads(t.data_ptr(), t.shape[2], b if t.shape[0] > 1 else 0,
-                    s if t.shape[1] > 1 else 0, h if t.shape[2] > 1 else 0)
+    if t.dtype is not torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{what} must be a bfloat16 [batch, seq, heads, head_dim]")
+    n0, n1, h, d = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if n0 != b or n1 != s or d != head_dim or s3 != 1:
+        raise ValueError(f"{what} must be [{b}, {s}, heads, {head_dim}], a head's values "
+                         "contiguous")
+    return _pack_heads(t.data_ptr(), h, s0 if b > 1 else 0, s1 if s > 1 else 0,
+                       s2 if h > 1 else 0)
 
 
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
-
-
-def _rope_common(rope, first, positions, gamma_q, gamma_k):
-    b, s = first.shape[0], first.shape[1]
-    if positions is not None:
-        _is(positions.dtype == torch.int32 and positions.is_contiguous()
-            and positions.numel() == rope.axes * b * s,
-            "positions must be contiguous int32 [axes, batch, seq]")
-    return (b, s), None if positions is None else positions.data_ptr()
+def _positions(rope, positions, b: int, s: int):
+    if positions is None:
+        return None
+    return _flat(positions, rope.axes * b * s, torch.int32, "positions ([axes, batch, seq])")
 
 
 def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, eps: float = 1e-6,
@@ -645,7 +647,7 @@ def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, e
     [axes, batch, seq]; None: 0, 1, ... in each sequence). ``out_q=q`` works in place."""
     first = q if q is not None else k
     _is(first is not None, "q and k are both None")
-    tokens, pos = _rope_common(rope, first, positions, gamma_q, gamma_k)
+    b, s = first.size(0), first.size(1)
     if q is not None and out_q is None:
         out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k is not None and out_k is None:
@@ -653,11 +655,10 @@ def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, e
     _here(q, k, positions, gamma_q, gamma_k, out_q, out_k)
     d = rope.head_dim
     _check("pb_qk_norm_rope", lib().pb_qk_norm_rope(
-        ctypes.byref(rope.plan), tokens[0], tokens[1], _ref(_heads(q, d, tokens, "q")),
-        _ref(_heads(k, d, tokens, "k")), _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
-        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, pos,
-        _ref(_heads(out_q, d, tokens, "out_q")), _ref(_heads(out_k, d, tokens, "out_k")),
-        _stream(stream)))
+        ctypes.addressof(rope.plan), b, s, _heads(q, d, b, s, "q"), _heads(k, d, b, s, "k"),
+        _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
+        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, _positions(rope, positions, b, s),
+        _heads(out_q, d, b, s, "out_q"), _heads(out_k, d, b, s, "out_k"), _stream(stream)))
     return out_q, out_k
 
 
@@ -676,7 +677,7 @@ def qk_norm_rope_backward(rope: Rope, q, k, positions, dq, dk, gamma_q=None, gam
     that gamma, and added to with ``accumulate`` (give the buffer)."""
     first = dq if dq is not None else dk
     _is(first is not None, "dq and dk are both None")
-    tokens, pos = _rope_common(rope, first, positions, gamma_q, gamma_k)
+    b, s = first.size(0), first.size(1)
     d, dev = rope.head_dim, first.device
     if dq is not None and out_dq is None:
         out_dq = torch.empty(dq.shape, dtype=dq.dtype, device=dev)
@@ -691,11 +692,11 @@ def qk_norm_rope_backward(rope: Rope, q, k, positions, dq, dk, gamma_q=None, gam
         scratch = torch.empty(qk_norm_rope_scratch_bytes(), dtype=torch.uint8, device=dev)
     _here(q, k, positions, dq, dk, gamma_q, gamma_k, out_dq, out_dk, dgamma_q, dgamma_k, scratch)
     _check("pb_qk_norm_rope_backward", lib().pb_qk_norm_rope_backward(
-        ctypes.byref(rope.plan), tokens[0], tokens[1], _ref(_heads(q, d, tokens, "q")),
-        _ref(_heads(k, d, tokens, "k")), _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
-        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, pos,
-        _ref(_heads(dq, d, tokens, "dq")), _ref(_heads(dk, d, tokens, "dk")),
-        _ref(_heads(out_dq, d, tokens, "out_dq")), _ref(_heads(out_dk, d, tokens, "out_dk")),
+        ctypes.addressof(rope.plan), b, s, _heads(q, d, b, s, "q"), _heads(k, d, b, s, "k"),
+        _flat(gamma_q, d, torch.bfloat16, "gamma_q"),
+        _flat(gamma_k, d, torch.bfloat16, "gamma_k"), eps, _positions(rope, positions, b, s),
+        _heads(dq, d, b, s, "dq"), _heads(dk, d, b, s, "dk"), _heads(out_dq, d, b, s, "out_dq"),
+        _heads(out_dk, d, b, s, "out_dk"),
         _flat(dgamma_q, d, torch.float32, "dgamma_q"),
         _flat(dgamma_k, d, torch.float32, "dgamma_k"), int(accumulate), _ptr(scratch),
         0 if scratch is None else scratch.numel(), _stream(stream)))
@@ -710,6 +711,12 @@ def linear_scratch_bytes() -> int:
     return n.value
 
 
+# pb_linear_args as bytes
+_LINEAR_FORMAT = "@6iPqPqPPqiPqPqi0q"
+_pack_linear = struct.Struct(_LINEAR_FORMAT).pack
+assert struct.calcsize(_LINEAR_FORMAT) == ctypes.sizeof(pb_linear_args)
+
+
 def linear(x, w, bias=None, residual=None, activation: str = "none",
            layout: int = PB_WEIGHT_IN_OUT, out=None, out_dtype=None, pre=None, scratch=None,
            status=None, stream=None):
@@ -718,27 +725,29 @@ def linear(x, w, bias=None, residual=None, activation: str = "none",
     fp32. ``pre`` (a [m, n] tensor of their type) receives ``x @ w + bias``. ``scratch`` (a
     uint8 CUDA tensor of ``linear_scratch_bytes()``) lets the product be split along k."""
     m, k = x.shape
-    n = w.shape[1 if layout == PB_WEIGHT_IN_OUT else 0]
+    in_out = layout == PB_WEIGHT_IN_OUT
+    n = w.size(1 if in_out else 0)
     dt = x.dtype
-    _is(dt in (torch.bfloat16, torch.float16), "x must be torch.bfloat16 or torch.float16")
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("x must be torch.bfloat16 or torch.float16")
     if out is None:
         out = _new_rows(m, n, out_dtype or dt, x.device)
-    _is(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
-    _is(out.dtype in (dt, torch.float32), f"out must be {dt} or torch.float32")
+    od, rd = out.dtype, None if residual is None else residual.dtype
+    if (od is not dt and od is not torch.float32) or (out_dtype is not None and od != out_dtype):
+        raise ValueError(f"out must be {dt} or torch.float32, and out_dtype")
+    if rd is not None and rd is not dt and rd is not torch.float32:
+        raise ValueError(f"residual must be {dt} or torch.float32")
     _here(x, w, bias, residual, out, pre, scratch, status)
-    a = pb_linear_args(m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], x.data_ptr(),
-                       _rows(x, (m, k), dt, "x"), w.data_ptr(),
-                       _rows(w, (k, n) if layout == PB_WEIGHT_IN_OUT else (n, k), dt, "w"),
-                       _flat(bias, n, dt, "bias"))
-    if residual is not None:
-        _is(residual.dtype in (dt, torch.float32), f"residual must be {dt} or torch.float32")
-        a.residual, a.residual_dtype = residual.data_ptr(), _DTYPES[residual.dtype]
-        a.ldr = _rows(residual, (m, n), residual.dtype, "residual")
-    if pre is not None:
-        a.pre, a.ldp = pre.data_ptr(), _rows(pre, (m, n), dt, "pre")
-    a.y, a.ldy, a.y_dtype = out.data_ptr(), _rows(out, (m, n), out.dtype, "out"), \
-        _DTYPES[out.dtype]
-    _check("pb_linear", lib().pb_linear(ctypes.byref(a), _ptr(scratch),
+    args = _pack_linear(
+        m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], x.data_ptr(),
+        _rows(x, m, k, dt, "x"), w.data_ptr(),
+        _rows(w, k, n, dt, "w") if in_out else _rows(w, n, k, dt, "w"),
+        _flat(bias, n, dt, "bias") or 0, 0 if residual is None else residual.data_ptr(),
+        0 if residual is None else _rows(residual, m, n, rd, "residual"),
+        0 if residual is None else _DTYPES[rd], 0 if pre is None else pre.data_ptr(),
+        0 if pre is None else _rows(pre, m, n, dt, "pre"), out.data_ptr(),
+        _rows(out, m, n, od, "out"), _DTYPES[od])
+    _check("pb_linear", lib().pb_linear(args, _ptr(scratch),
                                         0 if scratch is None else scratch.numel(), _ptr(status),
                                         _stream(stream)))
     return out
@@ -770,17 +779,17 @@ def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = 
     _here(dy, x, w, pre, dx, dw, db, scratch, status)
     _is((pre is not None) == (ACTIVATIONS[activation] != 0), "pre goes with an activation")
     a = pb_linear_grads(m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], int(accumulate),
-                        dy.data_ptr(), _rows(dy, (m, n), dt, "dy"))
+                        dy.data_ptr(), _rows(dy, m, n, dt, "dy"))
     if need_dw:
         _is(x is not None, "dw needs x")
-        a.x, a.ldx = x.data_ptr(), _rows(x, (m, k), dt, "x")
-        a.dw, a.lddw = dw.data_ptr(), _rows(dw, w_shape, torch.float32, "dw")
+        a.x, a.ldx = x.data_ptr(), _rows(x, m, k, dt, "x")
+        a.dw, a.lddw = dw.data_ptr(), _rows(dw, *w_shape, torch.float32, "dw")
     if need_dx:
         _is(w is not None, "dx needs w")
-        a.w, a.ldw = w.data_ptr(), _rows(w, w_shape, dt, "w")
-        a.dx, a.lddx = dx.data_ptr(), _rows(dx, (m, k), dt, "dx")
+        a.w, a.ldw = w.data_ptr(), _rows(w, *w_shape, dt, "w")
+        a.dx, a.lddx = dx.data_ptr(), _rows(dx, m, k, dt, "dx")
         if pre is not None:
-            a.pre, a.ldp = pre.data_ptr(), _rows(pre, (m, k), dt, "pre")
+            a.pre, a.ldp = pre.data_ptr(), _rows(pre, m, k, dt, "pre")
     a.db = _flat(db, n, torch.float32, "db")
     _check("pb_linear_backward", lib().pb_linear_backward(
         ctypes.byref(a), _ptr(scratch), 0 if scratch is None else scratch.numel(), _ptr(status),
@@ -797,9 +806,9 @@ def activation_backward(dy, pre, activation: str, out=None, stream=None):
     _here(dy, pre, out)
     _check("pb_activation_backward", lib().pb_activation_backward(
         rows, cols, _DTYPES[dy.dtype], ACTIVATIONS[activation], _ptr(dy),
-        _rows(dy, (rows, cols), dy.dtype, "dy"), _ptr(pre),
-        _rows(pre, (rows, cols), dy.dtype, "pre"), _ptr(out),
-        _rows(out, (rows, cols), dy.dtype, "out"), _stream(stream)))
+        _rows(dy, rows, cols, dy.dtype, "dy"), _ptr(pre),
+        _rows(pre, rows, cols, dy.dtype, "pre"), _ptr(out),
+        _rows(out, rows, cols, dy.dtype, "out"), _stream(stream)))
     return out
 
 
