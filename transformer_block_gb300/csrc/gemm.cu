@@ -36,7 +36,15 @@ constexpr int BN = kGemmBN;       // output columns per pair tile
 constexpr int BK = kGemmBK;
 constexpr int A_BYTES = BM * BK * 2;        // 16 KB: this CTA's rows of A (one M tile)
 constexpr int B_BYTES = (BN / 2) * BK * 2;  // 16 KB: this CTA's half of B
-constexpr int THREADS = 192;
+// Epilogue warps: four, one for each quarter of the tensor memory's lanes. kEpiLinear has
+// eight, each quarter's columns shared by two: its epilogue may read a pre-activation or a
+// residual and evaluate an activation or its derivative, which four warps do not hide behind a
+// main loop of K = 2048 (8192 x 8192 x 2048 with GeLU': 224 us with four).
+template <int KIND>
+struct Warps {
+  static constexpr int EPI = KIND == kEpiLinear ? 8 : 4;
+  static constexpr int THREADS = 64 + 32 * EPI;
+};
 constexpr uint32_t TMEM_COLS = 512;
 // Per epilogue warp, a 32 x 32 fp32 chunk (rows padded to 33 words: conflict-free both
 // ways) for the coalesced gradient stores.
@@ -48,7 +56,7 @@ static_assert(4 * 32 * STAGE_PITCH * 4 >= 4 * 4096, "four warps' two 2 KB store 
 // (2 x 256 columns). MT = 2: a 512 x 256 unit whose two M tiles share every B stage (a
 // quarter less operand traffic per FLOP), four stages of two A tiles and B, one 256-column
 // accumulator per M tile (not double-buffered).
-template <int MT>
+template <int MT, int EPI_WARPS = 4>
 struct Geo {
   static_assert(MT == 1 || MT == 2, "one or two M tiles per unit");
   static constexpr int STAGES = MT == 2 ? 4 : 6;
@@ -57,7 +65,8 @@ struct Geo {
   // 1024-byte aligned: the forward epilogues' TMA-store buffers (64-byte swizzle) live here
   static constexpr size_t EPI_STAGE_OFF =
       (size_t(STAGES) * STAGE_BYTES + 8 * NUM_BARS + 16 + 1023) / 1024 * 1024;
-  static constexpr size_t SMEM_BYTES = 1024 + EPI_STAGE_OFF + 4 * 32 * STAGE_PITCH * 4;
+  static constexpr size_t SMEM_BYTES =
+      1024 + EPI_STAGE_OFF + (EPI_WARPS == 4 ? 4 * 32 * STAGE_PITCH * 4 : EPI_WARPS * 4096);
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of the GEMM");
 };
 
@@ -522,11 +531,12 @@ __device__ __forceinline__ float sigmoid_approx(float z) {
 // GeLU's tanh form is z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
 constexpr float kTanh2C = 1.5957691216057308f, kTanhA = 0.044715f;
 
-__device__ __forceinline__ void act_apply(int act, float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void act_apply(int act, float (&v)[N]) {
   if (act == kActNone) return;
   if (act == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+    for (int i = 0; i < N; i += 2) {
       float a = act_held(v[i]), b = act_held(v[i + 1]);
       gelu_pair(a, b);
       v[i] = v[i] > kActFar ? v[i] : a;
@@ -534,46 +544,47 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[32]) {
     }
   } else if (act == kActGeluTanh) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float z = act_held(v[i]);
       const float a = z * sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
       v[i] = v[i] > kActFar ? v[i] : a;
     }
   } else if (act == kActSilu) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float z = act_held(v[i]);
       const float a = z * sigmoid_approx(z);
       v[i] = v[i] > kActFar ? v[i] : a;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
   }
 }
 
 // d *= act'(z)
-__device__ __forceinline__ void act_grad_apply(int act, float (&d)[32], const float (&zs)[32]) {
+template <int N>
+__device__ __forceinline__ void act_grad_apply(int act, float (&d)[N], const float (&zs)[N]) {
   if (act == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
+    for (int i = 0; i < N; i += 2)
       gelu_grad_pair(d[i], d[i + 1], act_held(zs[i]), act_held(zs[i + 1]));
   } else if (act == kActGeluTanh) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float z = act_held(zs[i]);
       const float s = sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
       d[i] *= s + z * s * (1.f - s) * kTanh2C * (1.f + 3.f * kTanhA * z * z);
     }
   } else if (act == kActSilu) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float z = act_held(zs[i]), s = sigmoid_approx(z);
       d[i] *= s * (1.f + z * (1.f - s));
     }
   } else if (act == kActRelu) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) d[i] = zs[i] > 0.f ? d[i] : zs[i] <= 0.f ? 0.f : zs[i];
+    for (int i = 0; i < N; ++i) d[i] = zs[i] > 0.f ? d[i] : zs[i] <= 0.f ? 0.f : zs[i];
   }
 }
 
@@ -798,7 +809,7 @@ struct Sched {
 struct SkParams {
   int dp_tiles, sk_tiles, W;
   float* partials;  // [kSkMaxClusters][2][128][256]; kEpiLinear: [.. clusters][2 slots] of it
-  uint64_t* flags;  // [kSkMaxClusters][2][4]; kEpiLinear: a tile's counters [tiles][2][4]
+  uint64_t* flags;  // [kSkMaxClusters][2][4]; kEpiLinear: none
   uint64_t epoch;
   int seg;          // kEpiLinear, one M tile: k-blocks summed at a time in one accumulator
 };
@@ -861,34 +872,17 @@ __device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
   asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
-// One of n arrivals at a counter word of a launch: whether it is the last one, which leaves
-// the word at zero. Whatever another launch left in the word does not count: the upper 48
-// bits are the launch's epoch. Nobody waits; an exchange fails only where another succeeded.
-__device__ __forceinline__ bool arrive_is_last(uint64_t* word, uint64_t epoch, int n) {
-  auto* w = reinterpret_cast<unsigned long long*>(word);
-  const unsigned long long mine = (static_cast<unsigned long long>(epoch) << 16);
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
-  for (;;) {
-    const unsigned long long count = (old & ~0xffffull) == mine ? (old & 0xffffull) : 0ull;
-    const unsigned long long seen = atomicCAS(w, old, mine | (count + 1));
-    if (seen == old) {
-      const bool last = int(count) + 1 == n;
-      if (last) *reinterpret_cast<volatile unsigned long long*>(w) = 0ull;
-      return last;
-    }
-    old = seen;
-  }
-}
-
 template <int KIND, int OP, int LAYOUT, int MT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 int K, const __grid_constant__ EpiParams ep, const SkParams sk, int* status,
                 uint64_t limit_ns) {
   static_assert(MT == 1 || LAYOUT == kKK, "two M tiles per unit: K-major operands only");
-  constexpr int STAGES = Geo<MT>::STAGES, STAGE_BYTES = Geo<MT>::STAGE_BYTES;
-  constexpr int NUM_BARS = Geo<MT>::NUM_BARS;
-  constexpr size_t EPI_STAGE_OFF = Geo<MT>::EPI_STAGE_OFF;
+  constexpr int EPI_WARPS = Warps<KIND>::EPI;
+  using G = Geo<MT, EPI_WARPS>;
+  constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES;
+  constexpr int NUM_BARS = G::NUM_BARS;
+  constexpr size_t EPI_STAGE_OFF = G::EPI_STAGE_OFF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -898,7 +892,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t full0 = smem_u32(bars);                   // [STAGES]
   const uint32_t empty0 = smem_u32(bars + STAGES);         // [STAGES]
   const uint32_t tfull0 = smem_u32(bars + 2 * STAGES);     // [2] accumulator ready
-  const uint32_t tempty0 = smem_u32(bars + 2 * STAGES + 2);  // [2] accumulator drained (x8)
+  const uint32_t tempty0 = smem_u32(bars + 2 * STAGES + 2);  // [2] accumulator drained
   const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -913,7 +907,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 8);
+      mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);  // the epilogue warps of both CTAs
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -1148,6 +1142,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         uses ^= 1u << acc;
         tc_fence_after();
         const int n0 = u.tn * BN;
+        // the 32-column chunks of this warp
+        const int c_first = int(warp - 2) / 4 * (BN / 64), c_last = c_first + BN / 64;
         if (MT == 1) {
           for (int ks = u.kb0 + sk.seg; ks < u.kb1; ks += sk.seg) {
             const int a = acc ^ 1;
@@ -1158,7 +1154,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uses ^= 1u << a;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = c_first; c < c_last; ++c) {
               if (n0 + c * 32 >= ep.N) break;
               uint32_t r[32], t[32];
               tmem_ld32(lane_base + uint32_t(a * BN + c * 32), t);
@@ -1178,21 +1174,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int g = 0; g < u.mt; ++g) {
           const int row = u.row0 + g * PM + int(rank) * BM + int(quad * 32 + lane);
           const uint32_t taddr = lane_base + uint32_t((MT == 2 ? g : acc) * BN);
-          // this warp's 32 x 256 of a partial tile: 16-byte pieces in the order [piece of a
-          // row][row], so a warp's accesses are whole 512-byte runs
-          const size_t part_off = (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
-          // the pairs that hold part of this tile: first (its last share) to last
-          int first = sc.cluster, last = sc.cluster;
-          bool mine = true;
           if (u.ts >= 0 && (u.kb0 > 0 || u.kb1 < sc.num_kb)) {
-            const int64_t it0 = int64_t(u.ts) * sc.num_kb;
-            first = int(it0 / sc.W);
-            last = int((it0 + sc.num_kb - 1) / sc.W);
-            float* dst = sk.partials +
-                         (size_t(sc.cluster) * 2 + (sc.cluster == first ? 1 : 0)) * (2 * 128 * BN) +
-                         part_off;
+            // Part of a tile along K: leave the sums for linear_finish_kernel, in 16-byte
+            // pieces in the order [piece of a row][row], so a warp's accesses are whole
+            // 512-byte runs. A pair's share holds two partial tiles at most: slot 1 for the
+            // tile whose first k-block it has, slot 0 for the one it only goes on with.
+            float* dst = sk.partials + (size_t(sc.cluster) * 2 + (u.kb0 == 0 ? 1 : 0)) * (2 * 128 * BN) +
+                         (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = c_first; c < c_last; ++c) {
               if (n0 + c * 32 >= ep.N) break;
               __syncwarp();
               uint32_t r[32];
@@ -1208,49 +1198,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                                      __uint_as_float(r[4 * q + 3])));
               }
             }
-            __threadfence();
-            __syncwarp();
-            int is_last = 0;
-            if (lane == 0)
-              is_last = arrive_is_last(sk.flags + (size_t(u.ts) * 2 + rank) * 4 + quad, sk.epoch,
-                                       last - first + 1);
-            mine = __shfl_sync(0xffffffffu, is_last, 0) != 0;
-            __threadfence();
-          }
-          if (!mine) continue;
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < BN / 32; ++c) {
-            const int col0 = n0 + c * 32;
-            if (col0 >= ep.N) break;
-            __syncwarp();
-            float v[32];
-            if (first == last) {
+            for (int c = c_first; c < c_last; ++c) {
+              const int col0 = n0 + c * 32;
+              if (col0 >= ep.N) break;
+              __syncwarp();
               uint32_t r[32];
               tmem_ld32(taddr + uint32_t(c * 32), r);
               tmem_ld_wait(r);
+              float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 2
-              for (int c2 = first; c2 <= last; ++c2) {
-                const float4* p4 = reinterpret_cast<const float4*>(
-                    sk.partials + (size_t(c2) * 2 + (c2 == first ? 1 : 0)) * (2 * 128 * BN) +
-                    part_off + c * 1024);
-                if (row < ep.M) {
-#pragma unroll
-                  for (int q = 0; q < 8; ++q) {
-                    const float4 pv = __ldcg(p4 + 32 * q);
-                    v[4 * q] += pv.x;
-                    v[4 * q + 1] += pv.y;
-                    v[4 * q + 2] += pv.z;
-                    v[4 * q + 3] += pv.w;
-                  }
-                }
-              }
+              linear_epilogue32<OP == kOpF16>(ep, row, col0, v, ss);
             }
-            linear_epilogue32<OP == kOpF16>(ep, row, col0, v, ss);
           }
         }
         release(acc);
@@ -1380,6 +1341,102 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// ---------------------------------------------------------------- split tiles of kEpiLinear
+// The tiles that were split along K: sums of the pairs' partial tiles, in the pairs' order, and
+// the epilogue. A kernel of its own and not, as the other kinds have it, the pair with the
+// tile's first k-block: nothing waits inside a launch, whatever else runs on the GPU, and the
+// sums are spread over all SMs (one pair reading five partial tiles of a 333 x 2504 x 5120
+// product took 45 of its 57 us).
+struct Split {
+  int num_m, num_n, num_kb, dp_tiles, W, mt, group;  // as in Sched and SkParams
+};
+
+// Block: 32 rows x 32 columns of a split tile.
+template <bool F16>
+__global__ void __launch_bounds__(256)
+    linear_finish_kernel(const __grid_constant__ LinearEpi e, int M, int N, const Split s,
+                         const float* partials) {
+  __shared__ float tile[32][36];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the products' launch is complete
+  const int c = int(blockIdx.x) & 7, slice = int(blockIdx.x >> 3) & 7, ts = int(blockIdx.x >> 6);
+  const int64_t it0 = int64_t(ts) * s.num_kb;
+  const int first = int(it0 / s.W), last = int((it0 + s.num_kb - 1) / s.W);
+  if (first == last) return;  // computed whole by one pair
+  int tm, tn;
+  tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
+  const int row0 = (tm * s.mt + ts % s.mt) * PM + slice * 32;
+  const int col0 = tn * BN + c * 32;
+  if (row0 >= M || col0 >= N) return;
+  const int r = int(threadIdx.x) & 31, q = int(threadIdx.x) >> 5;  // row, piece of 4 columns
+  const size_t at = size_t(slice) * (32 * BN) + c * 1024 + threadIdx.x * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = first; k <= last; ++k) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(
+        partials + (size_t(k) * 2 + (k == first ? 1 : 0)) * (2 * 128 * BN) + at));
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  *reinterpret_cast<float4*>(&tile[r][4 * q]) = sum;
+  __syncthreads();
+  // now a warp has four rows, a lane one column
+  const int col = col0 + r;
+  if (col >= N) return;
+  auto load = [&](const void* p, int64_t i) {
+    const uint16_t x = static_cast<const uint16_t*>(p)[i];
+    return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(uint32_t(x) << 16);
+  };
+  auto store = [&](void* p, int64_t i, float x) {
+    static_cast<uint16_t*>(p)[i] = F16 ? __half_as_ushort(__float2half_rn(x))
+                                       : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  };
+  const float bias = e.bias != nullptr ? load(e.bias, col) : 0.f;
+  float v[4], z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 4 * q + i;
+    v[i] = tile[4 * q + i][r] + bias;
+    z[i] = e.mul != nullptr && row < M ? load(e.mul, int64_t(row) * e.ld_mul + col) : 0.f;
+    if (e.pre != nullptr && row < M) store(e.pre, int64_t(row) * e.ld_pre + col, v[i]);
+  }
+  if (e.mul != nullptr)
+    act_grad_apply(e.act, v, z);
+  else
+    act_apply(e.act, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 4 * q + i;
+    if (row >= M) break;
+    if (e.resid != nullptr)
+      v[i] += e.resid_f32 ? static_cast<const float*>(e.resid)[row * e.ld_resid + col]
+                          : load(e.resid, row * e.ld_resid + col);
+    if (e.y32 != nullptr) {
+      float* y = e.y32 + row * e.ldy + col;
+      *y = e.accumulate ? *y + v[i] : v[i];
+    } else {
+      store(e.y16, row * e.ldy + col, v[i]);
+    }
+  }
+}
+
+cudaError_t launch_linear_finish(bool f16, const LinearEpi& e, int M, int N, const Split& s,
+                                 int tiles, const float* partials, cudaStream_t stream) {
+  // launched while the products still run, so that only its wait lies between the two
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles) * 64, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return f16 ? cudaLaunchKernelEx(&cfg, linear_finish_kernel<true>, e, M, N, s, partials)
+             : cudaLaunchKernelEx(&cfg, linear_finish_kernel<false>, e, M, N, s, partials);
+}
+
 // Process-wide launch counter for the stream-K flags, seeded so that a stale flag left in
 // a reused buffer by an earlier process is not taken for this launch's.
 uint64_t next_epoch() {
@@ -1397,8 +1454,9 @@ uint64_t next_epoch() {
 // with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6 of a chain of fp32 fused multiply-adds.
 // A 16-bit result rounds at 2^-9 and needs none of that.
 constexpr int kLinearSegment = 16;
-// kEpiLinear: k-blocks that a share of a split tile has at least.
-constexpr int kLinearMinBlocks = 4;
+// kEpiLinear: k-blocks that a share of a split tile has at least, and that splitting has to
+// save at least.
+constexpr int kLinearMinBlocks = 4, kLinearMinGain = 16;
 // Stream-K tiles of a two-M-tile launch: at most this many pairs share one tile along K.
 constexpr int kSkMaxSplit = 16;
 
@@ -1406,7 +1464,7 @@ template <int KIND, int OP, int LAYOUT = kKK, int MT = 1>
 cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, int N, int K,
                         const EpiParams& ep, int num_sms, int* status, uint64_t limit_ns,
                         void* sk_scratch, cudaStream_t stream) {
-  constexpr size_t SMEM_BYTES = Geo<MT>::SMEM_BYTES;
+  constexpr size_t SMEM_BYTES = Geo<MT, Warps<KIND>::EPI>::SMEM_BYTES;
   static PerDeviceInit setup;  // per device: shared-memory opt-in and co-resident pairs
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1414,7 +1472,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(Warps<KIND>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -1464,19 +1522,25 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
     }
     const int64_t iters = int64_t(sk.sk_tiles) * num_kb;
     sk.W = int((iters + sk_pairs - 1) / sk_pairs);
+    if (KIND == kEpiLinear && MT == 1 && sk.W + kLinearMinGain > 2 * num_kb) {
+      sk.sk_tiles = 0;
+      sk.dp_tiles = units;
+      sk.W = 0;
+    }
     sk.partials = static_cast<float*>(sk_scratch);
     sk.flags = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(sk_scratch) +
                                            size_t(kSkMaxClusters) * kSkPartialBytes);
     sk.epoch = next_epoch();
   }
   if (KIND == kEpiLinear) {
-    // Fewer tiles than pairs: all of them are split along K, over as many pairs as have at
-    // least kLinearMinBlocks k-blocks each.
+    // Fewer tiles than pairs: all of them are split along K, evenly over the pairs. The
+    // partial sums cost a second launch, so a split has to take kLinearMinGain k-blocks at
+    // least off the longest share.
     if (sk_scratch != nullptr && MT == 1 && units < max_clusters && max_clusters <= kSkMaxClusters) {
       const int64_t iters = int64_t(units) * num_kb;
       int64_t w = (iters + max_clusters - 1) / max_clusters;
       if (w < kLinearMinBlocks) w = kLinearMinBlocks;
-      if (w < num_kb) {
+      if (w + kLinearMinGain <= num_kb) {
         sk.W = int(w);
         sk.sk_tiles = units;
         sk.dp_tiles = 0;
@@ -1484,8 +1548,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
       }
     }
     sk.partials = static_cast<float*>(sk_scratch);
-    sk.flags = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(sk_scratch) + kLinearPartialBytes);
-    if (sk.sk_tiles > 0) sk.epoch = next_epoch();
+    sk.flags = nullptr;
     sk.seg = ep.lin.y32 != nullptr ? kLinearSegment : num_kb;
   }
   EpiParams e = ep;
@@ -1493,8 +1556,12 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   e.N = N;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA, tmB, K, e, sk, status,
-                            limit_ns);
+  const cudaError_t launched = cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA,
+                                                  tmB, K, e, sk, status, limit_ns);
+  if (KIND != kEpiLinear || launched != cudaSuccess || sk.sk_tiles == 0) return launched;
+  const Split split{(M + MT * PM - 1) / (MT * PM), (N + BN - 1) / BN, num_kb, sk.dp_tiles, sk.W,
+                    MT, kGroupM / MT};
+  return launch_linear_finish(OP == kOpF16, ep.lin, M, N, split, sk.sk_tiles, sk.partials, stream);
 }
 
 // Two M tiles per unit for the K-major GEMMs whose M spans at least two 256-row tiles and

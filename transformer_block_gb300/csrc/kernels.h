@@ -161,14 +161,10 @@ constexpr size_t kSkPartialBytes = size_t(2) * 128 * 256 * 4;  // one pair tile,
 constexpr size_t kSkFlagBytes = size_t(2) * 4 * 8;             // 2 CTAs x 4 warps x u64
 constexpr size_t kSkScratchBytes = size_t(kSkMaxClusters) * (kSkPartialBytes + kSkFlagBytes);
 
-// kEpiLinear's work space. Here no pair waits for another one: every pair that computed part
-// of a tile along K leaves its partial sums, and whichever arrives last adds them up in the
-// pairs' order and finishes the tile. A pair's share of the iterations has two partial tiles
-// at most (its first and its last). A tile's counter words hold the launch's epoch and the
-// arrivals, and the last to arrive clears its word, so the words need no preparation.
-constexpr size_t kLinearPartialBytes = size_t(kSkMaxClusters) * 2 * kSkPartialBytes;
-constexpr size_t kLinearCounterBytes = size_t(kSkMaxClusters) * 2 * 8 * 8;  // 8 warps a tile
-constexpr size_t kLinearScratchBytes = kLinearPartialBytes + kLinearCounterBytes;
+// kEpiLinear's work space: the partial sums of tiles that several pairs compute, two for every
+// pair (its share of the iterations starts and ends inside a tile). A second launch adds them
+// up in a fixed order; nothing in the space needs preparation.
+constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * 2 * kSkPartialBytes;
 
 size_t gemm_smem_bytes();
 // op: the type of A and B (K % 64 == 0, K % 128 == 0 for kOpE4m3). sk_scratch

@@ -845,7 +845,7 @@ pb_status check_linear_scratch(const void* scratch, size_t bytes) {
 
 // Columns whose row sums are taken at once: their partial sums fit the partial tiles' region.
 constexpr int64_t kSumCols = 131072;
-static_assert(size_t(kSumCols) * pb::kSumBlocks * 4 <= pb::kLinearPartialBytes, "row sums");
+static_assert(size_t(kSumCols) * pb::kSumBlocks * 4 <= pb::kLinearScratchBytes, "row sums");
 
 // Layer 0 reads bf16 x, the last layer writes y (bf16, or fp32 when y_f32); in between
 // the residual stream alternates between the fp32 buffers res0 and res1.
