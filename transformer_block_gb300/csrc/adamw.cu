@@ -106,6 +106,13 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// To 2^-23; exact rounding would cost more instructions than all else of a value's step.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The last values of a tensor, fewer than 8: element by element, zero behind the end.
 template <class T>
 __device__ __forceinline__ void load_tail(const T* p, int n, float (&f)[8]) {
@@ -212,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, 4)
     c1 = -1.f / expm1f(k * st.log_beta1);
     c2 = -1.f / expm1f(k * st.log_beta2);
   }
+  const float root2 = sqrtf(c2);
   for (int64_t i = blockIdx.x; i < tab.chunks; i += gridDim.x) {
     const int64_t chunk = tab.chunks - 1 - i;
     const Tensor& t = tab.t[find_tensor(tab, chunk)];
@@ -233,21 +241,21 @@ __global__ void __launch_bounds__(THREADS, 4)
       load_any(static_cast<const float*>(t.v) + at, n, v);
     }
     const float keep = lr * t.decay;
+    float r[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float ge = g[e] * gs;
       m[e] = st.beta1 * m[e] + st.one_minus_beta1 * ge;
       v[e] = st.beta2 * v[e] + st.one_minus_beta2 * ge * ge;
-      const float up = (m[e] * c1) / (sqrtf(v[e] * c2) + st.eps);
+      r[e] = sqrt_approx(v[e]);
+      const float up = __fdividef(m[e] * c1, r[e] * root2 + st.eps);
       p[e] = p[e] - keep * p[e] - lr * up;
     }
     store_any(static_cast<P*>(t.param) + at, n, p);
     if (t.copy != nullptr) store_any(t.copy + at, n, p);
     if (EIGHT) {
       store_codes<false>(static_cast<uint8_t*>(t.m) + at, t.m_scale + block, n, m);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = sqrtf(v[e]);
-      store_codes<true>(static_cast<uint8_t*>(t.v) + at, t.v_scale + block, n, v);
+      store_codes<true>(static_cast<uint8_t*>(t.v) + at, t.v_scale + block, n, r);
     } else {
       store_any(static_cast<float*>(t.m) + at, n, m);
       store_any(static_cast<float*>(t.v) + at, n, v);
@@ -260,40 +268,58 @@ __global__ void __launch_bounds__(THREADS, 4)
 constexpr int kNormBlocks = 1024;  // partial sums of one launch
 
 // Sum of squares of the block's chunks. fp32 within a thread (some thousand values at most
-// per 2^33 gradients), double between threads and blocks, in a fixed order.
+// per 2^33 gradients), double between threads and blocks, in a fixed order. A thread has the
+// loads of four pieces of 8 gradients in flight.
+constexpr int NORM_PIECES = 4;
+constexpr int NORM_CHUNK = CHUNK * NORM_PIECES;
+
+__device__ __forceinline__ void add_squares(const uint4& u, float (&s)[4], float) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] += __uint_as_float(w[e]) * __uint_as_float(w[e]);
+}
+__device__ __forceinline__ void add_squares(const uint4& u, float (&s)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+    s[e] += lo * lo + hi * hi;
+  }
+}
+
 template <int CAP, class G>
 __global__ void __launch_bounds__(THREADS) square_sum_kernel(
     const __grid_constant__ Table<CAP> tab, double* partials) {
   __shared__ double red[THREADS / 32];
+  constexpr int LOADS = NORM_PIECES * PER_THREAD * int(sizeof(G)) / 16;  // 16 bytes each
+  constexpr int VEC = 16 / int(sizeof(G));
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     const Tensor& t = tab.t[find_tensor(tab, chunk)];
-    const int64_t at = (chunk - t.first_chunk) * CHUNK + int64_t(threadIdx.x) * PER_THREAD;
-    if (at >= t.n) continue;
-    const int n = int(min(int64_t(PER_THREAD), t.n - at));
-    float g[8];
+    const int64_t at = (chunk - t.first_chunk) * NORM_CHUNK;
     const G* src = static_cast<const G*>(t.grad) + at;
-    if (n == 8) {
+    const int64_t left = t.n - at;
+    if (left >= NORM_CHUNK) {
       // plain loads: the step reads the gradients again
-      if constexpr (sizeof(G) == 4) {
-        const float4 a = reinterpret_cast<const float4*>(src)[0];
-        const float4 b = reinterpret_cast<const float4*>(src)[1];
-        g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
-        g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint4 u[LOADS];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[2 * e] = __uint_as_float(w[e] << 16);
-          g[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      for (int i = 0; i < LOADS; ++i)
+        u[i] = reinterpret_cast<const uint4*>(src)[i * THREADS + threadIdx.x];
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) add_squares(u[i], s, G{});
+    } else {
+      for (int i = 0; i < LOADS; ++i) {
+        const int64_t a = int64_t(i * THREADS + threadIdx.x) * VEC;
+        if (a + VEC <= left) {
+          add_squares(*reinterpret_cast<const uint4*>(src + a), s, G{});
+        } else {
+          for (int e = 0; e < VEC && a + e < left; ++e) {
+            const float g = as_float(src[a + e]);
+            s[e % 4] += g * g;
+          }
         }
       }
-    } else {
-      load_tail(src, n, g);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e % 4] += g[e] * g[e];
   }
   double d = (double(s[0]) + double(s[1])) + (double(s[2]) + double(s[3]));
 #pragma unroll
@@ -353,7 +379,7 @@ pb_status sm_count(int* sms) {
 
 // The next tensors that have values, from `at` on, as a kernel's table.
 template <int CAP>
-void fill(Table<CAP>& tab, const pb_adamw_tensor* tensors, int count, int& at) {
+void fill(Table<CAP>& tab, const pb_adamw_tensor* tensors, int count, int& at, int chunk = CHUNK) {
   tab.count = 0;
   tab.chunks = 0;
   for (; at < count && tab.count < CAP; ++at) {
@@ -362,7 +388,7 @@ void fill(Table<CAP>& tab, const pb_adamw_tensor* tensors, int count, int& at) {
     Tensor& t = tab.t[tab.count++];
     t = Tensor{a.param, static_cast<__nv_bfloat16*>(a.param_copy), a.grad, a.m, a.v, a.m_scale,
                a.v_scale, a.n, tab.chunks, a.weight_decay};
-    tab.chunks += (a.n + CHUNK - 1) / CHUNK;
+    tab.chunks += (a.n + chunk - 1) / chunk;
   }
 }
 
@@ -586,11 +612,11 @@ pb_status pb_grad_norm(int32_t n_tensors, const pb_adamw_tensor* tensors, int32_
     cudaError_t e = cudaSuccess;
     if (n_tensors - at <= kFew) {
       Table<kFew> tab;
-      fill(tab, tensors, n_tensors, at);
+      fill(tab, tensors, n_tensors, at, NORM_CHUNK);
       if (tab.count > 0) e = launch(tab);
     } else {
       Table<kMany> tab;
-      fill(tab, tensors, n_tensors, at);
+      fill(tab, tensors, n_tensors, at, NORM_CHUNK);
       if (tab.count > 0) e = launch(tab);
     }
     if (e != cudaSuccess) return cuda_failed(e, "gradient norm launch");

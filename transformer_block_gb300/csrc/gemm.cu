@@ -1510,7 +1510,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   sk.dp_tiles = units;
   const int rem = units % clusters;
   if (sk_scratch != nullptr && clusters <= kSkMaxClusters && units > clusters && rem != 0 &&
-      num_kb >= 8) {
+      num_kb >= 8 && KIND != kEpiLinear) {
     int sk_pairs = clusters;
     if (MT == 1) {
       sk.sk_tiles = clusters + rem;
@@ -1522,29 +1522,24 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
     }
     const int64_t iters = int64_t(sk.sk_tiles) * num_kb;
     sk.W = int((iters + sk_pairs - 1) / sk_pairs);
-    if (KIND == kEpiLinear && MT == 1 && sk.W + kLinearMinGain > 2 * num_kb) {
-      sk.sk_tiles = 0;
-      sk.dp_tiles = units;
-      sk.W = 0;
-    }
     sk.partials = static_cast<float*>(sk_scratch);
     sk.flags = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(sk_scratch) +
                                            size_t(kSkMaxClusters) * kSkPartialBytes);
     sk.epoch = next_epoch();
   }
   if (KIND == kEpiLinear) {
-    // Fewer tiles than pairs: all of them are split along K, evenly over the pairs. The
-    // partial sums cost a second launch, so a split has to take kLinearMinGain k-blocks at
-    // least off the longest share.
-    if (sk_scratch != nullptr && MT == 1 && units < max_clusters && max_clusters <= kSkMaxClusters) {
-      const int64_t iters = int64_t(units) * num_kb;
+    // The tiles of the last wave are split along K, evenly over the pairs, where that takes
+    // kLinearMinGain k-blocks at least off the wave: the partial sums cost a second launch.
+    const int tiles = MT * (units < max_clusters ? units : rem);
+    if (sk_scratch != nullptr && max_clusters <= kSkMaxClusters && tiles > 0) {
+      const int64_t iters = int64_t(tiles) * num_kb;
       int64_t w = (iters + max_clusters - 1) / max_clusters;
       if (w < kLinearMinBlocks) w = kLinearMinBlocks;
-      if (w + kLinearMinGain <= num_kb) {
+      if (w + kLinearMinGain <= MT * num_kb) {
         sk.W = int(w);
-        sk.sk_tiles = units;
-        sk.dp_tiles = 0;
-        clusters = int((iters + w - 1) / w);
+        sk.sk_tiles = tiles;
+        sk.dp_tiles = units - tiles / MT;
+        if (units < max_clusters) clusters = int((iters + w - 1) / w);
       }
     }
     sk.partials = static_cast<float*>(sk_scratch);

@@ -189,16 +189,20 @@ cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& 
                                cudaStream_t stream);
 
 // ---------------------------------------------------------------- linear (linear.cu)
-// Few rows of A: y as kEpiLinear's, D = A * B^T with B [N, K] (ldb) or, b_mn, stored [K, N].
+// Few rows of A: y as kEpiLinear's, D = A * B^T with B [N, K] or, b_mn, stored [K, N]. tmA: A
+// in boxes of 64 columns x few_box_rows(M) rows; tmB in boxes of 64 columns x
+// few_box_rows_b(b_mn) rows. scratch: kLinearScratchBytes, or null.
 constexpr int kFewRows = 32;
+constexpr int kFewColsKN = 256, kFewKsKN = 64, kFewColsNK = 128, kFewKsNK = 128;
+constexpr int few_box_rows(int M) { return (M + 7) / 8 * 8; }
+constexpr int few_box_rows_b(bool b_mn) { return b_mn ? kFewKsKN : kFewColsNK; }
 struct FewParams {
   int M, N, K;
-  const void* a;
-  const void* b;
-  int64_t lda, ldb;
   LinearEpi epi;
 };
-cudaError_t launch_linear_few(OpType op, bool b_mn, const FewParams& p, cudaStream_t stream);
+cudaError_t launch_linear_few(OpType op, bool b_mn, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                              const FewParams& p, void* scratch, int* status, uint64_t limit_ns,
+                              cudaStream_t stream);
 // out = dy * act'(pre), rows of cols 16-bit values.
 cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,
                                 int64_t ld_dy, const void* pre, int64_t ld_pre, void* out,

@@ -3,17 +3,17 @@
 //
 // Few tokens (a decoding step): y = resid + act(x W + b) for up to 32 rows of x is bound by
 // reading W once. A tile of the GEMM would hold 256 rows of A for it and leave most SMs
-// without a tile, so here a warp takes 64 output features and a share of K, loads W straight
-// into registers, 16 bytes a lane and 4 KB a warp in flight, and multiplies with mma.sync (a
-// register operand needs no shared memory, and the product's rate does not matter: 32 rows
-// cost an eighth of what the loads leave time for). W takes the instruction's 16-row side and
-// x its 8-column side. The sum over k may run in any order as long as both operands keep the
-// same one, so lane (g, t) of the fragments takes the eight consecutive k from 8 t on:
-//   W stored [N, K]: 16 bytes of row g and of row g + 8 of a tile are its fragments;
-//   W stored [K, N]: eight k-rows' 16 bytes at column 8 g hold columns (2 r, 2 r + 1) of
-//     8 g as tile r's rows g and g + 8; byte permutes pair two k-rows' halves.
-// The eight warps of a CTA take every eighth step of 32 k, the CTAs of a cluster equal parts of
-// K; partial sums meet in shared memory, then over the cluster, in a fixed order.
+// without a tile, so here one CTA an SM takes an equal share of all (tile of output features,
+// stage of k) steps, whatever tiles it cuts. One thread streams W (and x) through a ring of
+// five shared-memory stages of 32 KB of W by TMA without a pause between tiles: four times the
+// bytes in flight that the memory's latency asks for. Eight warps take 16 or 32 features each
+// and multiply with mma.sync, W on the instruction's 16-row side and x on its 8-column side
+// (the product's rate does not matter: 32 rows cost an eighth of the time that the loads
+// take). ldmatrix reads both operands from the 128-byte swizzled boxes, transposing W where it
+// is stored [K, N]; rows, columns and k outside the matrices arrive as zeros. A stage is 256
+// features x 64 k of a [K, N] matrix and 128 x 128 of an [N, K] one, so that memory is read in
+// runs of 512 or 256 bytes. Tiles that a CTA has whole are finished by it; of the others it
+// leaves partial sums, which a second launch adds up in the CTAs' order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -80,18 +80,26 @@ __device__ __forceinline__ uint16_t from_float(float x) {
 
 // ------------------------------------------------------------------ few tokens
 
-constexpr int FEW_WARPS = 8, FEW_THREADS = 32 * FEW_WARPS;
-constexpr int FEW_COLS = 64;      // output features of a CTA
-constexpr int FEW_STEP = 32;      // k of one step of a warp
-constexpr int FEW_PITCH = 68;     // floats a token's row of partial sums takes: no bank twice
+// Stages (of 32 KB of W, 0.7 us of an SM's share of the memory's rate) that equal shares have to
+// save for their second launch.
+constexpr int kFewMinGain = 4;
+constexpr int FEW_WARPS = 8;                       // multiplying warps
+constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1);  // and the producer's
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 u;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p));
-  return u;
-}
+template <int NT, bool KN>
+struct FewGeo {
+  static constexpr int COLS = KN ? kFewColsKN : kFewColsNK;  // output features of a tile
+  static constexpr int KS = KN ? kFewKsKN : kFewKsNK;        // k of a stage
+  static constexpr int RT = COLS / (16 * FEW_WARPS);         // 16-feature rows of a warp
+  static constexpr int W_BYTES = COLS * KS * 2;
+  static constexpr int X_BYTES = 8 * NT * 128;  // a box of 64 k x 8 NT rows of x
+  static constexpr int STAGE_BYTES = W_BYTES + KS / 64 * X_BYTES;
+  static constexpr int STAGES = 5;
+  // per warp, for the results: [8 NT tokens][16 RT features] floats
+  static constexpr int OUT_BYTES = 8 * NT * 16 * RT * 4;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + FEW_WARPS * OUT_BYTES;
+  static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
+};
 
 // Up to 8 values of 16 bits, the first n of them; zero behind.
 __device__ __forceinline__ uint4 ld_part(const uint16_t* p, int n) {
@@ -105,251 +113,317 @@ __device__ __forceinline__ uint4 ld_part(const uint16_t* p, int n) {
 }
 
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
   if (F16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, "
         "%7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// Four 8 x 8 matrices of 16-bit values; lane 8 i + j gives the address of row j of matrix i.
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
-// One step's operands of a lane: eight 16-byte pieces of W, one of x for every 8 tokens.
-template <int NT>
-struct FewStep {
-  uint4 w[8];
-  uint4 x[NT];
-};
+// 16-byte piece j of row r of a box whose rows are 128 bytes, in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(uint32_t box, int r, int j) {
+  return box + uint32_t(r * 128 + ((j ^ (r & 7)) << 4));
+}
 
-template <int NT, bool KN>
-__device__ __forceinline__ void few_load(const FewParams& p, int n0, int k0, int g, int t,
-                                         FewStep<NT>& s) {
-  const uint16_t* b = static_cast<const uint16_t*>(p.b);
-  const uint16_t* a = static_cast<const uint16_t*>(p.a);
-  const int k = k0 + 8 * t;
-  if (n0 + FEW_COLS <= p.N && k0 + FEW_STEP <= p.K) {
+// The results at (m + i step, n) from their sums z[i], those below M. All that is read is
+// loaded before anything is stored (the compiler has to take a store for a write to it).
+template <bool F16, int COUNT>
+__device__ __forceinline__ void finish_values(const LinearEpi& e, int M, int m, int step, int n,
+                                              float bias, float (&z)[COUNT]) {
+  float a[COUNT], r[COUNT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      s.w[i] = KN ? ld_stream(b + int64_t(k + i) * p.ldb + n0 + 8 * g)
-                  : ld_stream(b + int64_t(n0 + 8 * i + g) * p.ldb + k);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (KN) {
-        const int n = k + i < p.K ? p.N - (n0 + 8 * g) : 0;
-        s.w[i] = n > 0 ? ld_part(b + int64_t(k + i) * p.ldb + n0 + 8 * g, n)
-                       : make_uint4(0, 0, 0, 0);
-      } else {
-        const int row = n0 + 8 * i + g;
-        const int n = row < p.N ? p.K - k : 0;
-        s.w[i] = n > 0 ? ld_part(b + int64_t(row) * p.ldb + k, n) : make_uint4(0, 0, 0, 0);
-      }
-    }
+  for (int i = 0; i < COUNT; ++i) {
+    const int64_t row = m + i * step;
+    const bool live = row < M;
+    a[i] = e.mul != nullptr && live
+               ? to_float<F16>(static_cast<const uint16_t*>(e.mul)[row * e.ld_mul + n])
+               : 0.f;
+    r[i] = e.resid == nullptr || !live ? 0.f
+           : e.resid_f32 ? static_cast<const float*>(e.resid)[row * e.ld_resid + n]
+                         : to_float<F16>(static_cast<const uint16_t*>(e.resid)[row * e.ld_resid + n]);
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int m = 8 * j + g;
-    const int n = m < p.M ? p.K - k : 0;
-    s.x[j] = n > 0 ? ld_part(a + int64_t(m) * p.lda + k, n) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < COUNT; ++i) {
+    const int64_t row = m + i * step;
+    if (row >= M) break;
+    const float pre = z[i] + bias;
+    if (e.pre != nullptr)
+      static_cast<uint16_t*>(e.pre)[row * e.ld_pre + n] = from_float<F16>(pre);
+    float y = e.mul != nullptr ? pre * act_grad(e.act, a[i]) : act_value(e.act, pre);
+    if (e.resid != nullptr) y += r[i];
+    if (e.y32 != nullptr)
+      e.y32[row * e.ldy + n] = y;
+    else
+      static_cast<uint16_t*>(e.y16)[row * e.ldy + n] = from_float<F16>(y);
   }
 }
+template <bool F16>
+__device__ __forceinline__ float bias_at(const LinearEpi& e, int n, int N) {
+  return e.bias != nullptr && n < N ? to_float<F16>(static_cast<const uint16_t*>(e.bias)[n]) : 0.f;
+}
 
+// CTA c does steps [c W, (c + 1) W) of the tiles' steps (`total` stages each) in order.
+// partials: [CTA][2 slots][8 NT][COLS]; slot 1 for the tile whose first stage the CTA has.
 template <int NT, bool KN, bool F16>
-__device__ __forceinline__ void few_multiply(const FewStep<NT>& s, float (&acc)[4][NT][4]) {
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+    few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+               const __grid_constant__ FewParams p, int total, int64_t all, int64_t W,
+               float* partials, int* status, uint64_t limit_ns) {
+  using G = FewGeo<NT, KN>;
+  constexpr int STAGES = G::STAGES, RT = G::RT, KS = G::KS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * STAGES];
+  __shared__ int abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, FEW_WARPS);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const WaitCtl wc{&abort_flag, status, limit_ns};
+  int64_t it = int64_t(blockIdx.x) * W;
+  const int64_t it_end = min(all, it + W);
+  int tile = int(it / total), k = int(it - int64_t(tile) * total);
+  int stage = 0;
+  uint32_t phase = 0;
+
+  if (warp == FEW_WARPS) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      uint32_t last_par[STAGES];
+      uint32_t used = 0;
+      for (; it < it_end; ++it) {
+        if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, wc, 1)) break;
+        const uint32_t w = smem_u32(smem + size_t(stage) * G::STAGE_BYTES);
+        const uint32_t x = w + G::W_BYTES, bar = full0 + 8 * stage;
+        const int n0 = tile * G::COLS, k0 = k * KS;
+        mbar_arrive_expect_tx(bar, G::STAGE_BYTES);
+        if (KN) {  // boxes of 64 features x 64 k
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // k 4 h .. 4 h + 3 of the lane's eight
+          for (int i = 0; i < G::COLS / 64; ++i)
+            tma_load_2d(w + i * (G::W_BYTES / (G::COLS / 64)), &tm_w, bar, n0 + 64 * i, k0);
+        } else {   // boxes of 64 k x 128 features
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {  // 16 features
-      uint32_t a0, a1, a2, a3;
-      if (KN) {
-        auto word = [&](int row) {
-          const uint4& u = s.w[row];
-          return r == 0 ? u.x : r == 1 ? u.y : r == 2 ? u.z : u.w;
-        };
-        const uint32_t w0 = word(4 * h), w1 = word(4 * h + 1), w2 = word(4 * h + 2),
-                       w3 = word(4 * h + 3);
-        a0 = __byte_perm(w0, w1, 0x5410);
-        a1 = __byte_perm(w0, w1, 0x7632);
-        a2 = __byte_perm(w2, w3, 0x5410);
-        a3 = __byte_perm(w2, w3, 0x7632);
-      } else {
-        const uint4 &lo = s.w[2 * r], &hi = s.w[2 * r + 1];
-        a0 = h ? lo.z : lo.x;
-        a1 = h ? hi.z : hi.x;
-        a2 = h ? lo.w : lo.y;
-        a3 = h ? hi.w : hi.y;
+          for (int i = 0; i < KS / 64; ++i)
+            tma_load_2d(w + i * (G::W_BYTES / (KS / 64)), &tm_w, bar, k0 + 64 * i, n0);
+        }
+#pragma unroll
+        for (int i = 0; i < KS / 64; ++i)
+          tma_load_2d(x + i * G::X_BYTES, &tm_x, bar, k0 + 64 * i, 0);
+        last_par[stage] = phase;
+        used |= 1u << stage;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (++k == total) {
+          k = 0;
+          ++tile;
+        }
       }
+      // every copy has landed before the CTA leaves
+      for (int i = 0; i < STAGES; ++i)
+        if (used & (1u << i))
+          mbar_wait_drain(full0 + 8 * i, last_par[i],
+                          limit_ns > kDrainFloorNs ? limit_ns : kDrainFloorNs);
+    }
+    __syncwarp();
+    return;
+  }
+  // ---------------------------------------------------------------- products
+  const int mi = lane >> 3, mr = lane & 7;  // the matrix and row this lane addresses
+  const int g = lane >> 2, t = lane & 3;
+  float* out = reinterpret_cast<float*>(smem + STAGES * G::STAGE_BYTES + warp * G::OUT_BYTES);
+  while (it < it_end) {
+    const int k_first = k;
+    const int k_last = int(min(int64_t(total), k + (it_end - it)));
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        mma16816<F16>(acc[r][j], a0, a1, a2, a3, h ? s.x[j].z : s.x[j].x,
-                      h ? s.x[j].w : s.x[j].y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][j][e] = 0.f;
+    for (; k < k_last; ++k) {
+      if (!mbar_wait_warp(full0 + 8 * stage, phase, wc, 2)) return;
+      const uint32_t w = smem_u32(smem + size_t(stage) * G::STAGE_BYTES);
+#pragma unroll
+      for (int h = 0; h < KS / 32; ++h) {  // 32 k
+        const uint32_t x = w + G::W_BYTES + (h >> 1) * G::X_BYTES;
+        uint32_t b[NT][4];  // x: 8 tokens x 32 k
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          ldmatrix4<false>(swizzled(x, 8 * j + mr, 4 * (h & 1) + mi), b[j]);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)  // 16 k
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int f = 16 * (RT * warp + r);  // first feature
+            uint32_t a[4];
+            if (KN)  // a box for every 64 features; its rows are k, pieces 8 features
+              ldmatrix4<true>(swizzled(w + (f >> 6) * (G::W_BYTES / (G::COLS / 64)),
+                                       32 * h + 16 * hh + 8 * (mi >> 1) + mr,
+                                       (f & 63) / 8 + (mi & 1)),
+                              a);
+            else     // a box for every 64 k; its rows are features, pieces 8 k
+              ldmatrix4<false>(swizzled(w + (h >> 1) * (G::W_BYTES / (KS / 64)),
+                                        f + 8 * (mi & 1) + mr,
+                                        4 * (h & 1) + 2 * hh + (mi >> 1)),
+                               a);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              mma16816<F16>(acc[r][j], a, b[j][2 * hh], b[j][2 * hh + 1]);
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
+    // the warp's results [token][feature], so that lanes go along the features
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int m = 8 * j + 2 * t, f = 16 * r + g;
+        out[m * (16 * RT) + f] = acc[r][j][0];
+        out[(m + 1) * (16 * RT) + f] = acc[r][j][1];
+        out[m * (16 * RT) + f + 8] = acc[r][j][2];
+        out[(m + 1) * (16 * RT) + f + 8] = acc[r][j][3];
+      }
+    __syncwarp();
+    const bool whole = k_first == 0 && k_last == total;
+    const int f = lane % (16 * RT), nf = 16 * RT * warp + f;
+    const int n = tile * G::COLS + nf;
+    float* part = partials + (size_t(blockIdx.x) * 2 + (k_first == 0 ? 1 : 0)) * (8 * NT * G::COLS);
+    constexpr int STEP = 2 / RT;  // tokens the warp's lanes take at a time
+    const int m0 = lane / (16 * RT);
+    if (!whole) {
+#pragma unroll 4
+      for (int m = m0; m < p.M; m += STEP) __stcg(part + m * G::COLS + nf, out[m * (16 * RT) + f]);
+    } else if (n < p.N) {
+      const float bias = bias_at<F16>(p.epi, n, p.N);
+      for (int m = m0; m < p.M; m += 4 * STEP) {
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = out[min(m + i * STEP, 8 * NT - 1) * (16 * RT) + f];
+        finish_values<F16>(p.epi, p.M, m, STEP, n, bias, z);
+      }
+    }
+    __syncwarp();
+    it += k_last - k_first;
+    k = 0;
+    ++tile;
   }
 }
 
-// grid: tiles of FEW_COLS features x cluster size; steps: k-steps of one CTA's part of K.
+// The tiles that several CTAs share: a thread adds up one value.
 template <int NT, bool KN, bool F16>
-__global__ void __launch_bounds__(FEW_THREADS, 2)
-    few_kernel(const __grid_constant__ FewParams p, int splits, int steps) {
-  extern __shared__ float red[];  // [FEW_WARPS][8 NT][FEW_PITCH]
-  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int rank = int(blockIdx.x) % splits;
-  const int n0 = int(blockIdx.x) / splits * FEW_COLS;
-  const int total = (p.K + FEW_STEP - 1) / FEW_STEP;
-  const int end = min(total, (rank + 1) * steps);
-  float acc[4][NT][4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[r][j][e] = 0.f;
-  int k = rank * steps + warp;
-  if constexpr (NT <= 2) {  // the next step's loads are in flight during a step's products
-    FewStep<NT> now, next;
-    if (k < end) few_load<NT, KN>(p, n0, k * FEW_STEP, g, t, now);
-    for (; k < end; k += FEW_WARPS) {
-      if (k + FEW_WARPS < end)
-        few_load<NT, KN>(p, n0, (k + FEW_WARPS) * FEW_STEP, g, t, next);
-      few_multiply<NT, KN, F16>(now, acc);
-      now = next;
-    }
-  } else {  // the sums take the registers for that; sixteen warps cover one another's loads
-    FewStep<NT> now;
-    for (; k < end; k += FEW_WARPS) {
-      few_load<NT, KN>(p, n0, k * FEW_STEP, g, t, now);
-      few_multiply<NT, KN, F16>(now, acc);
-    }
-  }
-  // partial sums [token][feature] of every warp
-  float* mine = red + warp * (8 * NT * FEW_PITCH);
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int m = 8 * j + 2 * t;
-      const int f0 = KN ? 8 * g + 2 * r : 16 * r + g, f1 = KN ? f0 + 1 : f0 + 8;
-      mine[m * FEW_PITCH + f0] = acc[r][j][0];
-      mine[(m + 1) * FEW_PITCH + f0] = acc[r][j][1];
-      mine[m * FEW_PITCH + f1] = acc[r][j][2];
-      mine[(m + 1) * FEW_PITCH + f1] = acc[r][j][3];
-    }
-  __syncthreads();
-  const int f = int(threadIdx.x) % FEW_COLS, m_first = int(threadIdx.x) / FEW_COLS;
-  constexpr int ROWS = FEW_THREADS / FEW_COLS;
-  if (splits > 1) {
-    // the CTA's sums replace warp 0's; then every CTA of the cluster finishes some tokens
-#pragma unroll
-    for (int m = m_first; m < 8 * NT; m += ROWS) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < FEW_WARPS; ++w) s += red[(w * 8 * NT + m) * FEW_PITCH + f];
-      red[m * FEW_PITCH + f] = s;  // read and written by this thread alone
-    }
-    cluster_sync();
-  }
-  const int n = n0 + f;
-  const LinearEpi& e = p.epi;
-  const uint32_t base = smem_u32(red);
-  for (int m = m_first + (splits > 1 ? rank * ROWS : 0); m < p.M;
-       m += ROWS * (splits > 1 ? splits : 1)) {
-    float z = 0.f;
-    if (splits > 1) {
-      for (int r = 0; r < splits; ++r)
-        z += ld_cluster_f32(mapa_shared(base + uint32_t(m * FEW_PITCH + f) * 4u, uint32_t(r)));
-    } else {
-#pragma unroll
-      for (int w = 0; w < FEW_WARPS; ++w) z += red[(w * 8 * NT + m) * FEW_PITCH + f];
-    }
-    if (n >= p.N) continue;
-    if (e.bias != nullptr) z += to_float<F16>(static_cast<const uint16_t*>(e.bias)[n]);
-    if (e.pre != nullptr)
-      static_cast<uint16_t*>(e.pre)[int64_t(m) * e.ld_pre + n] = from_float<F16>(z);
-    float y;
-    if (e.mul != nullptr)
-      y = z * act_grad(e.act, to_float<F16>(
-                                  static_cast<const uint16_t*>(e.mul)[int64_t(m) * e.ld_mul + n]));
-    else
-      y = act_value(e.act, z);
-    if (e.resid != nullptr) {
-      const int64_t at = int64_t(m) * e.ld_resid + n;
-      y += e.resid_f32 ? static_cast<const float*>(e.resid)[at]
-                       : to_float<F16>(static_cast<const uint16_t*>(e.resid)[at]);
-    }
-    if (e.y32 != nullptr)
-      e.y32[int64_t(m) * e.ldy + n] = y;
-    else
-      static_cast<uint16_t*>(e.y16)[int64_t(m) * e.ldy + n] = from_float<F16>(y);
-  }
-  if (splits > 1) cluster_sync();  // no CTA leaves while its sums may still be read
+__global__ void __launch_bounds__(256)
+    few_finish_kernel(const __grid_constant__ FewParams p, int total, int64_t W,
+                      const float* partials) {
+  using G = FewGeo<NT, KN>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the products' launch is complete
+  const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
+  if (n >= p.N) return;
+  const int tile = n / G::COLS;
+  const int64_t it0 = int64_t(tile) * total;
+  const int first = int(it0 / W), last = int((it0 + total - 1) / W);
+  if (first == last) return;
+  const float bias = bias_at<F16>(p.epi, n, p.N);
+  float z[1] = {0.f};
+#pragma unroll 8
+  for (int c = first; c <= last; ++c)
+    z[0] += __ldcg(partials + (size_t(c) * 2 + (c == first ? 1 : 0)) * (8 * NT * G::COLS) +
+                m * G::COLS + n % G::COLS);
+  finish_values<F16>(p.epi, p.M, m, 1, n, bias, z);
 }
 
 template <int NT, bool KN, bool F16>
-cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
-  constexpr int SMEM = FEW_WARPS * 8 * NT * FEW_PITCH * 4;
+cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const FewParams& p,
+                       float* scratch, int* status, uint64_t limit_ns, cudaStream_t stream) {
+  using G = FewGeo<NT, KN>;
   static PerDeviceInit setup;  // per device: shared-memory opt-in; value: number of SMs
   int sms = 0;
   const cudaError_t err = per_device_init(
       setup,
       [](int dev, int* out) {
         const cudaError_t e = cudaFuncSetAttribute(
-            few_kernel<NT, KN, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            few_kernel<NT, KN, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
         if (e != cudaSuccess) return e;
         return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
       },
       &sms);
   if (err != cudaSuccess) return err;
-  const int tiles = (p.N + FEW_COLS - 1) / FEW_COLS;
-  const int total = (p.K + FEW_STEP - 1) / FEW_STEP;
-  // CTAs of a cluster that share a tile's K: as many as give the shortest sequence of waves
-  // over the two resident CTAs an SM, with a hundredth of a tile's time for each more, and two
-  // steps of every warp at least
-  const int slots = 2 * sms;
-  int splits = 1;
-  double best = 1e30;
-  for (int s = 1; s <= 8 && (s == 1 || total >= s * 2 * FEW_WARPS); ++s) {
-    const double cost = double((int64_t(tiles) * s + slots - 1) / slots) / s + 0.01 * s;
-    if (cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
-  const int steps = (total + splits - 1) / splits;
+  const int64_t tiles = (p.N + G::COLS - 1) / G::COLS;
+  const int total = (p.K + G::KS - 1) / G::KS;
+  const int64_t all = tiles * total;
+  // whole tiles, or equal shares where these are shorter by what the second launch costs
+  int64_t W = (tiles + sms - 1) / sms * total;
+  const int64_t even = (all + sms - 1) / sms;
+  if (scratch != nullptr && even + kFewMinGain <= W &&
+      kLinearScratchBytes >= size_t(sms) * 2 * 8 * NT * G::COLS * 4)
+    W = even;
+  const unsigned grid = unsigned((all + W - 1) / W);
+  few_kernel<NT, KN, F16><<<grid, FEW_THREADS, G::SMEM, stream>>>(tm_x, tm_w, p, total, all, W,
+                                                                scratch, status, limit_ns);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || W % total == 0) return e;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(splits);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles) * unsigned(splits), 1, 1);
-  cfg.blockDim = dim3(FEW_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.gridDim = dim3(unsigned((p.N + 255) / 256), unsigned(p.M), 1);
+  cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<NT, KN, F16>, p, splits, steps);
+  return cudaLaunchKernelEx(&cfg, few_finish_kernel<NT, KN, F16>, p, total, W,
+                            static_cast<const float*>(scratch));
 }
 
 template <bool KN, bool F16>
-cudaError_t launch_few_rows(const FewParams& p, cudaStream_t stream) {
-  if (p.M <= 8) return launch_few<1, KN, F16>(p, stream);
-  if (p.M <= 16) return launch_few<2, KN, F16>(p, stream);
-  if (p.M <= 24) return launch_few<3, KN, F16>(p, stream);
-  return launch_few<4, KN, F16>(p, stream);
+cudaError_t launch_few_rows(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const FewParams& p,
+                            float* scratch, int* status, uint64_t limit_ns, cudaStream_t stream) {
+  switch (few_box_rows(p.M)) {
+    case 8: return launch_few<1, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
+    case 16: return launch_few<2, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
+    case 24: return launch_few<3, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
+    default: return launch_few<4, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
+  }
 }
 
 // ------------------------------------------------------------------ activation backward
@@ -428,17 +502,23 @@ __global__ void __launch_bounds__(256)
   const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (c >= cols) return;
   float s = 0.f;
-  for (int k = 0; k < parts; ++k) s += partials[int64_t(k) * cols + c];
+#pragma unroll 16
+  for (int k = 0; k < parts; ++k) s += __ldcg(partials + int64_t(k) * cols + c);
   out[c] = accumulate ? out[c] + s : s;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_few(OpType op, bool b_mn, const FewParams& p, cudaStream_t stream) {
+cudaError_t launch_linear_few(OpType op, bool b_mn, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                              const FewParams& p, void* scratch, int* status, uint64_t limit_ns,
+                              cudaStream_t stream) {
   if (p.M < 1 || p.M > kFewRows || p.N < 1 || p.K < 1) return cudaErrorInvalidValue;
+  float* s = static_cast<float*>(scratch);
   if (op == kOpF16)
-    return b_mn ? launch_few_rows<true, true>(p, stream) : launch_few_rows<false, true>(p, stream);
-  return b_mn ? launch_few_rows<true, false>(p, stream) : launch_few_rows<false, false>(p, stream);
+    return b_mn ? launch_few_rows<true, true>(tmA, tmB, p, s, status, limit_ns, stream)
+                : launch_few_rows<false, true>(tmA, tmB, p, s, status, limit_ns, stream);
+  return b_mn ? launch_few_rows<true, false>(tmA, tmB, p, s, status, limit_ns, stream)
+              : launch_few_rows<false, false>(tmA, tmB, p, s, status, limit_ns, stream);
 }
 
 cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,

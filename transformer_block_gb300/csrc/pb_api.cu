@@ -1529,8 +1529,13 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
     ep.lin.y16 = a.y;
   ep.lin.ldy = a.ldy;
   if (a.m <= pb::kFewRows) {
-    pb::FewParams f{a.m, a.n, a.k, a.x, a.w, a.ldx, a.ldw, ep.lin};
-    PB_CUDA(pb::launch_linear_few(op, in_out, f, st), "linear launch");
+    const pb::FewParams f{a.m, a.n, a.k, ep.lin};
+    CUtensorMap tx, tw;
+    s = make_map_2d(&tx, a.x, x.rows, x.cols, x.ld, pb::few_box_rows(a.m), op);
+    if (s == PB_OK) s = make_map_2d(&tw, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(in_out), op);
+    if (s != PB_OK) return s;
+    PB_CUDA(pb::launch_linear_few(op, in_out, tx, tw, f, scratch, status, kDefaultLimitNs, st),
+            "linear launch");
     return PB_OK;
   }
   CUtensorMap tx, tw;
@@ -1618,8 +1623,14 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     ep.lin.y16 = a.dx;
     ep.lin.ldy = a.lddx;
     if (a.m <= pb::kFewRows) {
-      pb::FewParams f{a.m, a.k, a.n, a.dy, a.w, a.lddy, a.ldw, ep.lin};
-      PB_CUDA(pb::launch_linear_few(op, !in_out, f, st), "linear backward (dx) launch");
+      const pb::FewParams f{a.m, a.k, a.n, ep.lin};
+      CUtensorMap ta, tb;
+      s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::few_box_rows(a.m), op);
+      if (s == PB_OK)
+        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(!in_out), op);
+      if (s != PB_OK) return s;
+      PB_CUDA(pb::launch_linear_few(op, !in_out, ta, tb, f, scratch, status, kDefaultLimitNs, st),
+              "linear backward (dx) launch");
     } else {
       CUtensorMap ta, tb;
       s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::kGemmBoxRows, op);
