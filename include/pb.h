@@ -546,7 +546,7 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
  * dx is then the gradient of pre, dy w^T * activation'(pre), ready as that layer's dy.
  * accumulate != 0 adds dw and db to what is there (dx is always overwritten); with m = 0 they
  * are zero. The gradient of the residual is dy itself. ld*, pointers, scratch and status as
- * in pb_linear; scratch is needed where db is wanted. Results overlap nothing else. */
+ * in pb_linear. Results overlap nothing else. */
 typedef struct pb_linear_grads {
   int32_t m, n, k;
   int32_t dtype;

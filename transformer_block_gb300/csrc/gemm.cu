@@ -804,13 +804,15 @@ struct Sched {
   int cluster, clusters;
   int dp_tiles, sk_tiles, W;
   int mt, group;             // M tiles per unit; units per rasterisation group
+  int split;                 // kEpiLinear: pairs of a stream-K tile, each with W k-blocks of it
 };
 
 struct SkParams {
   int dp_tiles, sk_tiles, W;
-  float* partials;  // [kSkMaxClusters][2][128][256]; kEpiLinear: [.. clusters][2 slots] of it
+  float* partials;  // [kSkMaxClusters][2][128][256]; 
   uint64_t* flags;  // [kSkMaxClusters][2][4]; kEpiLinear: none
   uint64_t epoch;
+  int split;        // kEpiLinear: see Sched
   int seg;          // kEpiLinear, one M tile: k-blocks summed at a time in one accumulator
 };
 
@@ -850,6 +852,15 @@ struct UnitIter {
       tile_coords(t, s.num_m, s.num_n, s.group, tm, tn);
       u = Unit{tm * s.mt * 2 * kGemmBM, tn, s.mt, -1, 0, s.num_kb};
       t += s.clusters;
+      return true;
+    }
+    if (s.split > 0) {  // one part of one tile: pair split * ts + i has k-blocks [i W, (i + 1) W)
+      const int ts = s.cluster / s.split, kb0 = (s.cluster - ts * s.split) * s.W;
+      if (it < 0 || ts >= s.sk_tiles) return false;
+      it = -1;
+      tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
+      u = Unit{(tm * s.mt + ts % s.mt) * 2 * kGemmBM, tn, 1, ts, kb0,
+               min(s.num_kb, kb0 + s.W)};
       return true;
     }
     if (it >= it_end) return false;
@@ -945,6 +956,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   sc.dp_tiles = sk.dp_tiles;
   sc.sk_tiles = sk.sk_tiles;
   sc.W = sk.W;
+  sc.split = KIND == kEpiLinear ? sk.split : 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -1020,20 +1032,16 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
       bool ok = true;
       UnitIter ui(sc);
       Unit u;
-      uint32_t uses = 0;  // kEpiLinear: parity of each accumulator's uses so far
       while (ok && ui.next(sc, u)) {
         if (KIND == kEpiLinear && MT == 1) {
-          // The unit's first sk.seg k-blocks go to accumulator acc, each further segment to
-          // the other one, from which the epilogue warps add it to the first; the next unit
-          // starts in the other one.
+          // every sk.seg k-blocks of the unit to the other accumulator; the epilogue warps
+          // add them up
           for (int ks = u.kb0; ok && ks < u.kb1; ks += sk.seg) {
-            const int a = ks == u.kb0 ? acc : acc ^ 1;
             const int ke = min(u.kb1, ks + sk.seg);
-            if (!mbar_wait(tempty0 + 8 * a, ((uses >> a) & 1u) ^ 1u, wc, 2)) {
+            if (!mbar_wait(tempty0 + 8 * acc, acc_par ^ 1, wc, 2)) {
               ok = false;
               break;
             }
-            uses ^= 1u << a;
             tc_fence_after();
             for (int kb = ks; kb < ke; ++kb) {
               if (!mbar_wait(full0 + 8 * stage, phase, wc, 3)) {
@@ -1048,7 +1056,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
                                       : sdesc_kmajor_sw128(sa + A_BYTES);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_f16kind_ss_pair(tmem_base + uint32_t(a * BN), da + kStepA * k,
+                mma_f16kind_ss_pair(tmem_base + uint32_t(acc * BN), da + kStepA * k,
                                     db + kStepB * k, idesc, (kb > ks) || k > 0);
               mma_commit_pair(empty0 + 8 * stage, 0x3);
               if (++stage == STAGES) {
@@ -1056,9 +1064,11 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
                 phase ^= 1;
               }
             }
-            if (ok) mma_commit_pair(tfull0 + 8 * a, 0x3);
+            if (!ok) break;
+            mma_commit_pair(tfull0 + 8 * acc, 0x3);
+            acc ^= 1;
+            if (acc == 0) acc_par ^= 1;
           }
-          acc ^= 1;
           continue;
         }
         if (!mbar_wait(tempty0 + 8 * acc, acc_par ^ 1, wc, 2)) break;
@@ -1124,7 +1134,6 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
     UnitIter ui(sc);
     Unit u;
     bool ok = true;
-    uint32_t uses = 0;  // kEpiLinear, MT = 1: parity of each accumulator's uses so far
     const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
     auto release = [&](int a) {  // warp-wide: accumulator a may be written again
       tc_fence_before();
@@ -1138,38 +1147,48 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
     };
     while (ok && ui.next(sc, u)) {
       if (KIND == kEpiLinear) {
-        if (!mbar_wait_warp(tfull0 + 8 * acc, MT == 1 ? (uses >> acc) & 1u : acc_par, wc, 4)) break;
-        uses ^= 1u << acc;
-        tc_fence_after();
         const int n0 = u.tn * BN;
         // the 32-column chunks of this warp
         const int c_first = int(warp - 2) / 4 * (BN / 64), c_last = c_first + BN / 64;
-        if (MT == 1) {
-          for (int ks = u.kb0 + sk.seg; ks < u.kb1; ks += sk.seg) {
-            const int a = acc ^ 1;
-            if (!mbar_wait_warp(tfull0 + 8 * a, (uses >> a) & 1u, wc, 4)) {
+        if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
+        tc_fence_after();
+        if (MT == 1 && u.kb1 - u.kb0 > sk.seg) {
+          // Several segments: a lane keeps the sums of its row's columns in registers, so the
+          // products go on in the other accumulator, and leaves the total in the last one's.
+          float sum[BN / 64][32];
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+          for (int ks = u.kb0;;) {
+#pragma unroll
+            for (int c = 0; c < BN / 64; ++c) {
+              uint32_t r[32];
+              tmem_ld32(lane_base + uint32_t(acc * BN + (c_first + c) * 32), r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+            }
+            ks += sk.seg;
+            if (ks >= u.kb1) break;
+            release(acc);
+            acc ^= 1;
+            if (acc == 0) acc_par ^= 1;
+            if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) {
               ok = false;
               break;
             }
-            uses ^= 1u << a;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = c_first; c < c_last; ++c) {
-              if (n0 + c * 32 >= ep.N) break;
-              uint32_t r[32], t[32];
-              tmem_ld32(lane_base + uint32_t(a * BN + c * 32), t);
-              tmem_ld32(lane_base + uint32_t(acc * BN + c * 32), r);
-              tmem_ld_wait(r);
-              tmem_ld_wait_regs(t);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(t[i]));
-              tmem_st32(lane_base + uint32_t(acc * BN + c * 32), r);
-            }
-            tmem_st_wait();
-            release(a);
           }
           if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[c][i]);
+            tmem_st32(lane_base + uint32_t(acc * BN + (c_first + c) * 32), r);
+          }
+          tmem_st_wait();
         }
         for (int g = 0; g < u.mt; ++g) {
           const int row = u.row0 + g * PM + int(rank) * BM + int(quad * 32 + lane);
@@ -1177,9 +1196,8 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
           if (u.ts >= 0 && (u.kb0 > 0 || u.kb1 < sc.num_kb)) {
             // Part of a tile along K: leave the sums for linear_finish_kernel, in 16-byte
             // pieces in the order [piece of a row][row], so a warp's accesses are whole
-            // 512-byte runs. A pair's share holds two partial tiles at most: slot 1 for the
-            // tile whose first k-block it has, slot 0 for the one it only goes on with.
-            float* dst = sk.partials + (size_t(sc.cluster) * 2 + (u.kb0 == 0 ? 1 : 0)) * (2 * 128 * BN) +
+            // 512-byte runs.
+            float* dst = sk.partials + size_t(sc.cluster) * (2 * 128 * BN) +
                          (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
 #pragma unroll 1
             for (int c = c_first; c < c_last; ++c) {
@@ -1215,10 +1233,12 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
           }
         }
         release(acc);
-        if (MT == 1)
+        if (MT == 1) {
           acc ^= 1;
-        else
+          if (acc == 0) acc_par ^= 1;
+        } else {
           acc_par ^= 1;
+        }
         continue;
       }
       if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
@@ -1348,7 +1368,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
 // sums are spread over all SMs (one pair reading five partial tiles of a 333 x 2504 x 5120
 // product took 45 of its 57 us).
 struct Split {
-  int num_m, num_n, num_kb, dp_tiles, W, mt, group;  // as in Sched and SkParams
+  int num_m, num_n, dp_tiles, split, mt, group;  // as in Sched
 };
 
 // Block: 32 rows x 32 columns of a split tile.
@@ -1359,9 +1379,6 @@ __global__ void __launch_bounds__(256)
   __shared__ float tile[32][36];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the products' launch is complete
   const int c = int(blockIdx.x) & 7, slice = int(blockIdx.x >> 3) & 7, ts = int(blockIdx.x >> 6);
-  const int64_t it0 = int64_t(ts) * s.num_kb;
-  const int first = int(it0 / s.W), last = int((it0 + s.num_kb - 1) / s.W);
-  if (first == last) return;  // computed whole by one pair
   int tm, tn;
   tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
   const int row0 = (tm * s.mt + ts % s.mt) * PM + slice * 32;
@@ -1371,9 +1388,9 @@ __global__ void __launch_bounds__(256)
   const size_t at = size_t(slice) * (32 * BN) + c * 1024 + threadIdx.x * 4;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = first; k <= last; ++k) {
+  for (int k = 0; k < s.split; ++k) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(
-        partials + (size_t(k) * 2 + (k == first ? 1 : 0)) * (2 * 128 * BN) + at));
+        partials + (size_t(ts) * s.split + k) * (2 * 128 * BN) + at));
     sum.x += v.x;
     sum.y += v.y;
     sum.z += v.z;
@@ -1452,11 +1469,15 @@ uint64_t next_epoch() {
 // sum goes on in fp32 additions that round to nearest. The tensor core cuts its sums off
 // instead of rounding them, which leaves 1.0e-6 of relative error at K = 1024 and, growing
 // with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6 of a chain of fp32 fused multiply-adds.
-// A 16-bit result rounds at 2^-9 and needs none of that.
-constexpr int kLinearSegment = 16;
-// kEpiLinear: k-blocks that a share of a split tile has at least, and that splitting has to
-// save at least.
-constexpr int kLinearMinBlocks = 4, kLinearMinGain = 16;
+// Reading an accumulator costs the products about 0.4 us (2048 x 2048 x 8192: 45.1 us in one
+// chain, 46.9 in segments of 32, 48.5 of 16). A 16-bit result rounds at 2^-9 and needs none
+// of that.
+constexpr int kLinearSegment = 12;
+// kEpiLinear: k-blocks (0.28 us each) that a share of a split tile has at least, and that
+// splitting has to save at least: partial sums and second launch cost 5 to 10 us (saving 53 of
+// 80 took 333 x 2504 x 5120 from 27.9 to 19.6 us, saving 16 of 32 took 256 x 8192 x 2048 from
+// 15.4 to 19.2 us).
+constexpr int kLinearMinBlocks = 4, kLinearMinGain = 28;
 // Stream-K tiles of a two-M-tile launch: at most this many pairs share one tile along K.
 constexpr int kSkMaxSplit = 16;
 
@@ -1528,18 +1549,20 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
     sk.epoch = next_epoch();
   }
   if (KIND == kEpiLinear) {
-    // The tiles of the last wave are split along K, evenly over the pairs, where that takes
-    // kLinearMinGain k-blocks at least off the wave: the partial sums cost a second launch.
+    // The tiles of the last wave are split along K, each over the same number of pairs, where
+    // that takes kLinearMinGain k-blocks at least off the wave: the partial sums cost a second
+    // launch.
     const int tiles = MT * (units < max_clusters ? units : rem);
     if (sk_scratch != nullptr && max_clusters <= kSkMaxClusters && tiles > 0) {
-      const int64_t iters = int64_t(tiles) * num_kb;
-      int64_t w = (iters + max_clusters - 1) / max_clusters;
+      const int most = max_clusters / tiles;  // pairs for each tile
+      int w = most > 1 ? (num_kb + most - 1) / most : num_kb;
       if (w < kLinearMinBlocks) w = kLinearMinBlocks;
-      if (w + kLinearMinGain <= MT * num_kb) {
-        sk.W = int(w);
+      if (w + kLinearMinGain <= num_kb) {
+        sk.W = w;
+        sk.split = (num_kb + w - 1) / w;
         sk.sk_tiles = tiles;
         sk.dp_tiles = units - tiles / MT;
-        if (units < max_clusters) clusters = int((iters + w - 1) / w);
+        if (units < max_clusters) clusters = tiles * sk.split;
       }
     }
     sk.partials = static_cast<float*>(sk_scratch);
@@ -1554,8 +1577,8 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   const cudaError_t launched = cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA,
                                                   tmB, K, e, sk, status, limit_ns);
   if (KIND != kEpiLinear || launched != cudaSuccess || sk.sk_tiles == 0) return launched;
-  const Split split{(M + MT * PM - 1) / (MT * PM), (N + BN - 1) / BN, num_kb, sk.dp_tiles, sk.W,
-                    MT, kGroupM / MT};
+  const Split split{(M + MT * PM - 1) / (MT * PM), (N + BN - 1) / BN, sk.dp_tiles, sk.split, MT,
+                    kGroupM / MT};
   return launch_linear_finish(OP == kOpF16, ep.lin, M, N, split, sk.sk_tiles, sk.partials, stream);
 }
 

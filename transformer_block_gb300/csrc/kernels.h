@@ -161,10 +161,9 @@ constexpr size_t kSkPartialBytes = size_t(2) * 128 * 256 * 4;  // one pair tile,
 constexpr size_t kSkFlagBytes = size_t(2) * 4 * 8;             // 2 CTAs x 4 warps x u64
 constexpr size_t kSkScratchBytes = size_t(kSkMaxClusters) * (kSkPartialBytes + kSkFlagBytes);
 
-// kEpiLinear's work space: the partial sums of tiles that several pairs compute, two for every
-// pair (its share of the iterations starts and ends inside a tile). A second launch adds them
-// up in a fixed order; nothing in the space needs preparation.
-constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * 2 * kSkPartialBytes;
+// kEpiLinear's work space: the partial sums of tiles that several pairs compute, one for every
+// pair. A second launch adds them up in a fixed order; nothing in it needs preparation.
+constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * kSkPartialBytes;
 
 size_t gemm_smem_bytes();
 // op: the type of A and B (K % 64 == 0, K % 128 == 0 for kOpE4m3). sk_scratch
@@ -207,11 +206,10 @@ cudaError_t launch_linear_few(OpType op, bool b_mn, const CUtensorMap& tmA, cons
 cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,
                                 int64_t ld_dy, const void* pre, int64_t ld_pre, void* out,
                                 int64_t ld_out, cudaStream_t stream);
-// out[c] (+)= sum over rows of m[r, c] (16-bit values, 16-byte rows, any cols), through
-// partials [kSumBlocks][cols] fp32, in a fixed order.
-constexpr int kSumBlocks = 64;
+// out[c] (+)= sum over rows of m[r, c] (16-bit values, 16-byte rows, any cols), in a fixed
+// order.
 cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols, int64_t ld,
-                            float* partials, float* out, bool accumulate, cudaStream_t stream);
+                            float* out, bool accumulate, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention (swa.cu)
 struct SwaParams {

@@ -144,6 +144,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // 16-byte piece j of row r of a box whose rows are 128 bytes, in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t box, int r, int j) {
   return box + uint32_t(r * 128 + ((j ^ (r & 7)) << 4));
@@ -459,52 +465,72 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ sums over the rows
 
-// Block (x, y): columns [256 x, 256 x + 256), the y-th of gridDim.y parts of the rows; 32
-// threads across (8 columns each), 8 rows at a time.
+// Cluster: 64 columns; its CTAs: equal parts of the rows; 8 threads across (16 bytes each), 32
+// rows at a time, four such loads of a thread in flight. Sums over a CTA's threads, then over
+// the cluster in distributed shared memory, in a fixed order.
+constexpr int SUM_COLS = 64;
 template <bool F16>
 __global__ void __launch_bounds__(256)
-    row_sum_kernel(const uint16_t* m, int64_t rows, int64_t cols, int64_t ld, float* partials) {
-  __shared__ float red[8][32][9];
-  const int tx = int(threadIdx.x) & 31, ty = int(threadIdx.x) >> 5;
-  const int64_t c = int64_t(blockIdx.x) * 256 + tx * 8;
-  const int64_t per = (rows + gridDim.y - 1) / gridDim.y;
-  const int64_t r0 = int64_t(blockIdx.y) * per, r1 = min(rows, r0 + per);
+    row_sum_kernel(const uint16_t* m, int64_t rows, int64_t cols, int64_t ld, int parts, float* out,
+                   bool accumulate) {
+  __shared__ float red[8][SUM_COLS];
+  const int tx = int(threadIdx.x) & 7, ty = int(threadIdx.x) >> 3;
+  const int rank = int(blockIdx.x) % parts;
+  const int64_t c0 = int64_t(blockIdx.x) / parts * SUM_COLS, c = c0 + tx * 8;
+  const int64_t per = (rows + parts - 1) / parts;
+  const int64_t r0 = rank * per, r1 = min(rows, r0 + per);
   const int n = int(max(int64_t(0), min(int64_t(8), cols - c)));
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
-  if (n > 0)
-    for (int64_t r = r0 + ty; r < r1; r += 8) {
-      const uint4 u = ld_part(m + r * ld + c, n);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  auto add = [&](const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[2 * i] += to_float<F16>(uint16_t(w[i]));
-        s[2 * i + 1] += to_float<F16>(uint16_t(w[i] >> 16));
-      }
+    for (int i = 0; i < 4; ++i) {
+      s[2 * i] += to_float<F16>(uint16_t(w[i]));
+      s[2 * i + 1] += to_float<F16>(uint16_t(w[i] >> 16));
     }
+  };
+  if (n > 0) {
+    const uint16_t* p = m + c;
+    int64_t r = r0 + ty;
+    for (; r + 96 < r1; r += 128) {
+      uint4 u[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[ty][tx][i] = s[i];
-  __syncthreads();
-  // thread k of the block: column k
-  const int64_t col = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (col < cols) {
-    float v = 0.f;
+      for (int i = 0; i < 4; ++i) u[i] = ld_part(p + (r + 32 * i) * ld, n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += red[k][threadIdx.x / 8][threadIdx.x % 8];
-    partials[int64_t(blockIdx.y) * cols + col] = v;
+      for (int i = 0; i < 4; ++i) add(u[i]);
+    }
+    for (; r < r1; r += 32) add(ld_part(p + r * ld, n));
   }
-}
-
-__global__ void __launch_bounds__(256)
-    row_sum_final_kernel(const float* partials, int parts, int64_t cols, float* out,
-                         bool accumulate) {
-  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.f;
-#pragma unroll 16
-  for (int k = 0; k < parts; ++k) s += __ldcg(partials + int64_t(k) * cols + c);
-  out[c] = accumulate ? out[c] + s : s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    for (int o = 8; o < 32; o <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+  if ((threadIdx.x & 31) < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[threadIdx.x >> 5][tx * 8 + i] = s[i];
+  }
+  __syncthreads();
+  float v = 0.f;
+  if (threadIdx.x < SUM_COLS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += red[k][threadIdx.x];
+  }
+  if (parts > 1) {
+    __syncthreads();
+    if (threadIdx.x < SUM_COLS) red[0][threadIdx.x] = v;
+    __syncthreads();
+    cluster_sync();
+    if (rank == 0 && threadIdx.x < SUM_COLS) {
+      v = 0.f;
+      for (int k = 0; k < parts; ++k)
+        v += ld_cluster_f32(mapa_shared(smem_u32(&red[0][threadIdx.x]), uint32_t(k)));
+    }
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its sums may still be read
+  }
+  if (rank == 0 && threadIdx.x < SUM_COLS && c0 + threadIdx.x < cols)
+    out[c0 + threadIdx.x] = accumulate ? out[c0 + threadIdx.x] + v : v;
 }
 
 }  // namespace
@@ -538,21 +564,26 @@ cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, 
 }
 
 cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols, int64_t ld,
-                            float* partials, float* out, bool accumulate, cudaStream_t stream) {
+                            float* out, bool accumulate, cudaStream_t stream) {
   if (rows < 1 || cols < 1) return cudaSuccess;
-  // 32 rows a part at least, and no more parts than kSumBlocks
-  const int64_t want = (rows + 31) / 32;
-  const unsigned parts = unsigned(want < kSumBlocks ? want : kSumBlocks);
-  const unsigned blocks = unsigned((cols + 255) / 256);
+  // up to eight CTAs share a cluster's rows, 128 rows each at least
+  const int parts = rows >= 1024 ? 8 : rows <= 128 ? 1 : int(rows / 128);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(parts);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((cols + SUM_COLS - 1) / SUM_COLS) * unsigned(parts), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   const auto* src = static_cast<const uint16_t*>(m);
-  if (op == kOpF16)
-    row_sum_kernel<true><<<dim3(blocks, parts), 256, 0, stream>>>(src, rows, cols, ld, partials);
-  else
-    row_sum_kernel<false><<<dim3(blocks, parts), 256, 0, stream>>>(src, rows, cols, ld, partials);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  row_sum_final_kernel<<<blocks, 256, 0, stream>>>(partials, int(parts), cols, out, accumulate);
-  return cudaGetLastError();
+  return op == kOpF16 ? cudaLaunchKernelEx(&cfg, row_sum_kernel<true>, src, rows, cols, ld, parts,
+                                           out, accumulate)
+                      : cudaLaunchKernelEx(&cfg, row_sum_kernel<false>, src, rows, cols, ld, parts,
+                                           out, accumulate);
 }
 
 }  // namespace pb

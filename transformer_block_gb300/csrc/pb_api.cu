@@ -843,10 +843,6 @@ pb_status check_linear_scratch(const void* scratch, size_t bytes) {
   return PB_OK;
 }
 
-// Columns whose row sums are taken at once: their partial sums fit the partial tiles' region.
-constexpr int64_t kSumCols = 131072;
-static_assert(size_t(kSumCols) * pb::kSumBlocks * 4 <= pb::kLinearScratchBytes, "row sums");
-
 // Layer 0 reads bf16 x, the last layer writes y (bf16, or fp32 when y_f32); in between
 // the residual stream alternates between the fp32 buffers res0 and res1.
 pb_status run_stack(pb_handle* const* layers, int32_t n, const void* x, void* y,
@@ -1582,8 +1578,6 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
   if (a.dw != nullptr) s = check_matrix(dw, "dw");
   if (s != PB_OK) return s;
   if (!aligned(a.db, 4)) return fail(PB_ERR_INVALID_ARG, "db must be 4-byte aligned");
-  if (a.db != nullptr && a.m > 0 && scratch == nullptr)
-    return fail(PB_ERR_WORKSPACE, "db needs scratch");
   const Matrix* outs[3] = {&dx, &dw, &db};
   const char* const names[3] = {"dx", "dw", "db"};
   const Matrix* all[8] = {&dy, &x, &w, &pre, &dx, &dw, &db, &work};
@@ -1607,12 +1601,9 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     }
     return PB_OK;
   }
-  for (int64_t c = 0; a.db != nullptr && c < a.n; c += kSumCols) {
-    const int64_t cols = a.n - c < kSumCols ? a.n - c : kSumCols;
-    PB_CUDA(pb::launch_row_sums(op, static_cast<const uint16_t*>(a.dy) + c, a.m, cols, a.lddy,
-                                static_cast<float*>(scratch), a.db + c, a.accumulate != 0, st),
+  if (a.db != nullptr)
+    PB_CUDA(pb::launch_row_sums(op, a.dy, a.m, a.n, a.lddy, a.db, a.accumulate != 0, st),
             "bias gradient launch");
-  }
   if (a.dx != nullptr) {
     // the contraction runs over n: dy and an [k, n] w are K-major
     EpiParams ep{};

@@ -20,8 +20,10 @@
 // first half and the chunk as far into their second half, so each access of the lanes of a
 // head is one run of 16 bytes a lane, and for pairs half a rotation apart both members sit in
 // one lane. A lane group takes one token and walks over its heads: sines and cosines are
-// computed once a token and a tensor, the next head's loads are in flight while a head is
-// worked on, and where there are few tokens the heads are split over more groups.
+// computed once a token and a tensor, and where there are few tokens the heads are split over
+// more groups. Three heads ahead of the one at work are on their way by asynchronous copies
+// into shared memory that only the lane itself reads back (no barrier): registers would hold
+// one.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -140,6 +142,27 @@ __device__ __forceinline__ void rotate(float* v, const float (&c)[8], const floa
   }
 }
 
+// The lane's ring of copies: [kRing][pieces][THREADS] 16-byte pieces, kRing - 1 heads ahead.
+constexpr int kRing = 4;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The oldest head's copies have landed.
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+}
+// A lane without values (a head whose chunks are no power of two) has zeros.
+__device__ __forceinline__ uint4 ring_read(uint32_t src, bool has_values) {
+  uint4 u;
+  if (!has_values) return make_uint4(0, 0, 0, 0);
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(src)
+               : "memory");
+  return u;
+}
+
 __device__ __forceinline__ float group_sum(float v, int lanes_log2) {
   for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -166,6 +189,7 @@ __device__ __forceinline__ Place place_of(const Params& p, const Job& j, unsigne
 
 template <bool ADJ>
 __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_constant__ Params p) {
+  __shared__ __align__(16) uint4 ring_mem[kRing * 2 * THREADS];
   const bool second = blockIdx.x >= p.job[0].blocks;
   const Job& j = p.job[second ? 1 : 0];
   const unsigned block = blockIdx.x - (second ? p.job[0].blocks : 0u);
@@ -177,11 +201,16 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
   chunk_offsets(p, u, lo, hi);
   const __nv_bfloat16* x = j.x.p + w.b * j.x.bs + w.s * j.x.ss;
   __nv_bfloat16* y = j.y.p + w.b * j.y.bs + w.s * j.y.ss;
-  uint4 n0 = {}, n1 = {};
-  if (live) {
-    n0 = *reinterpret_cast<const uint4*>(x + w.h0 * j.x.hs + lo);
-    n1 = *reinterpret_cast<const uint4*>(x + w.h0 * j.x.hs + hi);
-  }
+  const uint32_t ring = smem_u32(ring_mem) + threadIdx.x * 16;
+  auto fetch = [&](int h, int slot) {
+    if (live && h < w.h1) {
+      copy16(ring + (2 * slot) * (THREADS * 16), x + h * j.x.hs + lo);
+      copy16(ring + (2 * slot + 1) * (THREADS * 16), x + h * j.x.hs + hi);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(w.h0 + i, i);
   uint4 g0 = {}, g1 = {};
   if (j.gamma != nullptr && w.live) {
     g0 = __ldg(reinterpret_cast<const uint4*>(j.gamma + lo));
@@ -191,14 +220,12 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
   lane_angles<ADJ>(p, w.token, w.s, u, c, sn);
   // every group of the block makes the same number of steps, so its lanes meet in the sums
   for (int i = 0; i < j.per_split; ++i) {
-    const int h = w.h0 + i;
+    const int h = w.h0 + i, slot = i % kRing;
+    fetch(h + kRing - 1, (i + kRing - 1) % kRing);
+    copies_wait();
     float v[16];
-    unpack(n0, v);
-    unpack(n1, v + 8);
-    if (live && h + 1 < w.h1) {
-      n0 = *reinterpret_cast<const uint4*>(x + (h + 1) * j.x.hs + lo);
-      n1 = *reinterpret_cast<const uint4*>(x + (h + 1) * j.x.hs + hi);
-    }
+    unpack(ring_read(ring + (2 * slot) * (THREADS * 16), w.live), v);
+    unpack(ring_read(ring + (2 * slot + 1) * (THREADS * 16), w.live), v + 8);
     if (j.gamma != nullptr) {
       float sq = 0.f;
 #pragma unroll
@@ -223,6 +250,7 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
 // gamma_sum_kernel, so the result has the same bits on every run.
 template <bool ADJ>
 __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint4 ring_dyn[];  // [kRing][4][THREADS]
   __shared__ float red[THREADS / 32][kMaxDh];
   const bool second = blockIdx.x >= p.job[0].blocks;
   const Job& j = p.job[second ? 1 : 0];
@@ -248,27 +276,34 @@ __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_co
     const __nv_bfloat16* x = norm ? j.x.p + w.b * j.x.bs + w.s * j.x.ss : nullptr;
     const __nv_bfloat16* dy = j.dy.p + w.b * j.dy.bs + w.s * j.dy.ss;
     __nv_bfloat16* dx = j.y.p + w.b * j.y.bs + w.s * j.y.ss;
-    uint4 d0 = {}, d1 = {}, x0 = {}, x1 = {};
-    auto load = [&](int h) {
-      d0 = *reinterpret_cast<const uint4*>(dy + h * j.dy.hs + lo);
-      d1 = *reinterpret_cast<const uint4*>(dy + h * j.dy.hs + hi);
-      if (norm) {
-        x0 = *reinterpret_cast<const uint4*>(x + h * j.x.hs + lo);
-        x1 = *reinterpret_cast<const uint4*>(x + h * j.x.hs + hi);
+    const uint32_t ring = smem_u32(ring_dyn) + threadIdx.x * 16;
+    auto fetch = [&](int h, int slot) {
+      if (live && h < w.h1) {
+        const uint32_t at = ring + 4 * slot * (THREADS * 16);
+        copy16(at, dy + h * j.dy.hs + lo);
+        copy16(at + THREADS * 16, dy + h * j.dy.hs + hi);
+        if (norm) {
+          copy16(at + 2 * (THREADS * 16), x + h * j.x.hs + lo);
+          copy16(at + 3 * (THREADS * 16), x + h * j.x.hs + hi);
+        }
       }
+      copies_commit();
     };
-    if (live) load(w.h0);
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(w.h0 + i, i);
     float c[8], sn[8];
     lane_angles<ADJ>(p, w.token, w.s, u, c, sn);
     for (int i = 0; i < j.per_split; ++i) {
       const int h = w.h0 + i;
-      float d[16], v[16];
-      unpack(d0, d);
-      unpack(d1, d + 8);
-      unpack(x0, v);
-      unpack(x1, v + 8);
       const bool mine = live && h < w.h1;
-      if (live && h + 1 < w.h1) load(h + 1);
+      fetch(h + kRing - 1, (i + kRing - 1) % kRing);
+      copies_wait();
+      const uint32_t at = ring + 4 * (i % kRing) * (THREADS * 16);
+      float d[16], v[16];
+      unpack(ring_read(at, w.live), d);
+      unpack(ring_read(at + THREADS * 16, w.live), d + 8);
+      unpack(ring_read(at + 2 * (THREADS * 16), w.live), v);
+      unpack(ring_read(at + 3 * (THREADS * 16), w.live), v + 8);
       rotate<ADJ, true>(d, c, sn);
       if (norm) {
         float g[16];
@@ -475,6 +510,19 @@ pb_status fill_params(Params& p, const pb_rope* rope, int batch, int seq, float 
   std::copy(rope->section_end, rope->section_end + PB_ROPE_MAX_AXES, p.section_end);
   std::copy(rope->turns, rope->turns + p.rot / 2, p.turns);
   return PB_OK;
+}
+
+template <bool ADJ>
+cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
+  constexpr int SMEM = kRing * 4 * THREADS * 16;
+  static PerDeviceInit setup;  // per device: shared-memory opt-in
+  const cudaError_t e = per_device_init(setup, [](int, int*) {
+    return cudaFuncSetAttribute(qk_backward_kernel<ADJ>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  qk_backward_kernel<ADJ><<<grid, THREADS, SMEM, st>>>(p);
+  return cudaGetLastError();
 }
 
 // Splits the heads of a token over lane groups until `threads` threads have work.
@@ -720,11 +768,8 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
     gs.blocks[t] = j.blocks;
   }
   const unsigned grid = p.job[0].blocks + p.job[1].blocks;
-  if (rope->pairing == PB_ROPE_ADJACENT)
-    qk_backward_kernel<true><<<grid, THREADS, 0, st>>>(p);
-  else
-    qk_backward_kernel<false><<<grid, THREADS, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = rope->pairing == PB_ROPE_ADJACENT ? launch_backward<true>(p, grid, st)
+                                                    : launch_backward<false>(p, grid, st);
   if (e == cudaSuccess && (gs.out[0] != nullptr || gs.out[1] != nullptr)) {
     gamma_sum_kernel<<<dim3(unsigned(dh + 31) / 32, 2), dim3(32, 32), 0, st>>>(
         p.partials, dh, gs, accumulate != 0);

@@ -774,8 +774,6 @@ def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = 
         dw = _new_rows(*w_shape, torch.float32, dev, zero=accumulate)
     if bias and db is None:
         db = (torch.zeros if accumulate else torch.empty)(n, dtype=torch.float32, device=dev)
-    if db is not None and scratch is None:
-        scratch = torch.empty(linear_scratch_bytes(), dtype=torch.uint8, device=dev)
     _here(dy, x, w, pre, dx, dw, db, scratch, status)
     _is((pre is not None) == (ACTIVATIONS[activation] != 0), "pre goes with an activation")
     a = pb_linear_grads(m, n, k, _DTYPES[dt], layout, ACTIVATIONS[activation], int(accumulate),
