@@ -55,8 +55,10 @@ struct View {
 struct Job {
   View x, dy, y;  // dy: backward only; y: the result
   const __nv_bfloat16* gamma;
-  int heads, per_split;  // heads of a token that one lane group takes
-  unsigned blocks, groups;  // groups: tokens * splits
+  int heads;
+  // forward: heads of a token that one lane group takes; backward: (token, head) items
+  int per_group;
+  unsigned blocks, groups;  // forward: groups = tokens * splits
 };
 
 struct Params {
@@ -181,8 +183,8 @@ __device__ __forceinline__ Place place_of(const Params& p, const Job& j, unsigne
   w.token = group - split * p.tokens;
   w.b = w.token / p.S;
   w.s = int(w.token - unsigned(w.b) * p.S);
-  w.h0 = int(split) * j.per_split;
-  w.h1 = min(w.h0 + j.per_split, j.heads);
+  w.h0 = int(split) * j.per_group;
+  w.h1 = min(w.h0 + j.per_group, j.heads);
   w.live = u < p.dh / 16;
   return w;
 }
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
   float c[8], sn[8];
   lane_angles<ADJ>(p, w.token, w.s, u, c, sn);
   // every group of the block makes the same number of steps, so its lanes meet in the sums
-  for (int i = 0; i < j.per_split; ++i) {
+  for (int i = 0; i < j.per_group; ++i) {
     const int h = w.h0 + i, slot = i % kRing;
     fetch(h + kRing - 1, (i + kRing - 1) % kRing);
     copies_wait();
@@ -245,9 +247,36 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
   }
 }
 
-// Blocks walk over their tensor's lane groups with the stride of its blocks and carry the
-// sums of dgamma along; each block leaves one partial sum, added in the blocks' order by
-// gamma_sum_kernel, so the result has the same bits on every run.
+// A lane group's place among the (token, head) items of a tensor, in order.
+struct Cursor {
+  unsigned token;
+  int h, s;
+  int64_t b;
+  __device__ Cursor(const Params& p, int heads, int64_t item) {
+    token = unsigned(item / heads);
+    h = int(item - int64_t(token) * heads);
+    b = token / p.S;
+    s = int(token - unsigned(b) * p.S);
+  }
+  // to the next item; whether that is another token's
+  __device__ bool next(const Params& p, int heads) {
+    if (++h < heads) return false;
+    h = 0;
+    ++token;
+    if (unsigned(++s) == p.S) {
+      s = 0;
+      ++b;
+    }
+    return true;
+  }
+  __device__ int64_t offset(const View& v) const { return b * v.bs + s * v.ss + h * v.hs; }
+};
+
+// The grid is as many blocks as the SMs hold at a time, and every lane group has the same
+// number of items one after the other, whatever tokens they begin in: no second wave, and the
+// copies run on over the tokens' borders. A group carries its sums of dgamma along; each block
+// leaves one partial sum, added in the blocks' order by gamma_sum_kernel, so the result has
+// the same bits on every run.
 template <bool ADJ>
 __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint4 ring_dyn[];  // [kRing][4][THREADS]
@@ -259,9 +288,9 @@ __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_co
   const int u = int(threadIdx.x) & ((1 << p.lanes_log2) - 1);
   int lo, hi;
   chunk_offsets(p, u, lo, hi);
-  const bool norm = j.gamma != nullptr;
+  const bool norm = j.gamma != nullptr, has_values = u < p.dh / 16;
   uint4 g0 = {}, g1 = {};
-  if (norm && u < p.dh / 16) {
+  if (norm && has_values) {
     g0 = __ldg(reinterpret_cast<const uint4*>(j.gamma + lo));
     g1 = __ldg(reinterpret_cast<const uint4*>(j.gamma + hi));
   }
@@ -269,67 +298,69 @@ __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_co
 #pragma unroll
   for (int e = 0; e < 16; ++e) dg[e] = 0.f;
 
-  for (unsigned first = block * per_block; first < j.groups; first += j.blocks * per_block) {
-    const unsigned group = first + (threadIdx.x >> p.lanes_log2);
-    const Place w = place_of(p, j, min(group, j.groups - 1), u);
-    const bool live = w.live && group < j.groups;
-    const __nv_bfloat16* x = norm ? j.x.p + w.b * j.x.bs + w.s * j.x.ss : nullptr;
-    const __nv_bfloat16* dy = j.dy.p + w.b * j.dy.bs + w.s * j.dy.ss;
-    __nv_bfloat16* dx = j.y.p + w.b * j.y.bs + w.s * j.y.ss;
-    const uint32_t ring = smem_u32(ring_dyn) + threadIdx.x * 16;
-    auto fetch = [&](int h, int slot) {
-      if (live && h < w.h1) {
-        const uint32_t at = ring + 4 * slot * (THREADS * 16);
-        copy16(at, dy + h * j.dy.hs + lo);
-        copy16(at + THREADS * 16, dy + h * j.dy.hs + hi);
-        if (norm) {
-          copy16(at + 2 * (THREADS * 16), x + h * j.x.hs + lo);
-          copy16(at + 3 * (THREADS * 16), x + h * j.x.hs + hi);
-        }
-      }
-      copies_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) fetch(w.h0 + i, i);
-    float c[8], sn[8];
-    lane_angles<ADJ>(p, w.token, w.s, u, c, sn);
-    for (int i = 0; i < j.per_split; ++i) {
-      const int h = w.h0 + i;
-      const bool mine = live && h < w.h1;
-      fetch(h + kRing - 1, (i + kRing - 1) % kRing);
-      copies_wait();
-      const uint32_t at = ring + 4 * (i % kRing) * (THREADS * 16);
-      float d[16], v[16];
-      unpack(ring_read(at, w.live), d);
-      unpack(ring_read(at + THREADS * 16, w.live), d + 8);
-      unpack(ring_read(at + 2 * (THREADS * 16), w.live), v);
-      unpack(ring_read(at + 3 * (THREADS * 16), w.live), v + 8);
-      rotate<ADJ, true>(d, c, sn);
+  const int64_t items = int64_t(p.tokens) * j.heads;
+  const int64_t group = int64_t(block) * per_block + (threadIdx.x >> p.lanes_log2);
+  const int64_t item0 = group * j.per_group;
+  const int count = has_values && item0 < items ? int(min(items - item0, int64_t(j.per_group))) : 0;
+  Cursor at(p, j.heads, min(item0, items - 1)), ahead = at;
+  const uint32_t ring = smem_u32(ring_dyn) + threadIdx.x * 16;
+  auto fetch = [&](int i, int slot) {
+    if (i < count) {
+      const uint32_t to = ring + 4 * slot * (THREADS * 16);
+      const __nv_bfloat16* dy = j.dy.p + ahead.offset(j.dy);
+      copy16(to, dy + lo);
+      copy16(to + THREADS * 16, dy + hi);
       if (norm) {
-        float g[16];
-        unpack(g0, g);
-        unpack(g1, g + 8);
-        float sq = 0.f, dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sq += v[e] * v[e];
-          dot += d[e] * g[e] * v[e];
-        }
-        const float inv = 1.f / float(p.dh);
-        const float rstd = rsqrtf(group_sum(sq, p.lanes_log2) * inv + p.eps);
-        const float mean = group_sum(dot, p.lanes_log2) * inv * rstd;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float n = v[e] * rstd;
-          if (mine) dg[e] += d[e] * n;
-          d[e] = rstd * (d[e] * g[e] - n * mean);
-        }
+        const __nv_bfloat16* x = j.x.p + ahead.offset(j.x);
+        copy16(to + 2 * (THREADS * 16), x + lo);
+        copy16(to + 3 * (THREADS * 16), x + hi);
       }
-      if (mine) {
-        *reinterpret_cast<uint4*>(dx + h * j.y.hs + lo) = pack(d);
-        *reinterpret_cast<uint4*>(dx + h * j.y.hs + hi) = pack(d + 8);
+      ahead.next(p, j.heads);
+    }
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) fetch(i, i);
+  float c[8], sn[8];
+  lane_angles<ADJ>(p, at.token, at.s, u, c, sn);
+  // every group makes the same number of steps, so a head's lanes meet in the sums
+  for (int i = 0; i < j.per_group; ++i) {
+    const bool mine = i < count;
+    fetch(i + kRing - 1, (i + kRing - 1) % kRing);
+    copies_wait();
+    const uint32_t from = ring + 4 * (i % kRing) * (THREADS * 16);
+    float d[16], v[16];
+    unpack(ring_read(from, has_values), d);
+    unpack(ring_read(from + THREADS * 16, has_values), d + 8);
+    unpack(ring_read(from + 2 * (THREADS * 16), has_values), v);
+    unpack(ring_read(from + 3 * (THREADS * 16), has_values), v + 8);
+    rotate<ADJ, true>(d, c, sn);
+    if (norm) {
+      float g[16];
+      unpack(g0, g);
+      unpack(g1, g + 8);
+      float sq = 0.f, dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        sq += v[e] * v[e];
+        dot += d[e] * g[e] * v[e];
+      }
+      const float inv = 1.f / float(p.dh);
+      const float rstd = rsqrtf(group_sum(sq, p.lanes_log2) * inv + p.eps);
+      const float mean = group_sum(dot, p.lanes_log2) * inv * rstd;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float n = v[e] * rstd;
+        if (mine) dg[e] += d[e] * n;
+        d[e] = rstd * (d[e] * g[e] - n * mean);
       }
     }
+    if (mine) {
+      __nv_bfloat16* dx = j.y.p + at.offset(j.y);
+      *reinterpret_cast<uint4*>(dx + lo) = pack(d);
+      *reinterpret_cast<uint4*>(dx + hi) = pack(d + 8);
+    }
+    if (at.next(p, j.heads) && i + 1 < count) lane_angles<ADJ>(p, at.token, at.s, u, c, sn);
   }
   if (!norm) return;
   // lanes of the same u across the warp's groups, then the warps in order
@@ -525,12 +556,12 @@ cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Splits the heads of a token over lane groups until `threads` threads have work.
+// Forward: splits the heads of a token over lane groups until `threads` threads have work.
 void set_groups(Job& j, const Params& p, int64_t threads) {
   const int64_t per_head = int64_t(p.tokens) << p.lanes_log2;
   int64_t splits = std::min<int64_t>(j.heads, (threads + per_head - 1) / per_head);
-  j.per_split = int((j.heads + splits - 1) / splits);
-  splits = (j.heads + j.per_split - 1) / j.per_split;
+  j.per_group = int((j.heads + splits - 1) / splits);
+  splits = (j.heads + j.per_group - 1) / j.per_group;
   j.groups = p.tokens * unsigned(splits);
 }
 
@@ -758,12 +789,14 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
     j.y = to_view(out[t]);
     j.gamma = static_cast<const __nv_bfloat16*>(gamma[t]);
     j.heads = dy[t]->heads;
-    set_groups(j, p, int64_t(sms) * 1024);
-    // blocks for two waves of the SMs' two resident ones, shared by the number of heads
+    // the SMs' two resident blocks, shared by the number of heads
     const unsigned per_block = THREADS >> p.lanes_log2;
-    const unsigned all = (j.groups + per_block - 1) / per_block;
-    const int64_t share = (int64_t(sms) * 4 * j.heads + heads - 1) / heads;
-    j.blocks = unsigned(std::min<int64_t>(all, std::min<int64_t>(share, kMaxPartials)));
+    const int64_t items = int64_t(p.tokens) * j.heads;
+    int64_t blocks = int64_t(sms) * 2 * j.heads / heads;
+    blocks = std::max<int64_t>(1, std::min<int64_t>(blocks, kMaxPartials));
+    j.per_group = int((items + blocks * per_block - 1) / (blocks * per_block));
+    const int64_t groups = (items + j.per_group - 1) / j.per_group;
+    j.blocks = unsigned((groups + per_block - 1) / per_block);
     gs.out[t] = dgamma[t];
     gs.blocks[t] = j.blocks;
   }

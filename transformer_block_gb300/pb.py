@@ -8,6 +8,7 @@ been built, or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -209,9 +210,9 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:  # the raw handle: no Stream object for every call
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -649,9 +650,9 @@ def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, e
     _is(first is not None, "q and k are both None")
     b, s = first.size(0), first.size(1)
     if q is not None and out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k is not None and out_k is None:
-        out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
     _here(q, k, positions, gamma_q, gamma_k, out_q, out_k)
     d = rope.head_dim
     _check("pb_qk_norm_rope", lib().pb_qk_norm_rope(
@@ -662,6 +663,7 @@ def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, e
     return out_q, out_k
 
 
+@functools.cache
 def qk_norm_rope_scratch_bytes() -> int:
     n = ctypes.c_size_t()
     _check("pb_qk_norm_rope_scratch_bytes", lib().pb_qk_norm_rope_scratch_bytes(ctypes.byref(n)))
@@ -680,9 +682,9 @@ def qk_norm_rope_backward(rope: Rope, q, k, positions, dq, dk, gamma_q=None, gam
     b, s = first.size(0), first.size(1)
     d, dev = rope.head_dim, first.device
     if dq is not None and out_dq is None:
-        out_dq = torch.empty(dq.shape, dtype=dq.dtype, device=dev)
+        out_dq = torch.empty_like(dq, memory_format=torch.contiguous_format)
     if dk is not None and out_dk is None:
-        out_dk = torch.empty(dk.shape, dtype=dk.dtype, device=dev)
+        out_dk = torch.empty_like(dk, memory_format=torch.contiguous_format)
     new = torch.zeros if accumulate else torch.empty
     if gamma_q is not None and dq is not None and dgamma_q is None:
         dgamma_q = new(d, dtype=torch.float32, device=dev)
