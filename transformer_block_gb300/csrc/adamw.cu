@@ -17,8 +17,10 @@
 // with 8-bit states and bf16 gradients. A thread takes 8 consecutive values, so every access
 // is 16 bytes or more a lane with up to 8 loads in flight a thread, and a warp takes one state
 // block, so its scale is one warp-wide maximum. The tensors' pointers travel as a kernel
-// parameter: no table in device memory, nothing for a captured graph to keep alive. The step
-// walks the values from the last to the first: what the norm's pass (first to last) read last
+// parameter: no table in device memory, nothing for a captured graph to keep alive. A block
+// takes one chunk of 2048 values and ends: walking over chunks in resident blocks lets the SMs
+// drift apart and read and write all over the tensors (50M parameters, 32 bits, with the
+// norm: 291 us, a block a chunk 251). The step walks the values from the last to the first: what the norm's pass (first to last) read last
 // is still in the L2 cache.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -42,7 +44,7 @@ constexpr int PER_THREAD = 8;
 constexpr int CHUNK = THREADS * PER_THREAD;  // values of one tensor a block takes at a time
 static_assert(PB_ADAMW_BLOCK == 32 * PER_THREAD, "one warp takes one state block");
 constexpr float kE4m3Max = 448.f;
-constexpr uint32_t kE4m3Least = 1u;  // code of the least positive value, 2^-9
+constexpr float kE4m3Least = 0x1p-9f;  // the least positive value
 
 struct Tensor {
   void* param;
@@ -101,6 +103,34 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7])));
 }
+// Eight values two at a time (packed fp32 instructions).
+__device__ __forceinline__ void mul8(float (&y)[8], const float (&x)[8], float a) {
+  const uint64_t aa = f2(a, a);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) f2_split(f2_mul(f2(x[e], x[e + 1]), aa), y[e], y[e + 1]);
+}
+// y = a y + b x
+__device__ __forceinline__ void blend8(float (&y)[8], float a, float b, const float (&x)[8]) {
+  const uint64_t aa = f2(a, a), bb = f2(b, b);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2)
+    f2_split(f2_fma(f2(x[e], x[e + 1]), bb, f2_mul(f2(y[e], y[e + 1]), aa)), y[e], y[e + 1]);
+}
+// y = y + a x
+__device__ __forceinline__ void add8(float (&y)[8], float a, const float (&x)[8]) {
+  const uint64_t aa = f2(a, a);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2)
+    f2_split(f2_fma(f2(x[e], x[e + 1]), aa, f2(y[e], y[e + 1])), y[e], y[e + 1]);
+}
+__device__ __forceinline__ void square8(float (&y)[8], const float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint64_t xx = f2(x[e], x[e + 1]);
+    f2_split(f2_mul(xx, xx), y[e], y[e + 1]);
+  }
+}
+
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
@@ -110,6 +140,12 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bf
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -159,9 +195,10 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int n, float scale,
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
     const float2 x = e4m3x2_to_float2((w[e / 4] >> (8 * (e % 4))) & 0xffffu);
-    f[e] = x.x * scale;
-    f[e + 1] = x.y * scale;
+    f[e] = x.x;
+    f[e + 1] = x.y;
   }
+  mul8(f, f, scale);
 }
 
 // Warp-wide: the codes of the block's values and its scale. A block whose largest magnitude is
@@ -174,15 +211,15 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int n, flo
   // magnitudes compare as their bits
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   const bool zero = top < 7.888609052210118e-31f;
-  const float inv = zero ? 0.f : kE4m3Max / top;
-  uint2 c = quant8_e4m3(f, inv);
+  const float inv = zero ? 0.f : __fdividef(kE4m3Max, top);
+  float q[8];
+  mul8(q, f, inv);
   if (SECOND && !zero) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t& w = e < 4 ? c.x : c.y;
-      if (f[e] > 0.f && ((w >> (8 * (e % 4))) & 0xffu) == 0) w |= kE4m3Least << (8 * (e % 4));
-    }
+    for (int e = 0; e < 8; ++e)
+      if (f[e] > 0.f) q[e] = fmaxf(q[e], kE4m3Least);
   }
+  const uint2 c = quant8_e4m3(q, 1.f);
   if (n == 8) {
     __stcs(reinterpret_cast<uint2*>(p), c);
   } else {
@@ -190,7 +227,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int n, flo
     for (int e = 0; e < 8; ++e)
       if (e < n) p[e] = uint8_t((e < 4 ? c.x : c.y) >> (8 * (e % 4)));
   }
-  if ((threadIdx.x & 31) == 0) *scale = zero ? 0.f : top / kE4m3Max;
+  if ((threadIdx.x & 31) == 0) *scale = zero ? 0.f : top * (1.f / kE4m3Max);
 }
 
 // The tensor that holds `chunk`: the last one whose first chunk is not behind it.
@@ -220,46 +257,45 @@ __global__ void __launch_bounds__(THREADS, 4)
     c2 = -1.f / expm1f(k * st.log_beta2);
   }
   const float root2 = sqrtf(c2);
-  for (int64_t i = blockIdx.x; i < tab.chunks; i += gridDim.x) {
-    const int64_t chunk = tab.chunks - 1 - i;
-    const Tensor& t = tab.t[find_tensor(tab, chunk)];
-    const int64_t at = (chunk - t.first_chunk) * CHUNK + int64_t(threadIdx.x) * PER_THREAD;
-    // a warp without values leaves as a whole; with 8-bit states a warp with some stays whole
-    if (at - int64_t(threadIdx.x & 31) * PER_THREAD >= t.n) continue;
-    const int n = int(max(int64_t(0), min(int64_t(PER_THREAD), t.n - at)));
-    float g[8], m[8], v[8], p[8];
-    load_any(static_cast<const G*>(t.grad) + at, n, g);
-    load_any(static_cast<const P*>(t.param) + at, n, p);
-    const int64_t block = at / PB_ADAMW_BLOCK;
-    if (EIGHT) {
-      load_codes(static_cast<const uint8_t*>(t.m) + at, n, t.m_scale[block], m);
-      load_codes(static_cast<const uint8_t*>(t.v) + at, n, t.v_scale[block], v);
+  const int64_t chunk = tab.chunks - 1 - int64_t(blockIdx.x);
+  const Tensor& t = tab.t[find_tensor(tab, chunk)];
+  const int64_t at = (chunk - t.first_chunk) * CHUNK + int64_t(threadIdx.x) * PER_THREAD;
+  // a warp without values leaves as a whole; with 8-bit states a warp with some stays whole
+  if (at - int64_t(threadIdx.x & 31) * PER_THREAD >= t.n) return;
+  const int n = int(max(int64_t(0), min(int64_t(PER_THREAD), t.n - at)));
+  float g[8], m[8], v[8], p[8];
+  load_any(static_cast<const G*>(t.grad) + at, n, g);
+  load_any(static_cast<const P*>(t.param) + at, n, p);
+  const int64_t block = at / PB_ADAMW_BLOCK;
+  if (EIGHT) {
+    load_codes(static_cast<const uint8_t*>(t.m) + at, n, t.m_scale[block], m);
+    load_codes(static_cast<const uint8_t*>(t.v) + at, n, t.v_scale[block], v);
+    square8(v, v);
+  } else {
+    load_any(static_cast<const float*>(t.m) + at, n, m);
+    load_any(static_cast<const float*>(t.v) + at, n, v);
+  }
+  float r[8], up[8];
+  mul8(g, g, gs);
+  blend8(m, st.beta1, st.one_minus_beta1, g);
+  square8(up, g);
+  blend8(v, st.beta2, st.one_minus_beta2, up);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= v[e];
-    } else {
-      load_any(static_cast<const float*>(t.m) + at, n, m);
-      load_any(static_cast<const float*>(t.v) + at, n, v);
-    }
-    const float keep = lr * t.decay;
-    float r[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float ge = g[e] * gs;
-      m[e] = st.beta1 * m[e] + st.one_minus_beta1 * ge;
-      v[e] = st.beta2 * v[e] + st.one_minus_beta2 * ge * ge;
-      r[e] = sqrt_approx(v[e]);
-      const float up = __fdividef(m[e] * c1, r[e] * root2 + st.eps);
-      p[e] = p[e] - keep * p[e] - lr * up;
-    }
-    store_any(static_cast<P*>(t.param) + at, n, p);
-    if (t.copy != nullptr) store_any(t.copy + at, n, p);
-    if (EIGHT) {
-      store_codes<false>(static_cast<uint8_t*>(t.m) + at, t.m_scale + block, n, m);
-      store_codes<true>(static_cast<uint8_t*>(t.v) + at, t.v_scale + block, n, r);
-    } else {
-      store_any(static_cast<float*>(t.m) + at, n, m);
-      store_any(static_cast<float*>(t.v) + at, n, v);
-    }
+  for (int e = 0; e < 8; ++e) {
+    r[e] = sqrt_approx(v[e]);
+    // the denominator is a normal number: eps is one
+    up[e] = m[e] * rcp_approx(r[e] * root2 + st.eps);
+  }
+  add8(p, -lr * t.decay, p);
+  add8(p, -lr * c1, up);
+  store_any(static_cast<P*>(t.param) + at, n, p);
+  if (t.copy != nullptr) store_any(t.copy + at, n, p);
+  if (EIGHT) {
+    store_codes<false>(static_cast<uint8_t*>(t.m) + at, t.m_scale + block, n, m);
+    store_codes<true>(static_cast<uint8_t*>(t.v) + at, t.v_scale + block, n, r);
+  } else {
+    store_any(static_cast<float*>(t.m) + at, n, m);
+    store_any(static_cast<float*>(t.v) + at, n, v);
   }
 }
 
@@ -393,30 +429,28 @@ void fill(Table<CAP>& tab, const pb_adamw_tensor* tensors, int count, int& at, i
 }
 
 template <int CAP, class P, class G, bool EIGHT>
-cudaError_t launch_adamw(const Table<CAP>& tab, const Step& st, int sms, cudaStream_t stream) {
-  // four resident blocks an SM: 16 KB or more of loads in flight each
-  const int64_t grid = std::min<int64_t>(tab.chunks, int64_t(sms) * 4);
-  adamw_kernel<CAP, P, G, EIGHT><<<unsigned(grid), THREADS, 0, stream>>>(tab, st);
+cudaError_t launch_adamw(const Table<CAP>& tab, const Step& st, cudaStream_t stream) {
+  adamw_kernel<CAP, P, G, EIGHT><<<unsigned(tab.chunks), THREADS, 0, stream>>>(tab, st);
   return cudaGetLastError();
 }
 
 template <int CAP>
-cudaError_t launch_any(const Table<CAP>& tab, const Step& st, const pb_adamw_args& a, int sms,
+cudaError_t launch_any(const Table<CAP>& tab, const Step& st, const pb_adamw_args& a,
                        cudaStream_t s) {
   const bool p16 = a.param_dtype == PB_DTYPE_BF16, g16 = a.grad_dtype == PB_DTYPE_BF16;
   using B = __nv_bfloat16;
   if (a.state_bits == 8) {
     if (p16)
-      return g16 ? launch_adamw<CAP, B, B, true>(tab, st, sms, s)
-                 : launch_adamw<CAP, B, float, true>(tab, st, sms, s);
-    return g16 ? launch_adamw<CAP, float, B, true>(tab, st, sms, s)
-               : launch_adamw<CAP, float, float, true>(tab, st, sms, s);
+      return g16 ? launch_adamw<CAP, B, B, true>(tab, st, s)
+                 : launch_adamw<CAP, B, float, true>(tab, st, s);
+    return g16 ? launch_adamw<CAP, float, B, true>(tab, st, s)
+               : launch_adamw<CAP, float, float, true>(tab, st, s);
   }
   if (p16)
-    return g16 ? launch_adamw<CAP, B, B, false>(tab, st, sms, s)
-               : launch_adamw<CAP, B, float, false>(tab, st, sms, s);
-  return g16 ? launch_adamw<CAP, float, B, false>(tab, st, sms, s)
-             : launch_adamw<CAP, float, float, false>(tab, st, sms, s);
+    return g16 ? launch_adamw<CAP, B, B, false>(tab, st, s)
+               : launch_adamw<CAP, B, float, false>(tab, st, s);
+  return g16 ? launch_adamw<CAP, float, B, false>(tab, st, s)
+             : launch_adamw<CAP, float, float, false>(tab, st, s);
 }
 
 pb_status check_dtype(int32_t d, const char* what) {
@@ -463,8 +497,8 @@ pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_
     return record_error(PB_ERR_UNSUPPORTED, "state_bits must be 8 or 32");
   if (!(a.beta1 >= 0 && a.beta1 < 1 && a.beta2 >= 0 && a.beta2 < 1))
     return record_error(PB_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  if (!(float(a.eps) > 0.f && std::isfinite(a.eps)) || !std::isfinite(a.lr))
-    return record_error(PB_ERR_INVALID_ARG, "eps must be finite and > 0 in fp32, lr finite");
+  if (!(float(a.eps) >= 1.17549435e-38f && std::isfinite(a.eps)) || !std::isfinite(a.lr))
+    return record_error(PB_ERR_INVALID_ARG, "eps must be finite and a normal fp32 number, lr finite");
   if (a.d_step == nullptr && a.step < 1)
     return record_error(PB_ERR_INVALID_ARG, "step counts from 1");
   const void* scalars[3] = {a.d_lr, a.d_step, a.d_grad_scale};
@@ -528,9 +562,6 @@ pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_
     any_to = std::max(any_to, x.b);
     if (x.written) written_to = std::max(written_to, x.b);
   }
-  int sms = 0;
-  s = sm_count(&sms);
-  if (s != PB_OK) return s;
   Step st{};
   st.lr = float(a.lr);
   st.beta1 = float(a.beta1);
@@ -554,11 +585,11 @@ pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_
     if (n_tensors - at <= kFew) {
       Table<kFew> tab;
       fill(tab, tensors, n_tensors, at);
-      if (tab.count > 0) e = launch_any(tab, st, a, sms, cs);
+      if (tab.count > 0) e = launch_any(tab, st, a, cs);
     } else {
       Table<kMany> tab;
       fill(tab, tensors, n_tensors, at);
-      if (tab.count > 0) e = launch_any(tab, st, a, sms, cs);
+      if (tab.count > 0) e = launch_any(tab, st, a, cs);
     }
     if (e != cudaSuccess) return cuda_failed(e, "adamw launch");
   }

@@ -12,7 +12,7 @@
 // The angle only matters modulo a turn. A frequency is held as a 64-bit binary fraction of a
 // turn per position, so position times frequency, wrapped to 64 bits, is the angle's place in
 // its turn to 2^-33 at any 32-bit position (negative ones too); a product in fp32 would be off
-// by 0.06 radian at position 10^6. The top 32 bits go to sincospi.
+// by 0.06 radian at position 10^6. The top 32 bits, in radians, go to the fast sine and cosine.
 //
 // Both passes are bound by memory: 4 bytes a value forward, 6 backward (the norm's backward
 // reads x again and recomputes rstd, which costs less than storing it). A head belongs to dh /
@@ -125,22 +125,68 @@ __device__ __forceinline__ void lane_angles(const Params& p, unsigned token, int
     for (int a = 1; a < PB_ROPE_MAX_AXES; ++a)
       if (pair >= p.section_end[a - 1]) pos = at[a];
     const uint64_t turn = uint64_t(int64_t(pos)) * p.turns[pair];
-    // the place in the turn, in half turns: [-1, 1)
-    const float half = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(half, &sn[i], &c[i]);
+    // the place in the turn, in radians: [-pi, pi), where the fast functions are off by
+    // 2^-20.5 at most (a bf16 result's half step is 2^-9 of its value)
+    const float angle = float(int32_t(turn >> 32)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    __sincosf(angle, &sn[i], &c[i]);
   }
 }
 
-template <bool ADJ, bool INVERSE>
+// Values in pairs of neighbours, for packed fp32 instructions: u64 i holds values 2 i, 2 i + 1
+// of the lane's sixteen.
+__device__ __forceinline__ void unpack2(const uint4& u, uint64_t* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    v[e] = f2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack2(const uint64_t* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a, b;
+    f2_split(v[e], a, b);
+    w[e] = pack_bf16x2(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float a, b;
+  f2_split(v, a, b);
+  return a + b;
+}
+// (a, b) -> (a c + b s, b c - a s) for every pair.
+template <bool ADJ>
+__device__ __forceinline__ void rotate_back2(uint64_t (&v)[8], const float (&c)[8],
+                                             const float (&sn)[8]) {
+  if (ADJ) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      f2_split(v[i], a, b);
+      v[i] = f2_fma(v[i], f2(c[i], c[i]), f2_mul(f2(b, a), f2(sn[i], -sn[i])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t cc = f2(c[2 * i], c[2 * i + 1]), ss = f2(sn[2 * i], sn[2 * i + 1]);
+      const uint64_t ns = f2(-sn[2 * i], -sn[2 * i + 1]);
+      const uint64_t a = v[i], b = v[i + 4];
+      v[i] = f2_fma(a, cc, f2_mul(b, ss));
+      v[i + 4] = f2_fma(b, cc, f2_mul(a, ns));
+    }
+  }
+}
+
+template <bool ADJ>
 __device__ __forceinline__ void rotate(float* v, const float (&c)[8], const float (&sn)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int ia = ADJ ? (i < 4 ? 2 * i : 8 + 2 * (i - 4)) : i;
     const int ib = ADJ ? ia + 1 : i + 8;
-    const float s = INVERSE ? -sn[i] : sn[i];
     const float a = v[ia], b = v[ib];
-    v[ia] = a * c[i] - b * s;
-    v[ib] = a * s + b * c[i];
+    v[ia] = a * c[i] - b * sn[i];
+    v[ib] = a * sn[i] + b * c[i];
   }
 }
 
@@ -165,8 +211,15 @@ __device__ __forceinline__ uint4 ring_read(uint32_t src, bool has_values) {
   return u;
 }
 
+// LOG2: the logarithm of a head's lanes, 2 and 3 for heads of 64 and 128 values, or -1: p's.
+template <int LOG2>
 __device__ __forceinline__ float group_sum(float v, int lanes_log2) {
-  for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (LOG2 >= 0) {
+#pragma unroll
+    for (int o = (1 << LOG2) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    for (int o = (1 << lanes_log2) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 
@@ -189,7 +242,7 @@ __device__ __forceinline__ Place place_of(const Params& p, const Job& j, unsigne
   return w;
 }
 
-template <bool ADJ>
+template <bool ADJ, int LOG2>
 __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) uint4 ring_mem[kRing * 2 * THREADS];
   const bool second = blockIdx.x >= p.job[0].blocks;
@@ -232,14 +285,14 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
       float sq = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) sq += v[e] * v[e];
-      const float rstd = rsqrtf(group_sum(sq, p.lanes_log2) / float(p.dh) + p.eps);
+      const float rstd = rsqrtf(group_sum<LOG2>(sq, p.lanes_log2) / float(p.dh) + p.eps);
       float g[16];
       unpack(g0, g);
       unpack(g1, g + 8);
 #pragma unroll
       for (int e = 0; e < 16; ++e) v[e] *= rstd * g[e];
     }
-    rotate<ADJ, false>(v, c, sn);
+    rotate<ADJ>(v, c, sn);
     if (live && h < w.h1) {
       *reinterpret_cast<uint4*>(y + h * j.y.hs + lo) = pack(v);
       *reinterpret_cast<uint4*>(y + h * j.y.hs + hi) = pack(v + 8);
@@ -277,7 +330,7 @@ struct Cursor {
 // copies run on over the tokens' borders. A group carries its sums of dgamma along; each block
 // leaves one partial sum, added in the blocks' order by gamma_sum_kernel, so the result has
 // the same bits on every run.
-template <bool ADJ>
+template <bool ADJ, int LOG2>
 __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint4 ring_dyn[];  // [kRing][4][THREADS]
   __shared__ float red[THREADS / 32][kMaxDh];
@@ -294,28 +347,35 @@ __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_co
     g0 = __ldg(reinterpret_cast<const uint4*>(j.gamma + lo));
     g1 = __ldg(reinterpret_cast<const uint4*>(j.gamma + hi));
   }
-  float dg[16];
+  uint64_t dg[8];  // sums of dgamma
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dg[e] = 0.f;
+  for (int e = 0; e < 8; ++e) dg[e] = 0;
 
   const int64_t items = int64_t(p.tokens) * j.heads;
   const int64_t group = int64_t(block) * per_block + (threadIdx.x >> p.lanes_log2);
   const int64_t item0 = group * j.per_group;
   const int count = has_values && item0 < items ? int(min(items - item0, int64_t(j.per_group))) : 0;
   Cursor at(p, j.heads, min(item0, items - 1)), ahead = at;
+  const __nv_bfloat16 *next_dy = j.dy.p + ahead.offset(j.dy),
+                      *next_x = norm ? j.x.p + ahead.offset(j.x) : nullptr;
+  __nv_bfloat16* dx = j.y.p + at.offset(j.y);
   const uint32_t ring = smem_u32(ring_dyn) + threadIdx.x * 16;
   auto fetch = [&](int i, int slot) {
     if (i < count) {
       const uint32_t to = ring + 4 * slot * (THREADS * 16);
-      const __nv_bfloat16* dy = j.dy.p + ahead.offset(j.dy);
-      copy16(to, dy + lo);
-      copy16(to + THREADS * 16, dy + hi);
+      copy16(to, next_dy + lo);
+      copy16(to + THREADS * 16, next_dy + hi);
       if (norm) {
-        const __nv_bfloat16* x = j.x.p + ahead.offset(j.x);
-        copy16(to + 2 * (THREADS * 16), x + lo);
-        copy16(to + 3 * (THREADS * 16), x + hi);
+        copy16(to + 2 * (THREADS * 16), next_x + lo);
+        copy16(to + 3 * (THREADS * 16), next_x + hi);
       }
-      ahead.next(p, j.heads);
+      if (ahead.next(p, j.heads)) {
+        next_dy = j.dy.p + ahead.offset(j.dy);
+        if (norm) next_x = j.x.p + ahead.offset(j.x);
+      } else {
+        next_dy += j.dy.hs;
+        if (norm) next_x += j.x.hs;
+      }
     }
     copies_commit();
   };
@@ -329,51 +389,61 @@ __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_co
     fetch(i + kRing - 1, (i + kRing - 1) % kRing);
     copies_wait();
     const uint32_t from = ring + 4 * (i % kRing) * (THREADS * 16);
-    float d[16], v[16];
-    unpack(ring_read(from, has_values), d);
-    unpack(ring_read(from + THREADS * 16, has_values), d + 8);
-    unpack(ring_read(from + 2 * (THREADS * 16), has_values), v);
-    unpack(ring_read(from + 3 * (THREADS * 16), has_values), v + 8);
-    rotate<ADJ, true>(d, c, sn);
+    // a group behind its last item works on zeros
+    uint64_t d[8], v[8];
+    unpack2(ring_read(from, mine), d);
+    unpack2(ring_read(from + THREADS * 16, mine), d + 4);
+    rotate_back2<ADJ>(d, c, sn);
     if (norm) {
-      float g[16];
-      unpack(g0, g);
-      unpack(g1, g + 8);
-      float sq = 0.f, dot = 0.f;
+      unpack2(ring_read(from + 2 * (THREADS * 16), mine), v);
+      unpack2(ring_read(from + 3 * (THREADS * 16), mine), v + 4);
+      uint64_t g[8];
+      unpack2(g0, g);
+      unpack2(g1, g + 4);
+      uint64_t sq = 0, dot = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        sq += v[e] * v[e];
-        dot += d[e] * g[e] * v[e];
+      for (int e = 0; e < 8; ++e) {
+        g[e] = f2_mul(d[e], g[e]);
+        sq = f2_fma(v[e], v[e], sq);
+        dot = f2_fma(g[e], v[e], dot);
       }
       const float inv = 1.f / float(p.dh);
-      const float rstd = rsqrtf(group_sum(sq, p.lanes_log2) * inv + p.eps);
-      const float mean = group_sum(dot, p.lanes_log2) * inv * rstd;
+      const float rstd = rsqrtf(group_sum<LOG2>(sum2(sq), p.lanes_log2) * inv + p.eps);
+      // rstd (d gamma - n mean(d gamma n)), n = v rstd
+      const float k = -rstd * rstd * rstd * inv * group_sum<LOG2>(sum2(dot), p.lanes_log2);
+      const uint64_t rr = f2(rstd, rstd), kk = f2(k, k);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float n = v[e] * rstd;
-        if (mine) dg[e] += d[e] * n;
-        d[e] = rstd * (d[e] * g[e] - n * mean);
+      for (int e = 0; e < 8; ++e) {
+        dg[e] = f2_fma(d[e], f2_mul(v[e], rr), dg[e]);
+        d[e] = f2_fma(g[e], rr, f2_mul(v[e], kk));
       }
     }
     if (mine) {
-      __nv_bfloat16* dx = j.y.p + at.offset(j.y);
-      *reinterpret_cast<uint4*>(dx + lo) = pack(d);
-      *reinterpret_cast<uint4*>(dx + hi) = pack(d + 8);
+      *reinterpret_cast<uint4*>(dx + lo) = pack2(d);
+      *reinterpret_cast<uint4*>(dx + hi) = pack2(d + 4);
     }
-    if (at.next(p, j.heads) && i + 1 < count) lane_angles<ADJ>(p, at.token, at.s, u, c, sn);
+    if (!at.next(p, j.heads)) {
+      dx += j.y.hs;
+    } else if (i + 1 < count) {
+      dx = j.y.p + at.offset(j.y);
+      lane_angles<ADJ>(p, at.token, at.s, u, c, sn);
+    }
   }
   if (!norm) return;
   // lanes of the same u across the warp's groups, then the warps in order
+  float dgf[16];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f2_split(dg[e], dgf[2 * e], dgf[2 * e + 1]);
 #pragma unroll
   for (int e = 0; e < 16; ++e)
     for (int o = 16; o >= (1 << p.lanes_log2); o >>= 1)
-      dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], o);
+      dgf[e] += __shfl_xor_sync(0xffffffffu, dgf[e], o);
   const int warp = int(threadIdx.x) >> 5;
   if ((threadIdx.x & 31) < (1u << p.lanes_log2) && u < p.dh / 16) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      red[warp][lo + e] = dg[e];
-      red[warp][hi + e] = dg[8 + e];
+      red[warp][lo + e] = dgf[e];
+      red[warp][hi + e] = dgf[8 + e];
     }
   }
   __syncthreads();
@@ -543,16 +613,30 @@ pb_status fill_params(Params& p, const pb_rope* rope, int batch, int seq, float 
   return PB_OK;
 }
 
-template <bool ADJ>
+template <bool ADJ, int LOG2>
 cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
   constexpr int SMEM = kRing * 4 * THREADS * 16;
   static PerDeviceInit setup;  // per device: shared-memory opt-in
   const cudaError_t e = per_device_init(setup, [](int, int*) {
-    return cudaFuncSetAttribute(qk_backward_kernel<ADJ>,
+    return cudaFuncSetAttribute(qk_backward_kernel<ADJ, LOG2>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   });
   if (e != cudaSuccess) return e;
-  qk_backward_kernel<ADJ><<<grid, THREADS, SMEM, st>>>(p);
+  qk_backward_kernel<ADJ, LOG2><<<grid, THREADS, SMEM, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int LOG2>
+cudaError_t launch_backward_any(bool adjacent, const Params& p, unsigned grid, cudaStream_t st) {
+  return adjacent ? launch_backward<true, LOG2>(p, grid, st) : launch_backward<false, LOG2>(p, grid, st);
+}
+
+template <int LOG2>
+cudaError_t launch_forward(bool adjacent, const Params& p, unsigned grid, cudaStream_t st) {
+  if (adjacent)
+    qk_forward_kernel<true, LOG2><<<grid, THREADS, 0, st>>>(p);
+  else
+    qk_forward_kernel<false, LOG2><<<grid, THREADS, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -684,11 +768,10 @@ pb_status pb_qk_norm_rope(const pb_rope* rope, int32_t batch, int32_t seq, const
   }
   const unsigned grid = p.job[0].blocks + p.job[1].blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (rope->pairing == PB_ROPE_ADJACENT)
-    qk_forward_kernel<true><<<grid, THREADS, 0, st>>>(p);
-  else
-    qk_forward_kernel<false><<<grid, THREADS, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const bool adjacent = rope->pairing == PB_ROPE_ADJACENT;
+  const cudaError_t e = p.lanes_log2 == 3   ? launch_forward<3>(adjacent, p, grid, st)
+                        : p.lanes_log2 == 2 ? launch_forward<2>(adjacent, p, grid, st)
+                                            : launch_forward<-1>(adjacent, p, grid, st);
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "qk_norm_rope launch");
 }
 
@@ -801,8 +884,10 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
     gs.blocks[t] = j.blocks;
   }
   const unsigned grid = p.job[0].blocks + p.job[1].blocks;
-  cudaError_t e = rope->pairing == PB_ROPE_ADJACENT ? launch_backward<true>(p, grid, st)
-                                                    : launch_backward<false>(p, grid, st);
+  const bool adjacent = rope->pairing == PB_ROPE_ADJACENT;
+  cudaError_t e = p.lanes_log2 == 3   ? launch_backward_any<3>(adjacent, p, grid, st)
+                  : p.lanes_log2 == 2 ? launch_backward_any<2>(adjacent, p, grid, st)
+                                      : launch_backward_any<-1>(adjacent, p, grid, st);
   if (e == cudaSuccess && (gs.out[0] != nullptr || gs.out[1] != nullptr)) {
     gamma_sum_kernel<<<dim3(unsigned(dh + 31) / 32, 2), dim3(32, 32), 0, st>>>(
         p.partials, dh, gs, accumulate != 0);
