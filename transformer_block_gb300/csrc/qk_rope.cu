@@ -243,7 +243,7 @@ __device__ __forceinline__ Place place_of(const Params& p, const Job& j, unsigne
 }
 
 template <bool ADJ, int LOG2>
-__global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, 3) qk_forward_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) uint4 ring_mem[kRing * 2 * THREADS];
   const bool second = blockIdx.x >= p.job[0].blocks;
   const Job& j = p.job[second ? 1 : 0];
@@ -303,12 +303,11 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
 // A lane group's place among the (token, head) items of a tensor, in order.
 struct Cursor {
   unsigned token;
-  int h, s;
-  int64_t b;
+  int h, s, b;
   __device__ Cursor(const Params& p, int heads, int64_t item) {
     token = unsigned(item / heads);
     h = int(item - int64_t(token) * heads);
-    b = token / p.S;
+    b = int(token / p.S);
     s = int(token - unsigned(b) * p.S);
   }
   // to the next item; whether that is another token's
@@ -322,7 +321,7 @@ struct Cursor {
     }
     return true;
   }
-  __device__ int64_t offset(const View& v) const { return b * v.bs + s * v.ss + h * v.hs; }
+  __device__ int64_t offset(const View& v) const { return int64_t(b) * v.bs + s * v.ss + h * v.hs; }
 };
 
 // The grid is as many blocks as the SMs hold at a time, and every lane group has the same
@@ -463,6 +462,7 @@ struct GammaSum {
 __global__ void __launch_bounds__(1024) gamma_sum_kernel(const float* partials, int dh,
                                                          const GammaSum g, bool accumulate) {
   __shared__ float red[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums' launch is complete
   const int t = blockIdx.y, col = int(blockIdx.x) * 32 + int(threadIdx.x);
   if (g.out[t] == nullptr) return;
   float s = 0.f;
@@ -889,9 +889,17 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
                   : p.lanes_log2 == 2 ? launch_backward_any<2>(adjacent, p, grid, st)
                                       : launch_backward_any<-1>(adjacent, p, grid, st);
   if (e == cudaSuccess && (gs.out[0] != nullptr || gs.out[1] != nullptr)) {
-    gamma_sum_kernel<<<dim3(unsigned(dh + 31) / 32, 2), dim3(32, 32), 0, st>>>(
-        p.partials, dh, gs, accumulate != 0);
-    e = cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(dh + 31) / 32, 2, 1);
+    cfg.blockDim = dim3(32, 32, 1);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gamma_sum_kernel, static_cast<const float*>(p.partials), dh, gs,
+                           accumulate != 0);
   }
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "qk_norm_rope_backward launch");
 }
