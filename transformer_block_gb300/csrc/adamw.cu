@@ -247,6 +247,8 @@ __device__ __forceinline__ int find_tensor(const Table<CAP>& tab, int64_t chunk)
 template <int CAP, class P, class G, bool EIGHT>
 __global__ void __launch_bounds__(THREADS, 4)
     adamw_kernel(const __grid_constant__ Table<CAP> tab, const __grid_constant__ Step st) {
+  pdl_wait();
+  pdl_trigger();
   const float gs = st.d_grad_scale != nullptr ? *st.d_grad_scale : 1.f;
   if (!(fabsf(gs) <= 3.402823466e38f)) return;  // not finite: the step is left out
   const float lr = st.d_lr != nullptr ? *st.d_lr : st.lr;
@@ -327,6 +329,8 @@ template <int CAP, class G>
 __global__ void __launch_bounds__(THREADS) square_sum_kernel(
     const __grid_constant__ Table<CAP> tab, double* partials) {
   __shared__ double red[THREADS / 32];
+  pdl_wait();
+  pdl_trigger();
   constexpr int LOADS = NORM_PIECES * PER_THREAD * int(sizeof(G)) / 16;  // 16 bytes each
   constexpr int VEC = 16 / int(sizeof(G));
   float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -374,6 +378,8 @@ __global__ void __launch_bounds__(THREADS) square_sum_kernel(
 __global__ void __launch_bounds__(THREADS) norm_kernel(const double* partials, int count,
                                                        float max_norm, float* out) {
   __shared__ double red[THREADS];
+  pdl_wait();
+  pdl_trigger();
   double d = 0.0;
   for (int i = threadIdx.x; i < count; i += THREADS) d += partials[i];
   red[threadIdx.x] = d;
@@ -430,8 +436,8 @@ void fill(Table<CAP>& tab, const pb_adamw_tensor* tensors, int count, int& at, i
 
 template <int CAP, class P, class G, bool EIGHT>
 cudaError_t launch_adamw(const Table<CAP>& tab, const Step& st, cudaStream_t stream) {
-  adamw_kernel<CAP, P, G, EIGHT><<<unsigned(tab.chunks), THREADS, 0, stream>>>(tab, st);
-  return cudaGetLastError();
+  return launch_dependent(adamw_kernel<CAP, P, G, EIGHT>, dim3(unsigned(tab.chunks), 1, 1),
+                          dim3(THREADS, 1, 1), 0, 1, stream, tab, st);
 }
 
 template <int CAP>
@@ -632,12 +638,12 @@ pb_status pb_grad_norm(int32_t n_tensors, const pb_adamw_tensor* tensors, int32_
         std::min<int64_t>(tab.chunks, std::min<int64_t>(kNormBlocks, int64_t(sms) * 6)));
     using T = std::remove_reference_t<decltype(tab)>;
     constexpr int CAP = int(sizeof(T::t) / sizeof(Tensor));
-    if (grad_dtype == PB_DTYPE_BF16)
-      square_sum_kernel<CAP, __nv_bfloat16><<<grid, THREADS, 0, cs>>>(tab, partials + count);
-    else
-      square_sum_kernel<CAP, float><<<grid, THREADS, 0, cs>>>(tab, partials + count);
+    const cudaError_t e = launch_dependent(
+        grad_dtype == PB_DTYPE_BF16 ? square_sum_kernel<CAP, __nv_bfloat16>
+                                    : square_sum_kernel<CAP, float>,
+        dim3(grid, 1, 1), dim3(THREADS, 1, 1), 0, 1, cs, tab, partials + count);
     count += int(grid);
-    return cudaGetLastError();
+    return e;
   };
   while (at < n_tensors) {
     cudaError_t e = cudaSuccess;
@@ -652,8 +658,8 @@ pb_status pb_grad_norm(int32_t n_tensors, const pb_adamw_tensor* tensors, int32_
     }
     if (e != cudaSuccess) return cuda_failed(e, "gradient norm launch");
   }
-  norm_kernel<<<1, THREADS, 0, cs>>>(partials, count, max_norm, out);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(norm_kernel, dim3(1, 1, 1), dim3(THREADS, 1, 1), 0, 1, cs,
+                                         partials, count, max_norm, out);
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "gradient norm launch");
 }
 

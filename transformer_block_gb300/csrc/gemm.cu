@@ -937,6 +937,10 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   cluster_sync();  // both CTAs' barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  if (KIND == kEpiLinear) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const WaitCtl wc{abort_flag, status, limit_ns};
   // Teardown waits for the CTA's own copies and MMAs get at least a second, whatever the
   // wait limit, so shared and tensor memory are never released under them.
@@ -1377,7 +1381,8 @@ __global__ void __launch_bounds__(256)
     linear_finish_kernel(const __grid_constant__ LinearEpi e, int M, int N, const Split s,
                          const float* partials) {
   __shared__ float tile[32][36];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the products' launch is complete
+  pdl_wait();  // the products' launch is complete
+  pdl_trigger();
   const int c = int(blockIdx.x) & 7, slice = int(blockIdx.x >> 3) & 7, ts = int(blockIdx.x >> 6);
   int tm, tn;
   tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
@@ -1440,18 +1445,9 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_linear_finish(bool f16, const LinearEpi& e, int M, int N, const Split& s,
                                  int tiles, const float* partials, cudaStream_t stream) {
-  // launched while the products still run, so that only its wait lies between the two
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles) * 64, 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return f16 ? cudaLaunchKernelEx(&cfg, linear_finish_kernel<true>, e, M, N, s, partials)
-             : cudaLaunchKernelEx(&cfg, linear_finish_kernel<false>, e, M, N, s, partials);
+  const dim3 grid(unsigned(tiles) * 64, 1, 1), block(256, 1, 1);
+  return launch_dependent(f16 ? linear_finish_kernel<true> : linear_finish_kernel<false>, grid,
+                          block, 0, 1, stream, e, M, N, s, partials);
 }
 
 // Process-wide launch counter for the stream-K flags, seeded so that a stale flag left in
@@ -1574,9 +1570,13 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   e.N = N;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   cfg.stream = stream;
-  const cudaError_t launched = cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA,
-                                                  tmB, K, e, sk, status, limit_ns);
-  if (KIND != kEpiLinear || launched != cudaSuccess || sk.sk_tiles == 0) return launched;
+  if (KIND != kEpiLinear)
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA, tmB, K, e, sk, status,
+                              limit_ns);
+  const cudaError_t launched =
+      launch_dependent(gemm_kernel<KIND, OP, LAYOUT, MT>, cfg.gridDim, cfg.blockDim, SMEM_BYTES, 2,
+                       stream, tmA, tmB, K, e, sk, status, limit_ns);
+  if (launched != cudaSuccess || sk.sk_tiles == 0) return launched;
   const Split split{(M + MT * PM - 1) / (MT * PM), (N + BN - 1) / BN, sk.dp_tiles, sk.split, MT,
                     kGroupM / MT};
   return launch_linear_finish(OP == kOpF16, ep.lin, M, N, split, sk.sk_tiles, sk.partials, stream);

@@ -34,6 +34,29 @@ cudaError_t per_device_init(PerDeviceInit& s, F&& init, int* value_out = nullptr
   return s.err[dev];
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Launches a kernel that calls pdl_wait (ptx.cuh) before it touches memory, so that its launch
+// and prologue run during the end of the kernel before it. cluster: CTAs of a cluster.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                             unsigned cluster, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---------------------------------------------------------------- LayerNorm (ln.cu)
 constexpr int kLnMaxH = 16384;
 constexpr int kStatusRange = 7;  // == PB_ERR_RANGE
@@ -190,18 +213,23 @@ cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& 
 // ---------------------------------------------------------------- linear (linear.cu)
 // Few rows of A: y as kEpiLinear's, D = A * B^T with B [N, K] or, b_mn, stored [K, N]. tmA: A
 // in boxes of 64 columns x few_box_rows(M) rows; tmB in boxes of 64 columns x
-// few_box_rows_b(b_mn) rows. scratch: kLinearScratchBytes, or null.
+// few_box_rows_b(b_mn, narrow) rows. narrow: tiles of 64 features (see linear.cu). scratch:
+// kLinearScratchBytes, or null.
 constexpr int kFewRows = 32;
-constexpr int kFewColsKN = 256, kFewKsKN = 64, kFewColsNK = 128, kFewKsNK = 128;
+constexpr int few_cols(bool b_mn, bool narrow) { return narrow ? 64 : b_mn ? 256 : 128; }
+constexpr int few_ks(bool b_mn, bool narrow) { return b_mn && !narrow ? 64 : 128; }
 constexpr int few_box_rows(int M) { return (M + 7) / 8 * 8; }
-constexpr int few_box_rows_b(bool b_mn) { return b_mn ? kFewKsKN : kFewColsNK; }
+constexpr int few_box_rows_b(bool b_mn, bool narrow) {
+  return b_mn ? few_ks(b_mn, narrow) : few_cols(b_mn, narrow);
+}
+constexpr bool few_narrow(int N, int num_sms) { return (N + 63) / 64 <= num_sms; }
 struct FewParams {
   int M, N, K;
   LinearEpi epi;
 };
-cudaError_t launch_linear_few(OpType op, bool b_mn, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                              const FewParams& p, void* scratch, int* status, uint64_t limit_ns,
-                              cudaStream_t stream);
+cudaError_t launch_linear_few(OpType op, bool b_mn, bool narrow, const CUtensorMap& tmA,
+                              const CUtensorMap& tmB, const FewParams& p, void* scratch,
+                              int* status, uint64_t limit_ns, cudaStream_t stream);
 // out = dy * act'(pre), rows of cols 16-bit values.
 cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,
                                 int64_t ld_dy, const void* pre, int64_t ld_pre, void* out,

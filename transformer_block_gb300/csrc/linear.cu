@@ -80,24 +80,27 @@ __device__ __forceinline__ uint16_t from_float(float x) {
 
 // ------------------------------------------------------------------ few tokens
 
-// Stages (of 32 KB of W, 0.7 us of an SM's share of the memory's rate) that equal shares have to
-// save for their second launch.
-constexpr int kFewMinGain = 4;
-constexpr int FEW_WARPS = 8;                       // multiplying warps
-constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1);  // and the producer's
-
-template <int NT, bool KN>
+// Values of W that equal shares have to take off the longest one for their second launch
+// (98,304 do: 2048 x 2048 for 32 tokens 10.0 -> 7.4 us; 81,920 do not: 8192 x 8192 for one
+// token 23.3 -> 28.4).
+constexpr int64_t kFewMinGain = 3 << 15;
+// A wide tile (eight multiplying warps) or a narrow one (four): where narrow tiles give the SMs
+// one each at most, whole tiles need no second launch, and fewer SMs than all still draw the
+// memory's whole rate.
+template <int NT, bool KN, bool NARROW>
 struct FewGeo {
-  static constexpr int COLS = KN ? kFewColsKN : kFewColsNK;  // output features of a tile
-  static constexpr int KS = KN ? kFewKsKN : kFewKsNK;        // k of a stage
-  static constexpr int RT = COLS / (16 * FEW_WARPS);         // 16-feature rows of a warp
+  static constexpr int WARPS = NARROW ? 4 : 8;  // multiplying warps; one more is the producer's
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int COLS = few_cols(KN, NARROW);  // output features of a tile
+  static constexpr int KS = few_ks(KN, NARROW);      // k of a stage
+  static constexpr int RT = COLS / (16 * WARPS);     // 16-feature rows of a warp
   static constexpr int W_BYTES = COLS * KS * 2;
   static constexpr int X_BYTES = 8 * NT * 128;  // a box of 64 k x 8 NT rows of x
   static constexpr int STAGE_BYTES = W_BYTES + KS / 64 * X_BYTES;
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = NARROW ? 8 : 5;
   // per warp, for the results: [8 NT tokens][16 RT features] floats
   static constexpr int OUT_BYTES = 8 * NT * 16 * RT * 4;
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + FEW_WARPS * OUT_BYTES;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + WARPS * OUT_BYTES;
   static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -194,12 +197,12 @@ __device__ __forceinline__ float bias_at(const LinearEpi& e, int n, int N) {
 
 // CTA c does steps [c W, (c + 1) W) of the tiles' steps (`total` stages each) in order.
 // partials: [CTA][2 slots][8 NT][COLS]; slot 1 for the tile whose first stage the CTA has.
-template <int NT, bool KN, bool F16>
-__global__ void __launch_bounds__(FEW_THREADS, 1)
+template <int NT, bool KN, bool F16, bool NARROW>
+__global__ void __launch_bounds__(FewGeo<NT, KN, NARROW>::THREADS, 1)
     few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                const __grid_constant__ FewParams p, int total, int64_t all, int64_t W,
                float* partials, int* status, uint64_t limit_ns) {
-  using G = FewGeo<NT, KN>;
+  using G = FewGeo<NT, KN, NARROW>;
   constexpr int STAGES = G::STAGES, RT = G::RT, KS = G::KS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * STAGES];
@@ -211,12 +214,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, FEW_WARPS);
+      mbar_init(empty0 + 8 * i, G::WARPS);
     }
     abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   const WaitCtl wc{&abort_flag, status, limit_ns};
   int64_t it = int64_t(blockIdx.x) * W;
   const int64_t it_end = min(all, it + W);
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   int stage = 0;
   uint32_t phase = 0;
 
-  if (warp == FEW_WARPS) {
+  if (warp == G::WARPS) {
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer
       uint32_t last_par[STAGES];
@@ -235,11 +240,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         const uint32_t x = w + G::W_BYTES, bar = full0 + 8 * stage;
         const int n0 = tile * G::COLS, k0 = k * KS;
         mbar_arrive_expect_tx(bar, G::STAGE_BYTES);
-        if (KN) {  // boxes of 64 features x 64 k
+        if (KN) {  // boxes of 64 features x KS k
 #pragma unroll
           for (int i = 0; i < G::COLS / 64; ++i)
             tma_load_2d(w + i * (G::W_BYTES / (G::COLS / 64)), &tm_w, bar, n0 + 64 * i, k0);
-        } else {   // boxes of 64 k x 128 features
+        } else {   // boxes of 64 k x COLS features
 #pragma unroll
           for (int i = 0; i < KS / 64; ++i)
             tma_load_2d(w + i * (G::W_BYTES / (KS / 64)), &tm_w, bar, k0 + 64 * i, n0);
@@ -357,12 +362,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 }
 
 // The tiles that several CTAs share: a thread adds up one value.
-template <int NT, bool KN, bool F16>
+template <int NT, bool KN, bool F16, bool NARROW>
 __global__ void __launch_bounds__(256)
     few_finish_kernel(const __grid_constant__ FewParams p, int total, int64_t W,
                       const float* partials) {
-  using G = FewGeo<NT, KN>;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the products' launch is complete
+  using G = FewGeo<NT, KN, NARROW>;
+  pdl_wait();  // the products' launch is complete
+  pdl_trigger();
   const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
   if (n >= p.N) return;
   const int tile = n / G::COLS;
@@ -378,17 +384,17 @@ __global__ void __launch_bounds__(256)
   finish_values<F16>(p.epi, p.M, m, 1, n, bias, z);
 }
 
-template <int NT, bool KN, bool F16>
+template <int NT, bool KN, bool F16, bool NARROW>
 cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const FewParams& p,
                        float* scratch, int* status, uint64_t limit_ns, cudaStream_t stream) {
-  using G = FewGeo<NT, KN>;
+  using G = FewGeo<NT, KN, NARROW>;
   static PerDeviceInit setup;  // per device: shared-memory opt-in; value: number of SMs
   int sms = 0;
   const cudaError_t err = per_device_init(
       setup,
       [](int dev, int* out) {
         const cudaError_t e = cudaFuncSetAttribute(
-            few_kernel<NT, KN, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+            few_kernel<NT, KN, F16, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
         if (e != cudaSuccess) return e;
         return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
       },
@@ -400,36 +406,39 @@ cudaError_t launch_few(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const F
   // whole tiles, or equal shares where these are shorter by what the second launch costs
   int64_t W = (tiles + sms - 1) / sms * total;
   const int64_t even = (all + sms - 1) / sms;
-  if (scratch != nullptr && even + kFewMinGain <= W &&
+  if (scratch != nullptr && (W - even) * G::KS * G::COLS >= kFewMinGain &&
       kLinearScratchBytes >= size_t(sms) * 2 * 8 * NT * G::COLS * 4)
     W = even;
   const unsigned grid = unsigned((all + W - 1) / W);
-  few_kernel<NT, KN, F16><<<grid, FEW_THREADS, G::SMEM, stream>>>(tm_x, tm_w, p, total, all, W,
-                                                                scratch, status, limit_ns);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(few_kernel<NT, KN, F16, NARROW>, dim3(grid, 1, 1),
+                                         dim3(G::THREADS, 1, 1), G::SMEM, 1, stream, tm_x, tm_w, p,
+                                         total, all, W, scratch, status, limit_ns);
   if (e != cudaSuccess || W % total == 0) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((p.N + 255) / 256), unsigned(p.M), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_finish_kernel<NT, KN, F16>, p, total, W,
-                            static_cast<const float*>(scratch));
+  return launch_dependent(few_finish_kernel<NT, KN, F16, NARROW>,
+                          dim3(unsigned((p.N + 255) / 256), unsigned(p.M), 1), dim3(256, 1, 1), 0, 1,
+                          stream, p, total, W, scratch);
 }
 
-template <bool KN, bool F16>
+template <bool KN, bool F16, bool NARROW>
 cudaError_t launch_few_rows(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const FewParams& p,
-                            float* scratch, int* status, uint64_t limit_ns, cudaStream_t stream) {
+                            float* s, int* status, uint64_t limit_ns, cudaStream_t stream) {
   switch (few_box_rows(p.M)) {
-    case 8: return launch_few<1, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
-    case 16: return launch_few<2, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
-    case 24: return launch_few<3, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
-    default: return launch_few<4, KN, F16>(tm_x, tm_w, p, scratch, status, limit_ns, stream);
+    case 8: return launch_few<1, KN, F16, NARROW>(tm_x, tm_w, p, s, status, limit_ns, stream);
+    case 16: return launch_few<2, KN, F16, NARROW>(tm_x, tm_w, p, s, status, limit_ns, stream);
+    case 24: return launch_few<3, KN, F16, NARROW>(tm_x, tm_w, p, s, status, limit_ns, stream);
+    default: return launch_few<4, KN, F16, NARROW>(tm_x, tm_w, p, s, status, limit_ns, stream);
   }
+}
+
+template <bool F16>
+cudaError_t launch_few_any(bool b_mn, bool narrow, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                           const FewParams& p, float* s, int* status, uint64_t limit_ns,
+                           cudaStream_t stream) {
+  if (b_mn)
+    return narrow ? launch_few_rows<true, F16, true>(tm_x, tm_w, p, s, status, limit_ns, stream)
+                  : launch_few_rows<true, F16, false>(tm_x, tm_w, p, s, status, limit_ns, stream);
+  return narrow ? launch_few_rows<false, F16, true>(tm_x, tm_w, p, s, status, limit_ns, stream)
+                : launch_few_rows<false, F16, false>(tm_x, tm_w, p, s, status, limit_ns, stream);
 }
 
 // ------------------------------------------------------------------ activation backward
@@ -474,6 +483,8 @@ __global__ void __launch_bounds__(256)
     row_sum_kernel(const uint16_t* m, int64_t rows, int64_t cols, int64_t ld, int parts, float* out,
                    bool accumulate) {
   __shared__ float red[8][SUM_COLS];
+  pdl_wait();
+  pdl_trigger();
   const int tx = int(threadIdx.x) & 7, ty = int(threadIdx.x) >> 3;
   const int rank = int(blockIdx.x) % parts;
   const int64_t c0 = int64_t(blockIdx.x) / parts * SUM_COLS, c = c0 + tx * 8;
@@ -535,16 +546,14 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_linear_few(OpType op, bool b_mn, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                              const FewParams& p, void* scratch, int* status, uint64_t limit_ns,
-                              cudaStream_t stream) {
+cudaError_t launch_linear_few(OpType op, bool b_mn, bool narrow, const CUtensorMap& tmA,
+                              const CUtensorMap& tmB, const FewParams& p, void* scratch,
+                              int* status, uint64_t limit_ns, cudaStream_t stream) {
   if (p.M < 1 || p.M > kFewRows || p.N < 1 || p.K < 1) return cudaErrorInvalidValue;
   float* s = static_cast<float*>(scratch);
-  if (op == kOpF16)
-    return b_mn ? launch_few_rows<true, true>(tmA, tmB, p, s, status, limit_ns, stream)
-                : launch_few_rows<false, true>(tmA, tmB, p, s, status, limit_ns, stream);
-  return b_mn ? launch_few_rows<true, false>(tmA, tmB, p, s, status, limit_ns, stream)
-              : launch_few_rows<false, false>(tmA, tmB, p, s, status, limit_ns, stream);
+  return op == kOpF16
+             ? launch_few_any<true>(b_mn, narrow, tmA, tmB, p, s, status, limit_ns, stream)
+             : launch_few_any<false>(b_mn, narrow, tmA, tmB, p, s, status, limit_ns, stream);
 }
 
 cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, const void* dy,
@@ -568,22 +577,10 @@ cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols
   if (rows < 1 || cols < 1) return cudaSuccess;
   // up to eight CTAs share a cluster's rows, 128 rows each at least
   const int parts = rows >= 1024 ? 8 : rows <= 128 ? 1 : int(rows / 128);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(parts);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((cols + SUM_COLS - 1) / SUM_COLS) * unsigned(parts), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const auto* src = static_cast<const uint16_t*>(m);
-  return op == kOpF16 ? cudaLaunchKernelEx(&cfg, row_sum_kernel<true>, src, rows, cols, ld, parts,
-                                           out, accumulate)
-                      : cudaLaunchKernelEx(&cfg, row_sum_kernel<false>, src, rows, cols, ld, parts,
-                                           out, accumulate);
+  const dim3 grid(unsigned((cols + SUM_COLS - 1) / SUM_COLS) * unsigned(parts), 1, 1);
+  return launch_dependent(op == kOpF16 ? row_sum_kernel<true> : row_sum_kernel<false>, grid,
+                          dim3(256, 1, 1), 0, unsigned(parts), stream,
+                          static_cast<const uint16_t*>(m), rows, cols, ld, parts, out, accumulate);
 }
 
 }  // namespace pb

@@ -1526,11 +1526,17 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
   ep.lin.ldy = a.ldy;
   if (a.m <= pb::kFewRows) {
     const pb::FewParams f{a.m, a.n, a.k, ep.lin};
+    int dev = -1, sms = 0;
+    PB_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+    PB_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
+            "cudaDeviceGetAttribute");
+    const bool narrow = pb::few_narrow(a.n, sms);
     CUtensorMap tx, tw;
     s = make_map_2d(&tx, a.x, x.rows, x.cols, x.ld, pb::few_box_rows(a.m), op);
-    if (s == PB_OK) s = make_map_2d(&tw, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(in_out), op);
+    if (s == PB_OK) s = make_map_2d(&tw, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(in_out, narrow),
+                                    op);
     if (s != PB_OK) return s;
-    PB_CUDA(pb::launch_linear_few(op, in_out, tx, tw, f, scratch, status, kDefaultLimitNs, st),
+    PB_CUDA(pb::launch_linear_few(op, in_out, narrow, tx, tw, f, scratch, status, kDefaultLimitNs, st),
             "linear launch");
     return PB_OK;
   }
@@ -1615,12 +1621,18 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     ep.lin.ldy = a.lddx;
     if (a.m <= pb::kFewRows) {
       const pb::FewParams f{a.m, a.k, a.n, ep.lin};
+      int dev = -1, sms = 0;
+      PB_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+      PB_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
+              "cudaDeviceGetAttribute");
+      const bool narrow = pb::few_narrow(a.k, sms);
       CUtensorMap ta, tb;
       s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::few_box_rows(a.m), op);
       if (s == PB_OK)
-        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(!in_out), op);
+        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(!in_out, narrow),
+                        op);
       if (s != PB_OK) return s;
-      PB_CUDA(pb::launch_linear_few(op, !in_out, ta, tb, f, scratch, status, kDefaultLimitNs, st),
+      PB_CUDA(pb::launch_linear_few(op, !in_out, narrow, ta, tb, f, scratch, status, kDefaultLimitNs, st),
               "linear backward (dx) launch");
     } else {
       CUtensorMap ta, tb;

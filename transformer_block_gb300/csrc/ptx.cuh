@@ -156,6 +156,16 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
+// ------------------------------------------------------------------------- launches
+// Dependent launches (launch_dependent in kernels.h): a kernel so launched may begin while the
+// one before it on the stream still runs, once all of that one's blocks have begun and called
+// pdl_trigger (or ended), and must call pdl_wait, which returns when that kernel is complete
+// and its writes are visible, before it reads or writes memory.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------------- registers
 // Per-warpgroup register budgets (all four warps of the warpgroup execute it). The sum
 // over the block must stay within what the block was launched with (threads x registers

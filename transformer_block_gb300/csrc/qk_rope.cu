@@ -245,6 +245,8 @@ __device__ __forceinline__ Place place_of(const Params& p, const Job& j, unsigne
 template <bool ADJ, int LOG2>
 __global__ void __launch_bounds__(THREADS, 3) qk_forward_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) uint4 ring_mem[kRing * 2 * THREADS];
+  pdl_wait();
+  pdl_trigger();
   const bool second = blockIdx.x >= p.job[0].blocks;
   const Job& j = p.job[second ? 1 : 0];
   const unsigned block = blockIdx.x - (second ? p.job[0].blocks : 0u);
@@ -333,6 +335,8 @@ template <bool ADJ, int LOG2>
 __global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint4 ring_dyn[];  // [kRing][4][THREADS]
   __shared__ float red[THREADS / 32][kMaxDh];
+  pdl_wait();
+  pdl_trigger();
   const bool second = blockIdx.x >= p.job[0].blocks;
   const Job& j = p.job[second ? 1 : 0];
   const unsigned block = blockIdx.x - (second ? p.job[0].blocks : 0u);
@@ -462,7 +466,8 @@ struct GammaSum {
 __global__ void __launch_bounds__(1024) gamma_sum_kernel(const float* partials, int dh,
                                                          const GammaSum g, bool accumulate) {
   __shared__ float red[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums' launch is complete
+  pdl_wait();  // the partial sums' launch is complete
+  pdl_trigger();
   const int t = blockIdx.y, col = int(blockIdx.x) * 32 + int(threadIdx.x);
   if (g.out[t] == nullptr) return;
   float s = 0.f;
@@ -622,8 +627,8 @@ cudaError_t launch_backward(const Params& p, unsigned grid, cudaStream_t st) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   });
   if (e != cudaSuccess) return e;
-  qk_backward_kernel<ADJ, LOG2><<<grid, THREADS, SMEM, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(qk_backward_kernel<ADJ, LOG2>, dim3(grid, 1, 1), dim3(THREADS, 1, 1), SMEM,
+                          1, st, p);
 }
 
 template <int LOG2>
@@ -633,11 +638,8 @@ cudaError_t launch_backward_any(bool adjacent, const Params& p, unsigned grid, c
 
 template <int LOG2>
 cudaError_t launch_forward(bool adjacent, const Params& p, unsigned grid, cudaStream_t st) {
-  if (adjacent)
-    qk_forward_kernel<true, LOG2><<<grid, THREADS, 0, st>>>(p);
-  else
-    qk_forward_kernel<false, LOG2><<<grid, THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(adjacent ? qk_forward_kernel<true, LOG2> : qk_forward_kernel<false, LOG2>,
+                          dim3(grid, 1, 1), dim3(THREADS, 1, 1), 0, 1, st, p);
 }
 
 // Forward: splits the heads of a token over lane groups until `threads` threads have work.
@@ -889,17 +891,8 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
                   : p.lanes_log2 == 2 ? launch_backward_any<2>(adjacent, p, grid, st)
                                       : launch_backward_any<-1>(adjacent, p, grid, st);
   if (e == cudaSuccess && (gs.out[0] != nullptr || gs.out[1] != nullptr)) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(dh + 31) / 32, 2, 1);
-    cfg.blockDim = dim3(32, 32, 1);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gamma_sum_kernel, static_cast<const float*>(p.partials), dh, gs,
-                           accumulate != 0);
+    e = launch_dependent(gamma_sum_kernel, dim3(unsigned(dh + 31) / 32, 2, 1), dim3(32, 32, 1), 0, 1,
+                         st, p.partials, dh, gs, accumulate != 0);
   }
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "qk_norm_rope_backward launch");
 }
