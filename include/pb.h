@@ -483,6 +483,29 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
                                    float* dgamma_q, float* dgamma_k, int32_t accumulate,
                                    void* scratch, size_t scratch_bytes, void* stream);
 
+/* The step inside the block: every forward entry point on the handle then norms and rotates
+ * the q and k heads of its projection before the attention (one launch more), pb_backward takes
+ * their gradients back through it. dims.head_dim must be the plan's. gamma_q, gamma_k: bf16
+ * [head_dim] device pointers, read by each call, or NULL; positions: int32 [axes, batch, seq]
+ * device pointer, read by each call, or NULL for one axis. For training with a gamma, `saved`
+ * (device, 256-byte aligned, batch * seq * 2 * hidden * 2 bytes) keeps the projection's q and k
+ * between pb_forward_train and pb_backward, as their scratch does the rest; dgamma_q and
+ * dgamma_k (fp32 [head_dim], or NULL) receive the gammas' gradients, by pb_backward's
+ * accumulate. The struct is copied; what it points to must stay valid until the calls are done.
+ * NULL takes the step out again. In pb_trace_read its time counts with the attention. */
+typedef struct pb_block_rope {
+  pb_rope rope;
+  const void* gamma_q;
+  const void* gamma_k;
+  float eps;
+  const int32_t* positions;
+  void* saved;
+  size_t saved_bytes;
+  float* dgamma_q;
+  float* dgamma_k;
+} pb_block_rope;
+pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r);
+
 /* ------------------------------------------------------------------------------------
  * A linear layer outside the block (an embedding's or a head's projection, an adapter, a
  * projection around pb_qk_norm_rope): bias, activation and residual in the product's epilogue,

@@ -53,6 +53,8 @@ struct pb_handle {
   // copy stream and its events (start, input ready x2, compute done x2, output done)
   cudaStream_t copy_stream;
   cudaEvent_t copy_ev[6];
+  bool has_rope;        // pb_set_qk_norm_rope
+  pb_block_rope rope;
 };
 
 namespace {
@@ -369,6 +371,38 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// The q and k columns of a [T, >= 2H] matrix as heads (row stride ld).
+void qk_views(const pb_dims& d, __nv_bfloat16* base, int64_t ld, pb_heads* q, pb_heads* k) {
+  *q = pb_heads{base, d.heads, ld * d.seq, ld, d.head_dim};
+  *k = pb_heads{base + d.hidden, d.heads, ld * d.seq, ld, d.head_dim};
+}
+
+// The handle's norm and rotation of q and k, from `from` [T, 2H] to `to` (which may be `from`).
+pb_status run_rope(pb_handle* h, __nv_bfloat16* from, __nv_bfloat16* to, cudaStream_t st) {
+  const pb_block_rope& r = h->rope;
+  pb_heads q, k, qo, ko;
+  qk_views(h->d, from, 2 * int64_t(h->d.hidden), &q, &k);
+  qk_views(h->d, to, 2 * int64_t(h->d.hidden), &qo, &ko);
+  return pb_qk_norm_rope(&r.rope, h->d.batch, h->d.seq, &q, &k, r.gamma_q, r.gamma_k, r.eps,
+                         r.positions, &qo, &ko, st);
+}
+// Whether training keeps the projection's q and k in the caller's buffer.
+bool rope_saves(const pb_handle* h) {
+  return h->has_rope && (h->rope.gamma_q != nullptr || h->rope.gamma_k != nullptr);
+}
+// A training call on a handle whose norm needs `saved`.
+pb_status check_rope_saved(const pb_handle* h, const void* x, const void* y, const void* scratch,
+                           size_t scratch_bytes) {
+  if (!rope_saves(h)) return PB_OK;
+  const size_t n = size_t(h->d.batch) * h->d.seq * h->d.hidden * 4;
+  if (h->rope.saved == nullptr)
+    return fail(PB_ERR_WORKSPACE, "training with a query or key norm needs pb_block_rope.saved");
+  if (overlap(h->rope.saved, n, scratch, scratch_bytes) || overlap(h->rope.saved, n, x, n / 2) ||
+      overlap(h->rope.saved, n, y, n / 2))
+    return fail(PB_ERR_INVALID_ARG, "pb_block_rope.saved overlaps another argument");
+  return PB_OK;
+}
+
 // One block from x to y (each bf16, or fp32 inside a stack's residual stream),
 // intermediates in `scratch`.
 pb_status run_block(pb_handle* h, const void* x, bool x_f32, void* y, bool y_f32,
@@ -380,6 +414,8 @@ pb_status run_block(pb_handle* h, const void* x, bool x_f32, void* y, bool y_f32
   auto* qk = reinterpret_cast<__nv_bfloat16*>(scratch + L.qk);
   auto* vt = reinterpret_cast<__nv_bfloat16*>(scratch + L.vt);
   void* act = scratch + L.act;
+  // where the projection puts q and k: training keeps them from before their norm
+  auto* qk_in = train && rope_saves(h) ? static_cast<__nv_bfloat16*>(h->rope.saved) : qk;
 
   cudaEvent_t* ev = nullptr;
   if (h->trace_calls < h->trace_max) ev = &h->trace[size_t(h->trace_calls++) * 5];
@@ -412,7 +448,7 @@ pb_status run_block(pb_handle* h, const void* x, bool x_f32, void* y, bool y_f32
   e1.nh = d.heads;
   e1.dh = d.head_dim;
   e1.seq_pad = int64_t(L.seq_pad);
-  e1.qk = qk;
+  e1.qk = qk_in;
   e1.vt = vt;
   e1.act = act;
   e1.act_f16 = h->f16;
@@ -424,7 +460,7 @@ pb_status run_block(pb_handle* h, const void* x, bool x_f32, void* y, bool y_f32
   }
   if (train) e1.hpre = reinterpret_cast<__nv_bfloat16*>(scratch + L.hpre);
   if (!glu) {  // q|k and GeLU(h) by TMA stores (SwiGLU's 16-column outputs stay row stores)
-    s = make_store_map(&e1.tm_out0, qk, T, 2 * uint64_t(H), 2 * uint64_t(H), false);
+    s = make_store_map(&e1.tm_out0, qk_in, T, 2 * uint64_t(H), 2 * uint64_t(H), false);
     if (s == PB_OK) s = make_store_map(&e1.tm_out1, act, T, uint64_t(H + F), uint64_t(H + F), h->f16);
     if (s != PB_OK) return s;
     e1.tma_store = true;
@@ -433,6 +469,11 @@ pb_status run_block(pb_handle* h, const void* x, bool x_f32, void* y, bool y_f32
                           e1, h->num_sms, h->status, h->limit_ns, scratch + L.sk, st),
           "first GEMM launch");
   PB_CUDA(mark(2), "cudaEventRecord");
+
+  if (h->has_rope) {  // norm and rotation of q and k, where the handle has them
+    s = run_rope(h, qk_in, qk, st);
+    if (s != PB_OK) return s;
+  }
 
   // 3. sliding-window attention -> act[:, 0:H]
   CUtensorMap tm_k;
@@ -542,6 +583,10 @@ pb_status run_serial(pb_handle* h, const void* x, void* y, const __nv_bfloat16* 
   PB_CUDA(pb::launch_gemm(pb::kEpiBlockIn, h->op16, tm_xn, tm_wqkv, T, 3 * H, H, e1, h->num_sms,
                           h->status, h->limit_ns, scratch + L.sk, st),
           "QKV GEMM launch");
+  if (h->has_rope) {
+    s = run_rope(h, qk, qk, st);
+    if (s != PB_OK) return s;
+  }
   // 3. sliding-window attention -> act[:, 0:H]
   CUtensorMap tm_qk, tm_k, tm_vt;
   s = make_swa_maps(d, qk, vt, L.seq_pad, &tm_qk, &tm_k, &tm_vt);
@@ -691,6 +736,18 @@ pb_status run_backward(pb_handle* h, const void* x, const void* dy, const pb_gra
   PB_CUDA(pb::launch_swa_bwd(tm_q, tm_k, tm_vt, tm_do, tm_dq, sb, h->status, h->limit_ns, st),
           "attention backward launch");
   PB_CUDA(pb::launch_dq_to_bf16(f32(L.dq_acc), T, H, sb.scale, dz, NZ, st), "dq launch");
+  if (h->has_rope) {
+    // back through the rotation and the norm, in place; the partial sums of the gammas'
+    // gradients go where the GEMMs' partial tiles are at other times
+    const pb_block_rope& r = h->rope;
+    pb_heads q, k, dq, dk;
+    qk_views(d, static_cast<__nv_bfloat16*>(r.saved), 2 * int64_t(H), &q, &k);
+    qk_views(d, dz, NZ, &dq, &dk);
+    s = pb_qk_norm_rope_backward(&r.rope, d.batch, d.seq, &q, &k, r.gamma_q, r.gamma_k, r.eps,
+                                 r.positions, &dq, &dk, &dq, &dk, r.dgamma_q, r.dgamma_k, acc,
+                                 scratch + L.sk, pb::kSkScratchBytes, st);
+    if (s != PB_OK) return s;
+  }
   // 4. dLN(x) = dz W1cat
   CUtensorMap tm_dz, tm_w1t;
   s = make_map_2d(&tm_dz, dz, T, NZ, NZ, box);
@@ -1099,6 +1156,8 @@ pb_status pb_forward_train(pb_handle* h, const void* x, void* y, void* scratch,
   if (overlap(x, n, y, n)) return fail(PB_ERR_INVALID_ARG, "x and y overlap");
   if (overlap(x, n, scratch, L.train_total) || overlap(y, n, scratch, L.train_total))
     return fail(PB_ERR_INVALID_ARG, "x or y overlaps the scratch buffer");
+  s = check_rope_saved(h, x, y, scratch, L.train_total);
+  if (s != PB_OK) return s;
   return run_block(h, x, false, y, false, static_cast<uint8_t*>(scratch),
                    static_cast<cudaStream_t>(stream), true);
 }
@@ -1130,6 +1189,8 @@ pb_status pb_backward(pb_handle* h, const void* x, const void* dy, const pb_grad
     return fail(PB_ERR_INVALID_ARG, "dx overlaps x or dy");
   if (overlap(grads->dx, n, scratch, L.train_total) || overlap(dy, n, scratch, L.train_total))
     return fail(PB_ERR_INVALID_ARG, "dx or dy overlaps the scratch buffer");
+  s = check_rope_saved(h, grads->dx, dy, scratch, L.train_total);
+  if (s != PB_OK) return s;
   return run_backward(h, x, dy, *grads, accumulate != 0, static_cast<uint8_t*>(scratch),
                       static_cast<cudaStream_t>(stream));
 }
@@ -1290,6 +1351,37 @@ pb_status pb_set_wait_limit_ns(pb_handle* h, uint64_t limit_ns) {
   if (s != PB_OK) return s;
   if (limit_ns == 0) return fail(PB_ERR_INVALID_ARG, "limit must be > 0");
   h->limit_ns = limit_ns;
+  return PB_OK;
+}
+
+pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r) {
+  pb_status s = check_handle(h);
+  if (s != PB_OK) return s;
+  if (r == nullptr) {
+    h->has_rope = false;
+    return PB_OK;
+  }
+  if (r->rope.head_dim != h->d.head_dim)
+    return fail(PB_ERR_INVALID_ARG, "the rotation is for head_dim %d, the block has %d",
+                r->rope.head_dim, h->d.head_dim);
+  if (r->saved != nullptr && !aligned(r->saved, 256))
+    return fail(PB_ERR_INVALID_ARG, "saved must be a 256-byte aligned device pointer");
+  const size_t need = size_t(h->d.batch) * h->d.seq * h->d.hidden * 4;
+  if (r->saved != nullptr && r->saved_bytes < need)
+    return fail(PB_ERR_WORKSPACE, "saved has %zu bytes, %zu needed", r->saved_bytes, need);
+  if ((r->dgamma_q != nullptr && r->gamma_q == nullptr) ||
+      (r->dgamma_k != nullptr && r->gamma_k == nullptr))
+    return fail(PB_ERR_INVALID_ARG, "a gradient of gamma without gamma");
+  // the call with these arguments on no tokens checks the rest and does nothing
+  pb_heads q, k;
+  qk_views(h->d, nullptr, 2 * int64_t(h->d.hidden), &q, &k);
+  s = pb_qk_norm_rope(&r->rope, 0, h->d.seq, &q, &k, r->gamma_q, r->gamma_k, r->eps, r->positions,
+                      &q, &k, nullptr);
+  if (s != PB_OK) return s;
+  if (!aligned(r->dgamma_q, 4) || !aligned(r->dgamma_k, 4))
+    return fail(PB_ERR_INVALID_ARG, "dgamma_q and dgamma_k must be 4-byte aligned");
+  h->rope = *r;
+  h->has_rope = true;
   return PB_OK;
 }
 

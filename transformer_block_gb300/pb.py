@@ -87,6 +87,13 @@ class pb_heads(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class pb_block_rope(ctypes.Structure):
+    _fields_ = [("rope", pb_rope), ("gamma_q", ctypes.c_void_p), ("gamma_k", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("positions", ctypes.c_void_p),
+                ("saved", ctypes.c_void_p), ("saved_bytes", ctypes.c_size_t),
+                ("dgamma_q", ctypes.c_void_p), ("dgamma_k", ctypes.c_void_p)]
+
+
 class pb_linear_args(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("m", "n", "k", "dtype", "w_layout", "activation")] + [
         ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p),
@@ -163,6 +170,7 @@ SIGNATURES = {
     "pb_rope_init": (ctypes.c_int, [_I32, _I32, _I32, _I32, _P, _I32, ctypes.c_double, _P, _P]),
     "pb_qk_norm_rope": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P,
                                        _P]),
+    "pb_set_qk_norm_rope": (ctypes.c_int, [_P, _P]),
     "pb_qk_norm_rope_scratch_bytes": (ctypes.c_int, [ctypes.POINTER(_S)]),
     "pb_qk_norm_rope_backward": (ctypes.c_int, [_P, _I32, _I32, _P, _P, _P, _P, ctypes.c_float,
                                                 _P, _P, _P, _P, _P, _P, _P, _I32, _P, _S, _P]),
@@ -378,6 +386,35 @@ class ParallelBlock:
                                      int(accumulate), _ptr(scratch), scratch.numel(),
                                      _stream(stream)))
         return g
+
+    def set_qk_norm_rope(self, rope: "Rope | None", gamma_q=None, gamma_k=None,
+                         eps: float = 1e-6, positions=None, training: bool = False):
+        """``pb_set_qk_norm_rope``: q and k are normed (where there is a gamma) and rotated at
+        ``positions`` (int32 [axes, batch, seq], or None) before the attention, in every call
+        from now on; ``rope=None`` takes that out. The tensors are kept and read by each call.
+        ``training`` allocates what ``forward_train`` keeps and the gradients ``self.rope_grads``
+        (``dgamma_q``, ``dgamma_k``: fp32, written by ``backward``)."""
+        if rope is None:
+            _check("pb_set_qk_norm_rope", self._lib.pb_set_qk_norm_rope(self.handle, None))
+            self._rope, self.rope_grads = None, {}
+            return
+        d = self.dims
+        _here(gamma_q, gamma_k, positions, self.workspace)
+        saved, grads = None, {}
+        if training and (gamma_q is not None or gamma_k is not None):
+            saved = torch.empty(d.batch * d.seq * d.hidden * 4, dtype=torch.uint8,
+                                device=self.workspace.device)
+            for name, g in (("dgamma_q", gamma_q), ("dgamma_k", gamma_k)):
+                if g is not None:
+                    grads[name] = torch.zeros(d.head_dim, dtype=torch.float32, device=g.device)
+        r = pb_block_rope(rope.plan, _flat(gamma_q, d.head_dim, torch.bfloat16, "gamma_q"),
+                          _flat(gamma_k, d.head_dim, torch.bfloat16, "gamma_k"), eps,
+                          _positions(rope, positions, d.batch, d.seq), _ptr(saved),
+                          0 if saved is None else saved.numel(), _ptr(grads.get("dgamma_q")),
+                          _ptr(grads.get("dgamma_k")))
+        _check("pb_set_qk_norm_rope",
+               self._lib.pb_set_qk_norm_rope(self.handle, ctypes.byref(r)))
+        self._rope, self.rope_grads = (gamma_q, gamma_k, positions, saved), grads
 
     def status(self) -> int:
         return self._lib.pb_get_status(self.handle)
