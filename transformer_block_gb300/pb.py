@@ -598,6 +598,16 @@ def _here(*tensors):
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
+def _run_on(stream, call, *args):
+    """``call`` with ``stream`` (a torch.cuda.Stream or a raw handle) as the current stream, so
+    that what it allocates belongs to that stream and is not handed out again before its work
+    on it is done."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
 def _is(cond: bool, what: str):
     if not cond:
         raise ValueError(what)
@@ -683,6 +693,9 @@ def qk_norm_rope(rope: Rope, q, k, positions=None, gamma_q=None, gamma_k=None, e
     """``pb_qk_norm_rope``: norm (where there is a gamma) and rotation of ``q`` and ``k``
     ([batch, seq, heads, head_dim] bf16 views, either may be None) at ``positions`` (int32
     [axes, batch, seq]; None: 0, 1, ... in each sequence). ``out_q=q`` works in place."""
+    if stream is not None:
+        return _run_on(stream, qk_norm_rope, rope, q, k, positions, gamma_q, gamma_k, eps, out_q,
+                       out_k)
     first = q if q is not None else k
     _is(first is not None, "q and k are both None")
     b, s = first.size(0), first.size(1)
@@ -714,6 +727,9 @@ def qk_norm_rope_backward(rope: Rope, q, k, positions, dq, dk, gamma_q=None, gam
     inputs, from the gradients ``dq``, ``dk`` of its results. ``q`` and ``k`` are the forward's
     inputs (None where there is no gamma); a gamma's gradient is fp32 [head_dim], None without
     that gamma, and added to with ``accumulate`` (give the buffer)."""
+    if stream is not None:
+        return _run_on(stream, qk_norm_rope_backward, rope, q, k, positions, dq, dk, gamma_q,
+                       gamma_k, eps, out_dq, out_dk, dgamma_q, dgamma_k, accumulate, scratch)
     first = dq if dq is not None else dk
     _is(first is not None, "dq and dk are both None")
     b, s = first.size(0), first.size(1)
@@ -763,6 +779,9 @@ def linear(x, w, bias=None, residual=None, activation: str = "none",
     (or [n, k], ``PB_WEIGHT_OUT_IN``), bf16 or fp16; ``out_dtype`` (or ``out``'s) is theirs or
     fp32. ``pre`` (a [m, n] tensor of their type) receives ``x @ w + bias``. ``scratch`` (a
     uint8 CUDA tensor of ``linear_scratch_bytes()``) lets the product be split along k."""
+    if stream is not None:
+        return _run_on(stream, linear, x, w, bias, residual, activation, layout, out, out_dtype,
+                       pre, scratch, status)
     m, k = x.shape
     in_out = layout == PB_WEIGHT_IN_OUT
     n = w.size(1 if in_out else 0)
@@ -800,6 +819,9 @@ def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = 
     operands' type, dw (``w``'s layout) and db fp32, None where not wanted. ``pre`` and
     ``activation``: ``x`` is ``activation(pre)``, and dx is the gradient of ``pre``.
     ``accumulate`` adds to the given ``dw`` and ``db``."""
+    if stream is not None:
+        return _run_on(stream, linear_backward, dy, x, w, pre, activation, layout, need_dx, need_dw,
+                       bias, dx, dw, db, accumulate, scratch, status)
     m, n = dy.shape
     in_out = layout == PB_WEIGHT_IN_OUT
     k = (x if x is not None else w).shape[1 if x is not None or not in_out else 0]
@@ -836,6 +858,8 @@ def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = 
 
 def activation_backward(dy, pre, activation: str, out=None, stream=None):
     """``pb_activation_backward``: ``dy * activation'(pre)``, [rows, cols] bf16 or fp16."""
+    if stream is not None:
+        return _run_on(stream, activation_backward, dy, pre, activation, out)
     rows, cols = dy.shape
     _is(dy.dtype in (torch.bfloat16, torch.float16), "dy must be torch.bfloat16 or torch.float16")
     if out is None:
@@ -897,6 +921,8 @@ class AdamW:
     def grad_norm(self, max_norm: float, out=None, scratch=None, stream=None) -> torch.Tensor:
         """``pb_grad_norm``: fp32 [2], the norm of all gradients and the factor that clips them
         to ``max_norm`` (``step(grad_scale=out[1:])``)."""
+        if stream is not None:
+            return _run_on(stream, self.grad_norm, max_norm, out, scratch)
         if out is None:
             out = torch.empty(2, dtype=torch.float32, device=self.device)
         if scratch is None:
