@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpb.so")
 SOURCES = ["pb_api.cu", "ln.cu", "gemm.cu", "swa.cu", "pack.cu", "noalloc.cu", "quant.cu",
            "swa_bwd.cu", "bwd_aux.cu", "qk_rope.cu", "adamw.cu", "linear.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", os.path.join("..", "..", "include", "pb.h")]
+HEADERS = ["kernels.h", "ptx.cuh", "linear_gemm.cuh", os.path.join("..", "..", "include", "pb.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 

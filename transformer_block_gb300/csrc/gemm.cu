@@ -36,15 +36,7 @@ constexpr int BN = kGemmBN;       // output columns per pair tile
 constexpr int BK = kGemmBK;
 constexpr int A_BYTES = BM * BK * 2;        // 16 KB: this CTA's rows of A (one M tile)
 constexpr int B_BYTES = (BN / 2) * BK * 2;  // 16 KB: this CTA's half of B
-// Epilogue warps: four, one for each quarter of the tensor memory's lanes. kEpiLinear has
-// eight, each quarter's columns shared by two: its epilogue may read a pre-activation or a
-// residual and evaluate an activation or its derivative, which four warps do not hide behind a
-// main loop of K = 2048 (8192 x 8192 x 2048 with GeLU': 224 us with four).
-template <int KIND>
-struct Warps {
-  static constexpr int EPI = KIND == kEpiLinear ? 8 : 4;
-  static constexpr int THREADS = 64 + 32 * EPI;
-};
+constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;
 // Per epilogue warp, a 32 x 32 fp32 chunk (rows padded to 33 words: conflict-free both
 // ways) for the coalesced gradient stores.
@@ -56,7 +48,7 @@ static_assert(4 * 32 * STAGE_PITCH * 4 >= 4 * 4096, "four warps' two 2 KB store 
 // (2 x 256 columns). MT = 2: a 512 x 256 unit whose two M tiles share every B stage (a
 // quarter less operand traffic per FLOP), four stages of two A tiles and B, one 256-column
 // accumulator per M tile (not double-buffered).
-template <int MT, int EPI_WARPS = 4>
+template <int MT>
 struct Geo {
   static_assert(MT == 1 || MT == 2, "one or two M tiles per unit");
   static constexpr int STAGES = MT == 2 ? 4 : 6;
@@ -65,8 +57,7 @@ struct Geo {
   // 1024-byte aligned: the forward epilogues' TMA-store buffers (64-byte swizzle) live here
   static constexpr size_t EPI_STAGE_OFF =
       (size_t(STAGES) * STAGE_BYTES + 8 * NUM_BARS + 16 + 1023) / 1024 * 1024;
-  static constexpr size_t SMEM_BYTES =
-      1024 + EPI_STAGE_OFF + (EPI_WARPS == 4 ? 4 * 32 * STAGE_PITCH * 4 : EPI_WARPS * 4096);
+  static constexpr size_t SMEM_BYTES = 1024 + EPI_STAGE_OFF + 4 * 32 * STAGE_PITCH * 4;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of the GEMM");
 };
 
@@ -516,241 +507,6 @@ __device__ __forceinline__ void epilogue32(const EpiParams& ep, int row, int col
   }
 }
 
-// ---------------------------------------------------------------- kEpiLinear
-// Beyond |z| = kActFar every activation and derivative here equals its limit in fp32 (GeLU's
-// tails end at 13, the tanh form's at 9; SiLU's is 1e-33 there): z is held at that bound, so
-// an infinite z meets no infinity times zero. NaN stays NaN.
-constexpr float kActFar = 80.f;
-__device__ __forceinline__ float act_held(float z) {
-  return fabsf(z) > kActFar ? copysignf(kActFar, z) : z;
-}
-// 1 / (1 + exp(-z)) from the approximate exponential and reciprocal (2^-22 relative).
-__device__ __forceinline__ float sigmoid_approx(float z) {
-  return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * z));
-}
-// GeLU's tanh form is z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
-constexpr float kTanh2C = 1.5957691216057308f, kTanhA = 0.044715f;
-
-template <int N>
-__device__ __forceinline__ void act_apply(int act, float (&v)[N]) {
-  if (act == kActNone) return;
-  if (act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float a = act_held(v[i]), b = act_held(v[i + 1]);
-      gelu_pair(a, b);
-      v[i] = v[i] > kActFar ? v[i] : a;
-      v[i + 1] = v[i + 1] > kActFar ? v[i + 1] : b;
-    }
-  } else if (act == kActGeluTanh) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = act_held(v[i]);
-      const float a = z * sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
-      v[i] = v[i] > kActFar ? v[i] : a;
-    }
-  } else if (act == kActSilu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = act_held(v[i]);
-      const float a = z * sigmoid_approx(z);
-      v[i] = v[i] > kActFar ? v[i] : a;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
-  }
-}
-
-// d *= act'(z)
-template <int N>
-__device__ __forceinline__ void act_grad_apply(int act, float (&d)[N], const float (&zs)[N]) {
-  if (act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2)
-      gelu_grad_pair(d[i], d[i + 1], act_held(zs[i]), act_held(zs[i + 1]));
-  } else if (act == kActGeluTanh) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = act_held(zs[i]);
-      const float s = sigmoid_approx(kTanh2C * (z + kTanhA * z * z * z));
-      d[i] *= s + z * s * (1.f - s) * kTanh2C * (1.f + 3.f * kTanhA * z * z);
-    }
-  } else if (act == kActSilu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float z = act_held(zs[i]), s = sigmoid_approx(z);
-      d[i] *= s * (1.f + z * (1.f - s));
-    }
-  } else if (act == kActRelu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = zs[i] > 0.f ? d[i] : zs[i] <= 0.f ? 0.f : zs[i];
-  }
-}
-
-// 32 values of 16 bits from src (64 bytes, 16-byte aligned) or the first n of them.
-template <bool F16>
-__device__ __forceinline__ void load_row16(const void* src, int n, float (&v)[32]) {
-  const uint16_t* s = static_cast<const uint16_t*>(src);
-  uint32_t w[16];
-  if (n >= 32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 u = reinterpret_cast<const uint4*>(s)[q];
-      w[4 * q] = u.x;
-      w[4 * q + 1] = u.y;
-      w[4 * q + 2] = u.z;
-      w[4 * q + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[i] = (2 * i < n ? uint32_t(s[2 * i]) : 0u) |
-             (2 * i + 1 < n ? uint32_t(s[2 * i + 1]) << 16 : 0u);
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    } else {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-// fp32 result of a warp's 32 x 32 chunk: through shared memory, so that a store instruction
-// writes whole 128-byte rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q
-// of row r sits at piece q ^ (r & 7), so neither the rows' writes nor the reads meet a bank
-// twice.
-__device__ __forceinline__ void linear_store_f32(const EpiParams& ep, int row0, int col0,
-                                                 const float (&v)[32], uint32_t stage) {
-  const int lane = int(threadIdx.x & 31);
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                     stage + uint32_t(lane * 128 + ((q ^ (lane & 7)) << 4))),
-                 "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
-                 : "memory");
-  __syncwarp();
-  const int cq = (lane & 7) * 4;
-  const int n = ep.N - (col0 + cq);  // columns left from this lane's first on
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int r = 4 * it + (lane >> 3);
-    if (row0 + r < ep.M && n > 0) {
-      float sr[4];
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(sr[0]), "=f"(sr[1]), "=f"(sr[2]), "=f"(sr[3])
-                   : "r"(stage + uint32_t(r * 128 + (((lane & 7) ^ (r & 7)) << 4)))
-                   : "memory");
-      float* dst = ep.lin.y32 + int64_t(row0 + r) * ep.lin.ldy + col0 + cq;
-      if (n >= 4) {
-        float4 o = make_float4(sr[0], sr[1], sr[2], sr[3]);
-        if (ep.lin.accumulate) {
-          const float4 a = *reinterpret_cast<const float4*>(dst);
-          o.x += a.x;
-          o.y += a.y;
-          o.z += a.z;
-          o.w += a.w;
-        }
-        *reinterpret_cast<float4*>(dst) = o;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < n) dst[e] = ep.lin.accumulate ? dst[e] + sr[e] : sr[e];
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// 16-bit result of a warp's 32 rows x 32 columns, n of them inside the matrix. A TMA store
-// cuts a box off at the last column only to 16 bytes: where the columns end inside those, the
-// last chunk is stored by its lanes.
-template <bool F16>
-__device__ __forceinline__ void linear_store16(StoreStage& ss, const CUtensorMap* tm, void* dst,
-                                               int64_t ld, int row0, int col0, int M, int n,
-                                               const float (&v)[32]) {
-  uint32_t w[16];
-  pack_words16<F16>(v, w);
-  if (n >= 32 || n % 8 == 0) {
-    tma_store_rows32(ss, tm, row0, col0, M, w);
-    return;
-  }
-  const int row = row0 + int(threadIdx.x & 31);
-  if (row < M) {
-    uint16_t* d = static_cast<uint16_t*>(dst) + int64_t(row) * ld + col0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) d[i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
-  }
-}
-
-// Warp-wide, lane l holding row `row` = the warp's first row + l of columns [col0, col0 + 32).
-template <bool F16>
-__device__ __forceinline__ void linear_epilogue32(const EpiParams& ep, int row, int col0,
-                                                  float (&v)[32], StoreStage& ss) {
-  const LinearEpi& e = ep.lin;
-  const int row0 = row - int(threadIdx.x & 31);
-  if (row0 >= ep.M) return;
-  const bool live = row < ep.M;
-  const int n = ep.N - col0;
-  if (e.bias != nullptr) {
-    float b[32];
-    load_row16<F16>(static_cast<const uint16_t*>(e.bias) + col0, n, b);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += b[i];
-  }
-  if (e.pre != nullptr)
-    linear_store16<F16>(ss, &ep.tm_out1, e.pre, e.ld_pre, row0, col0, ep.M, n, v);
-  if (e.mul != nullptr) {
-    if (live) {
-      float z[32];
-      load_row16<F16>(static_cast<const uint16_t*>(e.mul) + int64_t(row) * e.ld_mul + col0, n, z);
-      act_grad_apply(e.act, v, z);
-    }
-  } else {
-    act_apply(e.act, v);
-  }
-  if (e.resid != nullptr && live) {
-    if (e.resid_f32) {
-      const float* r = static_cast<const float*>(e.resid) + int64_t(row) * e.ld_resid + col0;
-      if (n >= 32) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 f = reinterpret_cast<const float4*>(r)[q];
-          v[4 * q] += f.x;
-          v[4 * q + 1] += f.y;
-          v[4 * q + 2] += f.z;
-          v[4 * q + 3] += f.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < n) v[i] += r[i];
-      }
-    } else {
-      float r[32];
-      load_row16<F16>(static_cast<const uint16_t*>(e.resid) + int64_t(row) * e.ld_resid + col0, n,
-                      r);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += r[i];
-    }
-  }
-  if (e.y32 != nullptr) {
-    if (ss.n > 0) {  // the pre-activation's TMA store reads the same shared memory
-      if ((threadIdx.x & 31) == 0) bulk_wait_read();
-      __syncwarp();
-    }
-    linear_store_f32(ep, row0, col0, v, ss.base);
-  } else {
-    linear_store16<F16>(ss, &ep.tm_out0, e.y16, e.ldy, row0, col0, ep.M, n, v);
-  }
-}
-
 // Destination of columns [col0 + cq, col0 + cq + 4) of gradient row `row` (kEpiGrad).
 __device__ __forceinline__ float* grad_dst(const EpiParams& ep, int row, int col0, int cq) {
   if (row >= ep.split_row) return ep.g1 + int64_t(row - ep.split_row) * ep.ld1 + col0 + cq;
@@ -804,16 +560,13 @@ struct Sched {
   int cluster, clusters;
   int dp_tiles, sk_tiles, W;
   int mt, group;             // M tiles per unit; units per rasterisation group
-  int split;                 // kEpiLinear: pairs of a stream-K tile, each with W k-blocks of it
 };
 
 struct SkParams {
   int dp_tiles, sk_tiles, W;
-  float* partials;  // [kSkMaxClusters][2][128][256]; 
-  uint64_t* flags;  // [kSkMaxClusters][2][4]; kEpiLinear: none
+  float* partials;  // [kSkMaxClusters][2][128][256]
+  uint64_t* flags;  // [kSkMaxClusters][2][4]
   uint64_t epoch;
-  int split;        // kEpiLinear: see Sched
-  int seg;          // kEpiLinear, one M tile: k-blocks summed at a time in one accumulator
 };
 
 struct Unit {
@@ -854,15 +607,6 @@ struct UnitIter {
       t += s.clusters;
       return true;
     }
-    if (s.split > 0) {  // one part of one tile: pair split * ts + i has k-blocks [i W, (i + 1) W)
-      const int ts = s.cluster / s.split, kb0 = (s.cluster - ts * s.split) * s.W;
-      if (it < 0 || ts >= s.sk_tiles) return false;
-      it = -1;
-      tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
-      u = Unit{(tm * s.mt + ts % s.mt) * 2 * kGemmBM, tn, 1, ts, kb0,
-               min(s.num_kb, kb0 + s.W)};
-      return true;
-    }
     if (it >= it_end) return false;
     const int ts = int(it / s.num_kb);
     const int kb0 = int(it - int64_t(ts) * s.num_kb);
@@ -884,16 +628,14 @@ __device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
 }
 
 template <int KIND, int OP, int LAYOUT, int MT>
-__global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 int K, const __grid_constant__ EpiParams ep, const SkParams sk, int* status,
                 uint64_t limit_ns) {
   static_assert(MT == 1 || LAYOUT == kKK, "two M tiles per unit: K-major operands only");
-  constexpr int EPI_WARPS = Warps<KIND>::EPI;
-  using G = Geo<MT, EPI_WARPS>;
-  constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES;
-  constexpr int NUM_BARS = G::NUM_BARS;
-  constexpr size_t EPI_STAGE_OFF = G::EPI_STAGE_OFF;
+  constexpr int STAGES = Geo<MT>::STAGES, STAGE_BYTES = Geo<MT>::STAGE_BYTES;
+  constexpr int NUM_BARS = Geo<MT>::NUM_BARS;
+  constexpr size_t EPI_STAGE_OFF = Geo<MT>::EPI_STAGE_OFF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -903,7 +645,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   const uint32_t full0 = smem_u32(bars);                   // [STAGES]
   const uint32_t empty0 = smem_u32(bars + STAGES);         // [STAGES]
   const uint32_t tfull0 = smem_u32(bars + 2 * STAGES);     // [2] accumulator ready
-  const uint32_t tempty0 = smem_u32(bars + 2 * STAGES + 2);  // [2] accumulator drained
+  const uint32_t tempty0 = smem_u32(bars + 2 * STAGES + 2);  // [2] accumulator drained (x8)
   const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -918,7 +660,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);  // the epilogue warps of both CTAs
+      mbar_init(tempty0 + 8 * a, 8);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -937,10 +679,6 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   cluster_sync();  // both CTAs' barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (KIND == kEpiLinear) {
-    pdl_wait();
-    pdl_trigger();
-  }
   const WaitCtl wc{abort_flag, status, limit_ns};
   // Teardown waits for the CTA's own copies and MMAs get at least a second, whatever the
   // wait limit, so shared and tensor memory are never released under them.
@@ -960,7 +698,6 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   sc.dp_tiles = sk.dp_tiles;
   sc.sk_tiles = sk.sk_tiles;
   sc.W = sk.W;
-  sc.split = KIND == kEpiLinear ? sk.split : 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -1037,44 +774,6 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
       UnitIter ui(sc);
       Unit u;
       while (ok && ui.next(sc, u)) {
-        if (KIND == kEpiLinear && MT == 1) {
-          // every sk.seg k-blocks of the unit to the other accumulator; the epilogue warps
-          // add them up
-          for (int ks = u.kb0; ok && ks < u.kb1; ks += sk.seg) {
-            const int ke = min(u.kb1, ks + sk.seg);
-            if (!mbar_wait(tempty0 + 8 * acc, acc_par ^ 1, wc, 2)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            for (int kb = ks; kb < ke; ++kb) {
-              if (!mbar_wait(full0 + 8 * stage, phase, wc, 3)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t sa = smem_u32(smem + size_t(stage) * STAGE_BYTES);
-              const uint64_t da =
-                  AMN ? sdesc_mnmajor_sw128(sa, A_BYTES / 2) : sdesc_kmajor_sw128(sa);
-              const uint64_t db = BMN ? sdesc_mnmajor_sw128(sa + A_BYTES, B_BYTES / 2)
-                                      : sdesc_kmajor_sw128(sa + A_BYTES);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16kind_ss_pair(tmem_base + uint32_t(acc * BN), da + kStepA * k,
-                                    db + kStepB * k, idesc, (kb > ks) || k > 0);
-              mma_commit_pair(empty0 + 8 * stage, 0x3);
-              if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1;
-              }
-            }
-            if (!ok) break;
-            mma_commit_pair(tfull0 + 8 * acc, 0x3);
-            acc ^= 1;
-            if (acc == 0) acc_par ^= 1;
-          }
-          continue;
-        }
         if (!mbar_wait(tempty0 + 8 * acc, acc_par ^ 1, wc, 2)) break;
         tc_fence_after();
         // MT = 1: accumulator acc of two; MT = 2: M tile g in columns [g * BN, (g + 1) * BN)
@@ -1138,113 +837,7 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
     UnitIter ui(sc);
     Unit u;
     bool ok = true;
-    const uint32_t lane_base = tmem_base + ((quad * 32u) << 16);
-    auto release = [&](int a) {  // warp-wide: accumulator a may be written again
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader)
-          mbar_arrive(tempty0 + 8 * a);
-        else
-          mbar_arrive_remote(mapa_shared(tempty0 + 8 * a, 0));
-      }
-    };
     while (ok && ui.next(sc, u)) {
-      if (KIND == kEpiLinear) {
-        const int n0 = u.tn * BN;
-        // the 32-column chunks of this warp
-        const int c_first = int(warp - 2) / 4 * (BN / 64), c_last = c_first + BN / 64;
-        if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
-        tc_fence_after();
-        if (MT == 1 && u.kb1 - u.kb0 > sk.seg) {
-          // Several segments: a lane keeps the sums of its row's columns in registers, so the
-          // products go on in the other accumulator, and leaves the total in the last one's.
-          float sum[BN / 64][32];
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-          for (int ks = u.kb0;;) {
-#pragma unroll
-            for (int c = 0; c < BN / 64; ++c) {
-              uint32_t r[32];
-              tmem_ld32(lane_base + uint32_t(acc * BN + (c_first + c) * 32), r);
-              tmem_ld_wait(r);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
-            }
-            ks += sk.seg;
-            if (ks >= u.kb1) break;
-            release(acc);
-            acc ^= 1;
-            if (acc == 0) acc_par ^= 1;
-            if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-          }
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c) {
-            uint32_t r[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[c][i]);
-            tmem_st32(lane_base + uint32_t(acc * BN + (c_first + c) * 32), r);
-          }
-          tmem_st_wait();
-        }
-        for (int g = 0; g < u.mt; ++g) {
-          const int row = u.row0 + g * PM + int(rank) * BM + int(quad * 32 + lane);
-          const uint32_t taddr = lane_base + uint32_t((MT == 2 ? g : acc) * BN);
-          if (u.ts >= 0 && (u.kb0 > 0 || u.kb1 < sc.num_kb)) {
-            // Part of a tile along K: leave the sums for linear_finish_kernel, in 16-byte
-            // pieces in the order [piece of a row][row], so a warp's accesses are whole
-            // 512-byte runs.
-            float* dst = sk.partials + size_t(sc.cluster) * (2 * 128 * BN) +
-                         (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
-#pragma unroll 1
-            for (int c = c_first; c < c_last; ++c) {
-              if (n0 + c * 32 >= ep.N) break;
-              __syncwarp();
-              uint32_t r[32];
-              tmem_ld32(taddr + uint32_t(c * 32), r);
-              tmem_ld_wait(r);
-              if (row < ep.M) {
-                float4* d4 = reinterpret_cast<float4*>(dst + c * 1024);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  __stcg(d4 + 32 * q,
-                         make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                     __uint_as_float(r[4 * q + 2]),
-                                     __uint_as_float(r[4 * q + 3])));
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int c = c_first; c < c_last; ++c) {
-              const int col0 = n0 + c * 32;
-              if (col0 >= ep.N) break;
-              __syncwarp();
-              uint32_t r[32];
-              tmem_ld32(taddr + uint32_t(c * 32), r);
-              tmem_ld_wait(r);
-              float v[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-              linear_epilogue32<OP == kOpF16>(ep, row, col0, v, ss);
-            }
-          }
-        }
-        release(acc);
-        if (MT == 1) {
-          acc ^= 1;
-          if (acc == 0) acc_par ^= 1;
-        } else {
-          acc_par ^= 1;
-        }
-        continue;
-      }
       if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
       tc_fence_after();
       for (int g = 0; g < u.mt; ++g) {  // MT = 2: the unit's two M tiles, one after the other
@@ -1365,91 +958,6 @@ __global__ void __launch_bounds__(Warps<KIND>::THREADS, 1)
   }
 }
 
-// ---------------------------------------------------------------- split tiles of kEpiLinear
-// The tiles that were split along K: sums of the pairs' partial tiles, in the pairs' order, and
-// the epilogue. A kernel of its own and not, as the other kinds have it, the pair with the
-// tile's first k-block: nothing waits inside a launch, whatever else runs on the GPU, and the
-// sums are spread over all SMs (one pair reading five partial tiles of a 333 x 2504 x 5120
-// product took 45 of its 57 us).
-struct Split {
-  int num_m, num_n, dp_tiles, split, mt, group;  // as in Sched
-};
-
-// Block: 32 rows x 32 columns of a split tile.
-template <bool F16>
-__global__ void __launch_bounds__(256)
-    linear_finish_kernel(const __grid_constant__ LinearEpi e, int M, int N, const Split s,
-                         const float* partials) {
-  __shared__ float tile[32][36];
-  pdl_wait();  // the products' launch is complete
-  pdl_trigger();
-  const int c = int(blockIdx.x) & 7, slice = int(blockIdx.x >> 3) & 7, ts = int(blockIdx.x >> 6);
-  int tm, tn;
-  tile_coords(s.dp_tiles + ts / s.mt, s.num_m, s.num_n, s.group, tm, tn);
-  const int row0 = (tm * s.mt + ts % s.mt) * PM + slice * 32;
-  const int col0 = tn * BN + c * 32;
-  if (row0 >= M || col0 >= N) return;
-  const int r = int(threadIdx.x) & 31, q = int(threadIdx.x) >> 5;  // row, piece of 4 columns
-  const size_t at = size_t(slice) * (32 * BN) + c * 1024 + threadIdx.x * 4;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < s.split; ++k) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(
-        partials + (size_t(ts) * s.split + k) * (2 * 128 * BN) + at));
-    sum.x += v.x;
-    sum.y += v.y;
-    sum.z += v.z;
-    sum.w += v.w;
-  }
-  *reinterpret_cast<float4*>(&tile[r][4 * q]) = sum;
-  __syncthreads();
-  // now a warp has four rows, a lane one column
-  const int col = col0 + r;
-  if (col >= N) return;
-  auto load = [&](const void* p, int64_t i) {
-    const uint16_t x = static_cast<const uint16_t*>(p)[i];
-    return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(uint32_t(x) << 16);
-  };
-  auto store = [&](void* p, int64_t i, float x) {
-    static_cast<uint16_t*>(p)[i] = F16 ? __half_as_ushort(__float2half_rn(x))
-                                       : __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  };
-  const float bias = e.bias != nullptr ? load(e.bias, col) : 0.f;
-  float v[4], z[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = row0 + 4 * q + i;
-    v[i] = tile[4 * q + i][r] + bias;
-    z[i] = e.mul != nullptr && row < M ? load(e.mul, int64_t(row) * e.ld_mul + col) : 0.f;
-    if (e.pre != nullptr && row < M) store(e.pre, int64_t(row) * e.ld_pre + col, v[i]);
-  }
-  if (e.mul != nullptr)
-    act_grad_apply(e.act, v, z);
-  else
-    act_apply(e.act, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + 4 * q + i;
-    if (row >= M) break;
-    if (e.resid != nullptr)
-      v[i] += e.resid_f32 ? static_cast<const float*>(e.resid)[row * e.ld_resid + col]
-                          : load(e.resid, row * e.ld_resid + col);
-    if (e.y32 != nullptr) {
-      float* y = e.y32 + row * e.ldy + col;
-      *y = e.accumulate ? *y + v[i] : v[i];
-    } else {
-      store(e.y16, row * e.ldy + col, v[i]);
-    }
-  }
-}
-
-cudaError_t launch_linear_finish(bool f16, const LinearEpi& e, int M, int N, const Split& s,
-                                 int tiles, const float* partials, cudaStream_t stream) {
-  const dim3 grid(unsigned(tiles) * 64, 1, 1), block(256, 1, 1);
-  return launch_dependent(f16 ? linear_finish_kernel<true> : linear_finish_kernel<false>, grid,
-                          block, 0, 1, stream, e, M, N, s, partials);
-}
-
 // Process-wide launch counter for the stream-K flags, seeded so that a stale flag left in
 // a reused buffer by an earlier process is not taken for this launch's.
 uint64_t next_epoch() {
@@ -1461,19 +969,6 @@ uint64_t next_epoch() {
   return e == 0 ? ++counter : e;
 }
 
-// kEpiLinear: k-blocks (of 64) that one accumulator sums where the result is fp32, before the
-// sum goes on in fp32 additions that round to nearest. The tensor core cuts its sums off
-// instead of rounding them, which leaves 1.0e-6 of relative error at K = 1024 and, growing
-// with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6 of a chain of fp32 fused multiply-adds.
-// Reading an accumulator costs the products about 0.4 us (2048 x 2048 x 8192: 45.1 us in one
-// chain, 46.9 in segments of 32, 48.5 of 16). A 16-bit result rounds at 2^-9 and needs none
-// of that.
-constexpr int kLinearSegment = 12;
-// kEpiLinear: k-blocks (0.28 us each) that a share of a split tile has at least, and that
-// splitting has to save at least: partial sums and second launch cost 5 to 10 us (saving 53 of
-// 80 took 333 x 2504 x 5120 from 27.9 to 19.6 us, saving 16 of 32 took 256 x 8192 x 2048 from
-// 15.4 to 19.2 us).
-constexpr int kLinearMinBlocks = 4, kLinearMinGain = 28;
 // Stream-K tiles of a two-M-tile launch: at most this many pairs share one tile along K.
 constexpr int kSkMaxSplit = 16;
 
@@ -1481,7 +976,7 @@ template <int KIND, int OP, int LAYOUT = kKK, int MT = 1>
 cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, int N, int K,
                         const EpiParams& ep, int num_sms, int* status, uint64_t limit_ns,
                         void* sk_scratch, cudaStream_t stream) {
-  constexpr size_t SMEM_BYTES = Geo<MT, Warps<KIND>::EPI>::SMEM_BYTES;
+  constexpr size_t SMEM_BYTES = Geo<MT>::SMEM_BYTES;
   static PerDeviceInit setup;  // per device: shared-memory opt-in and co-resident pairs
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1489,7 +984,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(Warps<KIND>::THREADS, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -1515,7 +1010,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   if (attr_err != cudaSuccess) return attr_err;
   if (max_clusters <= 0) return cudaErrorLaunchOutOfResources;
   const int units = ((M + MT * PM - 1) / (MT * PM)) * ((N + BN - 1) / BN);
-  int clusters = units < max_clusters ? units : max_clusters;
+  const int clusters = units < max_clusters ? units : max_clusters;
   const int bke = OP == kOpE4m3 ? kGemmBK8 : BK;
   const int num_kb = (K + bke - 1) / bke;
   // Stream-K for the last waves when they would leave pairs idle. MT = 1: every full wave
@@ -1527,7 +1022,7 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
   sk.dp_tiles = units;
   const int rem = units % clusters;
   if (sk_scratch != nullptr && clusters <= kSkMaxClusters && units > clusters && rem != 0 &&
-      num_kb >= 8 && KIND != kEpiLinear) {
+      num_kb >= 8) {
     int sk_pairs = clusters;
     if (MT == 1) {
       sk.sk_tiles = clusters + rem;
@@ -1544,42 +1039,13 @@ cudaError_t launch_kind(const CUtensorMap& tmA, const CUtensorMap& tmB, int M, i
                                            size_t(kSkMaxClusters) * kSkPartialBytes);
     sk.epoch = next_epoch();
   }
-  if (KIND == kEpiLinear) {
-    // The tiles of the last wave are split along K, each over the same number of pairs, where
-    // that takes kLinearMinGain k-blocks at least off the wave: the partial sums cost a second
-    // launch.
-    const int tiles = MT * (units < max_clusters ? units : rem);
-    if (sk_scratch != nullptr && max_clusters <= kSkMaxClusters && tiles > 0) {
-      const int most = max_clusters / tiles;  // pairs for each tile
-      int w = most > 1 ? (num_kb + most - 1) / most : num_kb;
-      if (w < kLinearMinBlocks) w = kLinearMinBlocks;
-      if (w + kLinearMinGain <= num_kb) {
-        sk.W = w;
-        sk.split = (num_kb + w - 1) / w;
-        sk.sk_tiles = tiles;
-        sk.dp_tiles = units - tiles / MT;
-        if (units < max_clusters) clusters = tiles * sk.split;
-      }
-    }
-    sk.partials = static_cast<float*>(sk_scratch);
-    sk.flags = nullptr;
-    sk.seg = ep.lin.y32 != nullptr ? kLinearSegment : num_kb;
-  }
   EpiParams e = ep;
   e.M = M;
   e.N = N;
   cfg.gridDim = dim3(2 * clusters, 1, 1);
   cfg.stream = stream;
-  if (KIND != kEpiLinear)
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA, tmB, K, e, sk, status,
-                              limit_ns);
-  const cudaError_t launched =
-      launch_dependent(gemm_kernel<KIND, OP, LAYOUT, MT>, cfg.gridDim, cfg.blockDim, SMEM_BYTES, 2,
-                       stream, tmA, tmB, K, e, sk, status, limit_ns);
-  if (launched != cudaSuccess || sk.sk_tiles == 0) return launched;
-  const Split split{(M + MT * PM - 1) / (MT * PM), (N + BN - 1) / BN, sk.dp_tiles, sk.split, MT,
-                    kGroupM / MT};
-  return launch_linear_finish(OP == kOpF16, ep.lin, M, N, split, sk.sk_tiles, sk.partials, stream);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, OP, LAYOUT, MT>, tmA, tmB, K, e, sk, status,
+                            limit_ns);
 }
 
 // Two M tiles per unit for the K-major GEMMs whose M spans at least two 256-row tiles and
@@ -1646,39 +1112,6 @@ cudaError_t launch_gemm(EpiKind kind, OpType op, const CUtensorMap& tmA, const C
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& tmA,
-                               const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
-                               int* status, uint64_t limit_ns, void* scratch,
-                               cudaStream_t stream) {
-  if (M <= 0 || N <= 0 || K <= 0) return cudaSuccess;
-  // two M tiles a unit: where the units still fill the pairs (see two_m_tiles), and not for
-  // fp32 results, whose segments need both accumulators for one tile
-  const int64_t units2 = int64_t((M + 2 * PM - 1) / (2 * PM)) * ((N + BN - 1) / BN);
-  const bool two = layout == kKK && two_m_tiles(M, K) && ep.lin.y32 == nullptr &&
-                   units2 >= kSkMaxClusters;
-#define PB_GEMM_LINEAR(OP_)                                                                     \
-  switch (layout) {                                                                             \
-    case kKK:                                                                                   \
-      if (two)                                                                                  \
-        return launch_kind<kEpiLinear, OP_, kKK, 2>(tmA, tmB, M, N, K, ep, 0, status, limit_ns, \
-                                                    scratch, stream);                           \
-      return launch_kind<kEpiLinear, OP_, kKK>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
-                                               scratch, stream);                                \
-    case kKM:                                                                                   \
-      return launch_kind<kEpiLinear, OP_, kKM>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
-                                               scratch, stream);                                \
-    case kMM:                                                                                   \
-      return launch_kind<kEpiLinear, OP_, kMM>(tmA, tmB, M, N, K, ep, 0, status, limit_ns,      \
-                                               scratch, stream);                                \
-    default:                                                                                    \
-      return cudaErrorInvalidValue;                                                             \
-  }
-  if (op == kOpF16) PB_GEMM_LINEAR(kOpF16);
-  if (op == kOpBf16) PB_GEMM_LINEAR(kOpBf16);
-#undef PB_GEMM_LINEAR
-  return cudaErrorInvalidValue;
-}
-
 cudaError_t launch_gemm_layout(EpiKind kind, GemmLayout layout, const CUtensorMap& tmA,
                                const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
                                int num_sms, int* status, uint64_t limit_ns, void* sk_scratch,
@@ -1704,5 +1137,7 @@ cudaError_t launch_gemm_layout(EpiKind kind, GemmLayout layout, const CUtensorMa
 #undef PB_GEMM_LAYOUT
   return cudaErrorInvalidValue;
 }
+
+#include "linear_gemm.cuh"
 
 }  // namespace pb

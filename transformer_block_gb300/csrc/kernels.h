@@ -86,29 +86,6 @@ enum EpiKind : int {
   kEpiResidual = 2,  // y = bf16(D + bias + x)
   kEpiBwdAct = 3,    // D = dy [Wo ; W2]^T: d_attn (bf16), and dh = D * act'(h) into dz
   kEpiGrad = 4,      // fp32 gradient store (or accumulate), split by rows or columns
-  kEpiLinear = 5,    // y = resid + act(D + bias), or D * act'(mul): any M, N and K
-};
-
-// Activations of kEpiLinear (== pb_activation).
-enum Act : int { kActNone = 0, kActGelu = 1, kActGeluTanh = 2, kActSilu = 3, kActRelu = 4 };
-
-// kEpiLinear. 16-bit tensors have the operands' type. Row strides in elements, 16-byte rows
-// (any N: the last columns are handled one by one). The GEMM's y16 and pre leave by TMA stores
-// through tm_out0 and tm_out1.
-struct LinearEpi {
-  int act;
-  const void* bias;   // [N] 16-bit, or null
-  const void* mul;    // backward: D is multiplied by act'(mul), 16-bit [M, N], or null
-  int64_t ld_mul;
-  const void* resid;  // 16-bit or fp32 [M, N], or null
-  int64_t ld_resid;
-  bool resid_f32;
-  void* pre;          // D + bias is also stored here (16-bit), or null
-  int64_t ld_pre;
-  void* y16;          // 16-bit result, or
-  float* y32;         // fp32 result
-  int64_t ldy;
-  bool accumulate;    // y32 is added to
 };
 
 // Operand layouts: bit 0 set = A is MN-major (stored [K, M], M contiguous), bit 1 = B is
@@ -172,7 +149,6 @@ struct EpiParams {
   int64_t ld0, ld1;
   int split_row, split_col;
   bool accumulate;
-  LinearEpi lin;  // kEpiLinear
 };
 
 // Stream-K work space: the tiles of the last waves are split along K across all CTA
@@ -183,10 +159,6 @@ constexpr int kSkMaxClusters = 96;
 constexpr size_t kSkPartialBytes = size_t(2) * 128 * 256 * 4;  // one pair tile, fp32
 constexpr size_t kSkFlagBytes = size_t(2) * 4 * 8;             // 2 CTAs x 4 warps x u64
 constexpr size_t kSkScratchBytes = size_t(kSkMaxClusters) * (kSkPartialBytes + kSkFlagBytes);
-
-// kEpiLinear's work space: the partial sums of tiles that several pairs compute, one for every
-// pair. A second launch adds them up in a fixed order; nothing in it needs preparation.
-constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * kSkPartialBytes;
 
 size_t gemm_smem_bytes();
 // op: the type of A and B (K % 64 == 0, K % 128 == 0 for kOpE4m3). sk_scratch
@@ -203,15 +175,51 @@ cudaError_t launch_gemm_layout(EpiKind kind, GemmLayout layout, const CUtensorMa
                                int num_sms, int* status, uint64_t limit_ns, void* sk_scratch,
                                cudaStream_t stream);
 
-// kEpiLinear with bf16 or fp16 operands (kKK, kKM or kMM; any M, N, K). scratch:
-// kLinearScratchBytes, 256-byte aligned, or null: every tile is computed whole.
-cudaError_t launch_gemm_linear(OpType op, GemmLayout layout, const CUtensorMap& tmA,
-                               const CUtensorMap& tmB, int M, int N, int K, const EpiParams& ep,
-                               int* status, uint64_t limit_ns, void* scratch,
-                               cudaStream_t stream);
+// ---------------------------------------------------------------- linear
+// Activations (== pb_activation).
+enum Act : int { kActNone = 0, kActGelu = 1, kActGeluTanh = 2, kActSilu = 3, kActRelu = 4 };
 
-// ---------------------------------------------------------------- linear (linear.cu)
-// Few rows of A: y as kEpiLinear's, D = A * B^T with B [N, K] or, b_mn, stored [K, N]. tmA: A
+// What follows a product D of the linear layer: y = resid + act(D + bias), or y = D * act'(mul).
+// 16-bit tensors have the operands' type. Row strides in elements, 16-byte rows
+// (any N: the last columns are handled one by one). In the GEMM y16 and pre leave by TMA
+// stores.
+struct LinearEpi {
+  int act;
+  const void* bias;   // [N] 16-bit, or null
+  const void* mul;    // backward: D is multiplied by act'(mul), 16-bit [M, N], or null
+  int64_t ld_mul;
+  const void* resid;  // 16-bit or fp32 [M, N], or null
+  int64_t ld_resid;
+  bool resid_f32;
+  void* pre;          // D + bias is also stored here (16-bit), or null
+  int64_t ld_pre;
+  void* y16;          // 16-bit result, or
+  float* y32;         // fp32 result
+  int64_t ldy;
+  bool accumulate;    // y32 is added to
+};
+
+// Work space: the partial sums of tiles that several pairs compute, one for every pair. A second
+// launch adds them up in a fixed order; nothing in it needs preparation.
+constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * kSkPartialBytes;
+
+// linear_gemm.cuh: D = A * B^T on CTA pairs, bf16 or fp16, any M, N and K. A is [M, K], or with
+// a_mn stored [K, M]; B is [N, K], or with b_mn stored [K, N]. tm_a and tm_b: boxes of 64 columns
+// x kGemmBoxRows rows, of a stored-transposed operand x 64 rows; tm_y and tm_pre: store maps of
+// epi.y16 and epi.pre.
+struct LinearProduct {
+  CUtensorMap tm_a, tm_b, tm_y, tm_pre;
+  int M, N, K;
+  bool a_mn, b_mn;
+  LinearEpi epi;
+};
+// One product, or two at once (that depend on nothing of one another). scratch:
+// kLinearScratchBytes, 256-byte aligned, or null: every tile is computed whole.
+cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, void* scratch,
+                          int* status, uint64_t limit_ns, cudaStream_t stream);
+
+// linear.cu
+// Few rows of A: D = A * B^T with B [N, K] or, b_mn, stored [K, N]. tmA: A
 // in boxes of 64 columns x few_box_rows(M) rows; tmB in boxes of 64 columns x
 // few_box_rows_b(b_mn, narrow) rows. narrow: tiles of 64 features (see linear.cu). scratch:
 // kLinearScratchBytes, or null.

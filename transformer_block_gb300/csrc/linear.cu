@@ -1,4 +1,4 @@
-// linear.cu — the linear layer's kernels around its tensor-core GEMM (gemm.cu, kEpiLinear):
+// linear.cu — the linear layer's kernels around its products (linear_gemm.cuh):
 // the form for few tokens, the activation's backward pass, and the bias gradient.
 //
 // Few tokens (a decoding step): y = resid + act(x W + b) for up to 32 rows of x is bound by

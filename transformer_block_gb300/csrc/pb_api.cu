@@ -1603,21 +1603,21 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
 
   const pb::OpType op = a.dtype == PB_DTYPE_FP16 ? pb::kOpF16 : pb::kOpBf16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  EpiParams ep{};
-  ep.lin.act = a.activation;
-  ep.lin.bias = a.bias;
-  ep.lin.resid = a.residual;
-  ep.lin.ld_resid = a.ldr;
-  ep.lin.resid_f32 = r.esz == 4;
-  ep.lin.pre = a.pre;
-  ep.lin.ld_pre = a.ldp;
+  pb::LinearProduct p{};
+  p.epi.act = a.activation;
+  p.epi.bias = a.bias;
+  p.epi.resid = a.residual;
+  p.epi.ld_resid = a.ldr;
+  p.epi.resid_f32 = r.esz == 4;
+  p.epi.pre = a.pre;
+  p.epi.ld_pre = a.ldp;
   if (y.esz == 4)
-    ep.lin.y32 = static_cast<float*>(a.y);
+    p.epi.y32 = static_cast<float*>(a.y);
   else
-    ep.lin.y16 = a.y;
-  ep.lin.ldy = a.ldy;
+    p.epi.y16 = a.y;
+  p.epi.ldy = a.ldy;
   if (a.m <= pb::kFewRows) {
-    const pb::FewParams f{a.m, a.n, a.k, ep.lin};
+    const pb::FewParams f{a.m, a.n, a.k, p.epi};
     int dev = -1, sms = 0;
     PB_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
     PB_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
@@ -1632,18 +1632,19 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
             "linear launch");
     return PB_OK;
   }
-  CUtensorMap tx, tw;
-  s = make_map_2d(&tx, a.x, x.rows, x.cols, x.ld, pb::kGemmBoxRows, op);
+  p.M = a.m;
+  p.N = a.n;
+  p.K = a.k;
+  p.b_mn = in_out;
+  s = make_map_2d(&p.tm_a, a.x, x.rows, x.cols, x.ld, pb::kGemmBoxRows, op);
   if (s == PB_OK)
-    s = make_map_2d(&tw, a.w, w.rows, w.cols, w.ld, in_out ? 64 : pb::kGemmBoxRows, op);
+    s = make_map_2d(&p.tm_b, a.w, w.rows, w.cols, w.ld, in_out ? 64 : pb::kGemmBoxRows, op);
   if (s == PB_OK && y.esz == 2)
-    s = make_store_map(&ep.tm_out0, a.y, y.rows, y.cols, y.ld, op == pb::kOpF16);
+    s = make_store_map(&p.tm_y, a.y, y.rows, y.cols, y.ld, op == pb::kOpF16);
   if (s == PB_OK && a.pre != nullptr)
-    s = make_store_map(&ep.tm_out1, a.pre, pre.rows, pre.cols, pre.ld, op == pb::kOpF16);
+    s = make_store_map(&p.tm_pre, a.pre, pre.rows, pre.cols, pre.ld, op == pb::kOpF16);
   if (s != PB_OK) return s;
-  PB_CUDA(pb::launch_gemm_linear(op, in_out ? pb::kKM : pb::kKK, tx, tw, a.m, a.n, a.k, ep,
-                                 status, kDefaultLimitNs, scratch, st),
-          "linear launch");
+  PB_CUDA(pb::launch_linear(op, &p, 1, scratch, status, kDefaultLimitNs, st), "linear launch");
   return PB_OK;
 }
 
@@ -1702,17 +1703,18 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
   if (a.db != nullptr)
     PB_CUDA(pb::launch_row_sums(op, a.dy, a.m, a.n, a.lddy, a.db, a.accumulate != 0, st),
             "bias gradient launch");
+  pb::LinearProduct p[2] = {};
+  int count = 0;
   if (a.dx != nullptr) {
     // the contraction runs over n: dy and an [k, n] w are K-major
-    EpiParams ep{};
-    ep.lin.act = a.activation;
-    ep.lin.mul = mul ? a.pre : nullptr;
-    if (!mul) ep.lin.act = PB_ACT_NONE;
-    ep.lin.ld_mul = a.ldp;
-    ep.lin.y16 = a.dx;
-    ep.lin.ldy = a.lddx;
+    pb::LinearProduct& q = p[count];
+    q.epi.act = mul ? a.activation : PB_ACT_NONE;
+    q.epi.mul = mul ? a.pre : nullptr;
+    q.epi.ld_mul = a.ldp;
+    q.epi.y16 = a.dx;
+    q.epi.ldy = a.lddx;
     if (a.m <= pb::kFewRows) {
-      const pb::FewParams f{a.m, a.k, a.n, ep.lin};
+      const pb::FewParams f{a.m, a.k, a.n, q.epi};
       int dev = -1, sms = 0;
       PB_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
       PB_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
@@ -1721,40 +1723,46 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
       CUtensorMap ta, tb;
       s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::few_box_rows(a.m), op);
       if (s == PB_OK)
-        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(!in_out, narrow),
-                        op);
+        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, pb::few_box_rows_b(!in_out, narrow), op);
       if (s != PB_OK) return s;
-      PB_CUDA(pb::launch_linear_few(op, !in_out, narrow, ta, tb, f, scratch, status, kDefaultLimitNs, st),
+      PB_CUDA(pb::launch_linear_few(op, !in_out, narrow, ta, tb, f, scratch, status,
+                                    kDefaultLimitNs, st),
               "linear backward (dx) launch");
+      q.epi = pb::LinearEpi{};
     } else {
-      CUtensorMap ta, tb;
-      s = make_map_2d(&ta, a.dy, dy.rows, dy.cols, dy.ld, pb::kGemmBoxRows, op);
+      q.M = a.m;
+      q.N = a.k;
+      q.K = a.n;
+      q.b_mn = !in_out;
+      s = make_map_2d(&q.tm_a, a.dy, dy.rows, dy.cols, dy.ld, pb::kGemmBoxRows, op);
       if (s == PB_OK)
-        s = make_map_2d(&tb, a.w, w.rows, w.cols, w.ld, in_out ? pb::kGemmBoxRows : 64, op);
+        s = make_map_2d(&q.tm_b, a.w, w.rows, w.cols, w.ld, in_out ? pb::kGemmBoxRows : 64, op);
       if (s == PB_OK)
-        s = make_store_map(&ep.tm_out0, a.dx, dx.rows, dx.cols, dx.ld, op == pb::kOpF16);
+        s = make_store_map(&q.tm_y, a.dx, dx.rows, dx.cols, dx.ld, op == pb::kOpF16);
       if (s != PB_OK) return s;
-      PB_CUDA(pb::launch_gemm_linear(op, in_out ? pb::kKK : pb::kKM, ta, tb, a.m, a.k, a.n, ep,
-                                     status, kDefaultLimitNs, scratch, st),
-              "linear backward (dx) launch");
+      ++count;
     }
   }
   if (a.dw != nullptr) {
-    // the contraction runs over the tokens: both operands are MN-major
+    // the contraction runs over the tokens: both operands are stored transposed
     const Matrix& ra = in_out ? x : dy;
     const Matrix& rb = in_out ? dy : x;
-    CUtensorMap ta, tb;
-    s = make_map_2d(&ta, ra.p, ra.rows, ra.cols, ra.ld, 64, op);
-    if (s == PB_OK) s = make_map_2d(&tb, rb.p, rb.rows, rb.cols, rb.ld, 64, op);
+    pb::LinearProduct& q = p[count];
+    q.M = int(wr);
+    q.N = int(wc);
+    q.K = a.m;
+    q.a_mn = q.b_mn = true;
+    s = make_map_2d(&q.tm_a, ra.p, ra.rows, ra.cols, ra.ld, 64, op);
+    if (s == PB_OK) s = make_map_2d(&q.tm_b, rb.p, rb.rows, rb.cols, rb.ld, 64, op);
     if (s != PB_OK) return s;
-    EpiParams ep{};
-    ep.lin.y32 = a.dw;
-    ep.lin.ldy = a.lddw;
-    ep.lin.accumulate = a.accumulate != 0;
-    PB_CUDA(pb::launch_gemm_linear(op, pb::kMM, ta, tb, int(wr), int(wc), a.m, ep, status,
-                                   kDefaultLimitNs, scratch, st),
-            "linear backward (dw) launch");
+    q.epi.y32 = a.dw;
+    q.epi.ldy = a.lddw;
+    q.epi.accumulate = a.accumulate != 0;
+    ++count;
   }
+  if (count > 0)
+    PB_CUDA(pb::launch_linear(op, p, count, scratch, status, kDefaultLimitNs, st),
+            "linear backward launch");
   return PB_OK;
 }
 
