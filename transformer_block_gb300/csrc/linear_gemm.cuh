@@ -11,8 +11,8 @@
 //   waits inside a launch, whatever else runs on the GPU.
 // * fp32 results: the tensor core cuts its sums off instead of rounding them, which leaves 1.0e-6
 //   of relative error at K = 1024 and, growing with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6
-//   of a chain of fp32 fused multiply-adds. So an accumulator sums 768 k at a time, and the
-//   epilogue warps add these up in registers, rounding, while the products go on in the other
+//   of a chain of fp32 fused multiply-adds. So an accumulator sums 896 k at most, and the
+//   epilogue warps add such segments up in registers, rounding, while the products go on in the other
 //   accumulator. Reading one costs the products about 0.4 us (2048 x 2048 x 8192: 45.1 us in one
 //   chain, 46.9 in segments of 2048 k, 48.5 of 1024). A 16-bit result rounds at 2^-9 and is
 //   summed in one chain.
@@ -39,7 +39,7 @@ constexpr size_t LIN_SMEM = 1024 + LIN_OUT_OFF + LIN_EPI * 4096;
 static_assert(LIN_SMEM <= 227 * 1024, "shared memory of the linear kernel");
 
 // k-blocks (of 64) that one accumulator sums where the result is fp32.
-constexpr int kLinearSegment = 12;
+constexpr int kLinearSegment = 14;
 // k-blocks (0.28 us each) that a part of a split tile has at least, and that splitting has to
 // save at least: partial sums and second launch cost 5 to 10 us (saving 53 of 80 took 333 x
 // 2504 x 5120 from 27.9 to 19.6 us, saving 16 of 32 took 256 x 8192 x 2048 from 15.4 to 19.2).
@@ -287,6 +287,21 @@ __device__ __forceinline__ void linear_store16(StoreStage& ss, const CUtensorMap
     for (int i = 0; i < 32; ++i)
       if (i < n) d[i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
   }
+}
+
+// A lane's 32 columns of part of a tile, for linear_finish_kernel: in 16-byte pieces in the
+// order [piece of a row][row], so a warp's accesses are whole 512-byte runs.
+__device__ __forceinline__ void linear_store_part(float* dst, const float (&v)[32]) {
+  float4* d4 = reinterpret_cast<float4*>(dst);
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    __stcg(d4 + 32 * q, make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+}
+
+// fp32 results that are the product and nothing else.
+__device__ __forceinline__ bool linear_plain(const LinearEpi& e) {
+  return e.y32 != nullptr && e.act == kActNone && e.bias == nullptr && e.mul == nullptr &&
+         e.resid == nullptr && e.pre == nullptr;
 }
 
 // Warp-wide, lane l holding row `row` = the warp's first row + l of columns [col0, col0 + 32).
@@ -568,8 +583,10 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
       if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
       tc_fence_after();
       if (u.kb1 - u.kb0 > jb.seg) {
-        // Several segments: a lane keeps the sums of its row's columns in registers and leaves
-        // the total in the last segment's accumulator.
+        // Several segments: a lane keeps the sums of its row's columns in registers. What takes
+        // no epilogue (a weight's gradient, a split tile's part) is stored from there, with the
+        // accumulator released before (8192 x 8192 x 2048: 231 us where it was held for the
+        // stores); else the total goes back to the last segment's accumulator.
         float sum[BN / 64][32];
 #pragma unroll
         for (int c = 0; c < BN / 64; ++c)
@@ -594,6 +611,22 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           tc_fence_after();
         }
         if (!ok) break;
+        if (u.slot >= 0 || linear_plain(jb.epi)) {
+          release();
+          const int row0 = u.row0 + int(rank) * BM + int(quad * 32);
+          float* dst = work.partials + size_t(u.slot < 0 ? 0 : u.slot) * (2 * 128 * BN) +
+                       (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+            const int col0 = n0 + (c_first + c) * 32;
+            if (col0 >= N || row0 >= jb.M) break;
+            if (u.slot < 0)
+              linear_store_f32(jb, row0, col0, sum[c], ss.base);
+            else if (row0 + int(lane) < jb.M)
+              linear_store_part(dst + (c_first + c) * 1024, sum[c]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int c = 0; c < BN / 64; ++c) {
           uint32_t r[32];
@@ -606,8 +639,6 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
       const int row = u.row0 + int(rank) * BM + int(quad * 32 + lane);
       const uint32_t taddr = lane_base + uint32_t(acc * BN);
       if (u.slot >= 0) {
-        // Part of a tile along K: leave the sums for linear_finish_kernel, in 16-byte pieces in
-        // the order [piece of a row][row], so a warp's accesses are whole 512-byte runs.
         float* dst = work.partials + size_t(u.slot) * (2 * 128 * BN) +
                      (size_t(rank) * 4 + quad) * (32 * BN) + lane * 4;
 #pragma unroll 1
@@ -617,14 +648,10 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           uint32_t r[32];
           tmem_ld32(taddr + uint32_t(c * 32), r);
           tmem_ld_wait(r);
-          if (row < jb.M) {
-            float4* d4 = reinterpret_cast<float4*>(dst + c * 1024);
+          float v[32];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              __stcg(d4 + 32 * q,
-                     make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
-          }
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (row < jb.M) linear_store_part(dst + c * 1024, v);
         }
       } else {
 #pragma unroll 1
@@ -852,7 +879,9 @@ cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, v
     jb.num_m = (p.M + PM - 1) / PM;
     jb.num_n = (p.N + BN - 1) / BN;
     jb.num_kb = (p.K + BK - 1) / BK;
-    jb.seg = p.epi.y32 != nullptr ? kLinearSegment : jb.num_kb;
+    // fp32 results: segments of about one length, kLinearSegment k-blocks at most
+    const int segments = (jb.num_kb + kLinearSegment - 1) / kLinearSegment;
+    jb.seg = p.epi.y32 != nullptr ? (jb.num_kb + segments - 1) / segments : jb.num_kb;
     jb.a_mn = p.a_mn;
     jb.b_mn = p.b_mn;
   }
