@@ -221,12 +221,13 @@ __device__ __forceinline__ void load_row16(const void* src, int n, float (&v)[32
   }
 }
 
-// fp32 result of a warp's 32 x 32 chunk: through shared memory, so that a store instruction
-// writes whole 128-byte rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q
-// of row r sits at piece q ^ (r & 7), so neither the rows' writes nor the reads meet a bank
-// twice.
-__device__ __forceinline__ void linear_store_f32(const LinearJob& jb, int row0, int col0,
-                                                 const float (&v)[32], uint32_t stage) {
+// fp32 result of a warp's 32 x 32 chunk at y (row stride ld), of which `rows` rows and n columns
+// are inside the matrix: through shared memory, so that a store instruction writes whole 128-byte
+// rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q of row r sits at piece q
+// ^ (r & 7), so neither the rows' writes nor the reads meet a bank twice.
+__device__ __forceinline__ void linear_store_f32(float* y, int64_t ld, int rows, int n,
+                                                 bool accumulate, const float (&v)[32],
+                                                 uint32_t stage) {
   const int lane = int(threadIdx.x & 31);
 #pragma unroll
   for (int q = 0; q < 8; ++q)
@@ -235,36 +236,35 @@ __device__ __forceinline__ void linear_store_f32(const LinearJob& jb, int row0, 
                  "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
                  : "memory");
   __syncwarp();
-  const int cq = (lane & 7) * 4;
-  const int n = jb.N - (col0 + cq);  // columns left from this lane's first on
+  const int r0 = lane >> 3, q = lane & 7;  // this lane's first row and its piece of every fourth
+  float* dst = y + r0 * ld + 4 * q;
+  const int left = n - 4 * q;  // columns from this lane's first on
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int r = 4 * it + (lane >> 3);
-    if (row0 + r < jb.M && n > 0) {
-      float sr[4];
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(sr[0]), "=f"(sr[1]), "=f"(sr[2]), "=f"(sr[3])
-                   : "r"(stage + uint32_t(r * 128 + (((lane & 7) ^ (r & 7)) << 4)))
-                   : "memory");
-      float* dst = jb.epi.y32 + int64_t(row0 + r) * jb.epi.ldy + col0 + cq;
-      if (n >= 4) {
-        float4 o = make_float4(sr[0], sr[1], sr[2], sr[3]);
-        if (jb.epi.accumulate) {
-          const float4 a = *reinterpret_cast<const float4*>(dst);
-          o.x += a.x;
-          o.y += a.y;
-          o.z += a.z;
-          o.w += a.w;
-        }
-        *reinterpret_cast<float4*>(dst) = o;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < n) dst[e] = jb.epi.accumulate ? dst[e] + sr[e] : sr[e];
+  for (int it = 0; it < 8; ++it, dst += 4 * ld) {
+    const int r = 4 * it + r0;
+    float4 o;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
+                 : "r"(stage + uint32_t(r * 128 + ((q ^ (r & 7)) << 4)))
+                 : "memory");
+    if (r >= rows) continue;
+    if (left >= 4) {
+      if (accumulate) {
+        const float4 a = *reinterpret_cast<const float4*>(dst);
+        o.x += a.x;
+        o.y += a.y;
+        o.z += a.z;
+        o.w += a.w;
       }
+      *reinterpret_cast<float4*>(dst) = o;
+    } else {
+      const float w[3] = {o.x, o.y, o.z};
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < left) dst[e] = accumulate ? dst[e] + w[e] : w[e];
     }
   }
-  __syncwarp();
+  __syncwarp();  // the buffer may be written again
 }
 
 // 16-bit result of a warp's 32 rows x 32 columns, n of them inside the matrix. A TMA store
@@ -306,13 +306,13 @@ __device__ __forceinline__ bool linear_plain(const LinearEpi& e) {
 
 // Warp-wide, lane l holding row `row` = the warp's first row + l of columns [col0, col0 + 32).
 template <bool F16>
-__device__ __forceinline__ void linear_epilogue32(const LinearJob& jb, int row, int col0,
-                                                  float (&v)[32], StoreStage& ss) {
-  const LinearEpi& e = jb.epi;
+__device__ __forceinline__ void linear_epilogue32(const LinearEpi& e, const LinearJob& jb, int M,
+                                                  int N, int row, int col0, float (&v)[32],
+                                                  StoreStage& ss) {
   const int row0 = row - int(threadIdx.x & 31);
-  if (row0 >= jb.M) return;
-  const bool live = row < jb.M;
-  const int n = jb.N - col0;
+  if (row0 >= M) return;
+  const bool live = row < M;
+  const int n = N - col0;
   if (e.bias != nullptr) {
     float b[32];
     load_row16<F16>(static_cast<const uint16_t*>(e.bias) + col0, n, b);
@@ -320,7 +320,7 @@ __device__ __forceinline__ void linear_epilogue32(const LinearJob& jb, int row, 
     for (int i = 0; i < 32; ++i) v[i] += b[i];
   }
   if (e.pre != nullptr)
-    linear_store16<F16>(ss, &jb.tm_pre, e.pre, e.ld_pre, row0, col0, jb.M, n, v);
+    linear_store16<F16>(ss, &jb.tm_pre, e.pre, e.ld_pre, row0, col0, M, n, v);
   if (e.mul != nullptr) {
     if (live) {
       float z[32];
@@ -360,9 +360,10 @@ __device__ __forceinline__ void linear_epilogue32(const LinearJob& jb, int row, 
       if ((threadIdx.x & 31) == 0) bulk_wait_read();
       __syncwarp();
     }
-    linear_store_f32(jb, row0, col0, v, ss.base);
+    linear_store_f32(e.y32 + int64_t(row0) * e.ldy + col0, e.ldy, M - row0, n, e.accumulate, v,
+                     ss.base);
   } else {
-    linear_store16<F16>(ss, &jb.tm_y, e.y16, e.ldy, row0, col0, jb.M, n, v);
+    linear_store16<F16>(ss, &jb.tm_y, e.y16, e.ldy, row0, col0, M, n, v);
   }
 }
 
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
     bool ok = true;
     while (ok && it.next(work, pair, pairs, u)) {
       const LinearJob& jb = work.job[u.job];
-      const int n0 = u.tn * BN, N = jb.N;
+      const int M = jb.M, N = jb.N, n0 = u.tn * BN;
       if (!mbar_wait_warp(tfull0 + 8 * acc, acc_par, wc, 4)) break;
       tc_fence_after();
       if (u.kb1 - u.kb0 > jb.seg) {
@@ -594,12 +595,11 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
         for (int ks = u.kb0;;) {
 #pragma unroll
-          for (int c = 0; c < BN / 64; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + uint32_t(acc * BN + (c_first + c) * 32), r);
-            tmem_ld_wait(r);
+          for (int c = 0; c < BN / 32; ++c) {  // sixteen columns at a time: registers
+            uint32_t r[16];
+            tmem_ld16_wait(lane_base + uint32_t(acc * BN + c_first * 32 + c * 16), r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) sum[c / 2][16 * (c % 2) + i] += __uint_as_float(r[i]);
           }
           ks += jb.seg;
           if (ks >= u.kb1) break;
@@ -611,7 +611,8 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           tc_fence_after();
         }
         if (!ok) break;
-        if (u.slot >= 0 || linear_plain(jb.epi)) {
+        const LinearEpi& e = u.job == 0 ? work.job[0].epi : work.job[1].epi;
+        if (u.slot >= 0 || linear_plain(e)) {
           release();
           const int row0 = u.row0 + int(rank) * BM + int(quad * 32);
           float* dst = work.partials + size_t(u.slot < 0 ? 0 : u.slot) * (2 * 128 * BN) +
@@ -619,10 +620,11 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < BN / 64; ++c) {
             const int col0 = n0 + (c_first + c) * 32;
-            if (col0 >= N || row0 >= jb.M) break;
+            if (col0 >= N || row0 >= M) break;
             if (u.slot < 0)
-              linear_store_f32(jb, row0, col0, sum[c], ss.base);
-            else if (row0 + int(lane) < jb.M)
+              linear_store_f32(e.y32 + int64_t(row0) * e.ldy + col0, e.ldy, M - row0, N - col0,
+                               e.accumulate, sum[c], ss.base);
+            else if (row0 + int(lane) < M)
               linear_store_part(dst + (c_first + c) * 1024, sum[c]);
           }
           continue;
@@ -636,6 +638,8 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
         }
         tmem_st_wait();
       }
+      // in registers: read through a job's index inside the loops they cost more than the stores
+      const LinearEpi e = u.job == 0 ? work.job[0].epi : work.job[1].epi;
       const int row = u.row0 + int(rank) * BM + int(quad * 32 + lane);
       const uint32_t taddr = lane_base + uint32_t(acc * BN);
       if (u.slot >= 0) {
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (row < jb.M) linear_store_part(dst + c * 1024, v);
+          if (row < M) linear_store_part(dst + c * 1024, v);
         }
       } else {
 #pragma unroll 1
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          linear_epilogue32<F16>(jb, row, col0, v, ss);
+          linear_epilogue32<F16>(e, jb, M, N, row, col0, v, ss);
         }
       }
       release();
