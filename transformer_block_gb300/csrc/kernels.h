@@ -206,7 +206,7 @@ constexpr size_t kLinearScratchBytes = size_t(kSkMaxClusters) * kSkPartialBytes;
 // linear_gemm.cuh: D = A * B^T on CTA pairs, bf16 or fp16, any M, N and K. A is [M, K], or with
 // a_mn stored [K, M]; B is [N, K], or with b_mn stored [K, N]. tm_a and tm_b: boxes of 64 columns
 // x kGemmBoxRows rows, of a stored-transposed operand x 64 rows; tm_y and tm_pre: store maps of
-// epi.y16 and epi.pre.
+// the result (boxes of 32 16-bit or 16 fp32 columns x 32 rows) and of epi.pre.
 struct LinearProduct {
   CUtensorMap tm_a, tm_b, tm_y, tm_pre;
   int M, N, K;

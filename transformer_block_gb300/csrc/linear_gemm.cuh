@@ -221,7 +221,7 @@ __device__ __forceinline__ void load_row16(const void* src, int n, float (&v)[32
   }
 }
 
-// fp32 result of a warp's 32 x 32 chunk at y (row stride ld), of which `rows` rows and n columns
+// Without TMA: fp32 result of a warp's 32 x 32 chunk at y (row stride ld), of which `rows` rows and n columns
 // are inside the matrix: through shared memory, so that a store instruction writes whole 128-byte
 // rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q of row r sits at piece q
 // ^ (r & 7), so neither the rows' writes nor the reads meet a bank twice.
@@ -265,6 +265,54 @@ __device__ __forceinline__ void linear_store_f32(float* y, int64_t ld, int rows,
     }
   }
   __syncwarp();  // the buffer may be written again
+}
+
+// Warp-wide: the warp's 32 rows of 16 fp32 columns at col0 (lane l holds row row0 + l) to the
+// tensor of `tm`, or added to it, by one TMA copy from the buffers of tma_store_rows32 (their rows
+// are 64 bytes, too). One launch adds to an element once, so the order of adds does not matter.
+__device__ __forceinline__ void tma_store_f32x16(StoreStage& ss, const CUtensorMap* tm, int row0,
+                                                 int col0, bool add, const float* v) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t buf = ss.base + (ss.n & 1u) * 2048u;
+  if (ss.n >= 2) {  // the buffer's previous store (two ago) must have read it
+    if (lane == 0) bulk_wait_read_1();
+    __syncwarp();
+  }
+  const uint32_t rb = buf + lane * 64u, sw = (lane >> 1) & 3u;
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(rb + ((j ^ sw) << 4)),
+                 "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                 : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      tma_reduce_add_2d(tm, buf, col0, row0);
+    else
+      tma_store_2d(tm, buf, col0, row0);
+    bulk_commit();
+  }
+  ++ss.n;
+}
+
+// fp32 result of a warp's 32 rows x 32 columns, n of them inside the matrix. A TMA store cuts a
+// box off at the last column only to 16 bytes: where the columns end inside those, the last
+// chunk is stored by its lanes.
+__device__ __forceinline__ void linear_store32(StoreStage& ss, const CUtensorMap* tm, float* y,
+                                               int64_t ld, int row0, int col0, int M, int n,
+                                               bool accumulate, const float (&v)[32]) {
+  if (row0 >= M) return;
+  if (n >= 32 || n % 4 == 0) {
+    tma_store_f32x16(ss, tm, row0, col0, accumulate, v);
+    if (n > 16) tma_store_f32x16(ss, tm, row0, col0 + 16, accumulate, v + 16);
+    return;
+  }
+  if (ss.n > 0) {  // the TMA stores read the same shared memory
+    if ((threadIdx.x & 31) == 0) bulk_wait_read();
+    __syncwarp();
+  }
+  linear_store_f32(y + int64_t(row0) * ld + col0, ld, M - row0, n, accumulate, v, ss.base);
 }
 
 // 16-bit result of a warp's 32 rows x 32 columns, n of them inside the matrix. A TMA store
@@ -356,12 +404,7 @@ __device__ __forceinline__ void linear_epilogue32(const LinearEpi& e, const Line
     }
   }
   if (e.y32 != nullptr) {
-    if (ss.n > 0) {  // the pre-activation's TMA store reads the same shared memory
-      if ((threadIdx.x & 31) == 0) bulk_wait_read();
-      __syncwarp();
-    }
-    linear_store_f32(e.y32 + int64_t(row0) * e.ldy + col0, e.ldy, M - row0, n, e.accumulate, v,
-                     ss.base);
+    linear_store32(ss, &jb.tm_y, e.y32, e.ldy, row0, col0, M, n, e.accumulate, v);
   } else {
     linear_store16<F16>(ss, &jb.tm_y, e.y16, e.ldy, row0, col0, M, n, v);
   }
@@ -622,8 +665,8 @@ __global__ void __launch_bounds__(LIN_THREADS, 1)
             const int col0 = n0 + (c_first + c) * 32;
             if (col0 >= N || row0 >= M) break;
             if (u.slot < 0)
-              linear_store_f32(e.y32 + int64_t(row0) * e.ldy + col0, e.ldy, M - row0, N - col0,
-                               e.accumulate, sum[c], ss.base);
+              linear_store32(ss, &jb.tm_y, e.y32, e.ldy, row0, col0, M, N - col0, e.accumulate,
+                             sum[c]);
             else if (row0 + int(lane) < M)
               linear_store_part(dst + (c_first + c) * 1024, sum[c]);
           }

@@ -326,6 +326,22 @@ pb_status make_store_map(CUtensorMap* m, const void* base, uint64_t rows, uint64
   return PB_OK;
 }
 
+// As make_store_map for an fp32 output: boxes of 16 columns x 32 rows.
+pb_status make_store_map_f32(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                             uint64_t ld) {
+  EncodeTiledFn enc;
+  pb_status s = get_encoder(&enc);
+  if (s != PB_OK) return s;
+  const cuuint64_t gd[2] = {cols, rows};
+  const cuuint64_t gs[1] = {ld * 4};
+  const cuuint32_t bx[2] = {16, 32}, es[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), gd, gs, bx, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PB_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return PB_OK;
+}
+
 // Row-major [rows, cols] matrix of element type t read in boxes of 128 bytes of columns
 // (64 16-bit or 128 FP8 elements) x box_rows rows.
 pb_status make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
@@ -1639,8 +1655,9 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
   s = make_map_2d(&p.tm_a, a.x, x.rows, x.cols, x.ld, pb::kGemmBoxRows, op);
   if (s == PB_OK)
     s = make_map_2d(&p.tm_b, a.w, w.rows, w.cols, w.ld, in_out ? 64 : pb::kGemmBoxRows, op);
-  if (s == PB_OK && y.esz == 2)
-    s = make_store_map(&p.tm_y, a.y, y.rows, y.cols, y.ld, op == pb::kOpF16);
+  if (s == PB_OK)
+    s = y.esz == 4 ? make_store_map_f32(&p.tm_y, a.y, y.rows, y.cols, y.ld)
+                   : make_store_map(&p.tm_y, a.y, y.rows, y.cols, y.ld, op == pb::kOpF16);
   if (s == PB_OK && a.pre != nullptr)
     s = make_store_map(&p.tm_pre, a.pre, pre.rows, pre.cols, pre.ld, op == pb::kOpF16);
   if (s != PB_OK) return s;
@@ -1754,6 +1771,7 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     q.a_mn = q.b_mn = true;
     s = make_map_2d(&q.tm_a, ra.p, ra.rows, ra.cols, ra.ld, 64, op);
     if (s == PB_OK) s = make_map_2d(&q.tm_b, rb.p, rb.rows, rb.cols, rb.ld, 64, op);
+    if (s == PB_OK) s = make_store_map_f32(&q.tm_y, a.dw, dw.rows, dw.cols, dw.ld);
     if (s != PB_OK) return s;
     q.epi.y32 = a.dw;
     q.epi.ldy = a.lddw;
