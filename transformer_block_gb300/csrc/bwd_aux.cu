@@ -53,6 +53,10 @@ __global__ void attn_delta_kernel(const __nv_bfloat16* __restrict__ dO,
     const int64_t b = t / S, i = t % S;
     delta[(b * nh + head) * lse_ld + i] = acc;
   }
+  // The attention's tiles reach behind the last query: their P is 0 there, and 0 (dP - D) has
+  // to be 0, not the product with whatever the scratch memory held.
+  if (t % S == S - 1)
+    for (int64_t i = S + lane; i < lse_ld; i += 32) delta[(t / S * nh + head) * lse_ld + i] = 0.f;
 }
 
 __global__ void dq_to_bf16_kernel(const float* __restrict__ dq, int64_t T, int H, float scale,
