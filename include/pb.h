@@ -472,8 +472,9 @@ pb_status pb_qk_norm_rope(const pb_rope* rope, int32_t batch, int32_t seq, const
  * its inputs (bf16) and of gamma_q, gamma_k (fp32 [head_dim]; NULL skips one; accumulate != 0
  * adds to what is there). A result may be its own dq (dk) or q (k). `scratch` (device,
  * 256-byte aligned, >= pb_qk_norm_rope_scratch_bytes) is needed where there is a gamma and
- * must not be used by another call that may run concurrently. Sums over tokens and heads are
- * taken in a fixed order. batch or seq 0 gives zero sums. */
+ * must not be used by another call that may run concurrently. dgamma_q, dgamma_k and scratch
+ * overlap nothing else (one gamma for both: two gradients, added by the caller). Sums over
+ * tokens and heads are taken in a fixed order. batch or seq 0 gives zero sums. */
 pb_status pb_qk_norm_rope_scratch_bytes(size_t* bytes);
 pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t seq,
                                    const pb_heads* q, const pb_heads* k, const void* gamma_q,
@@ -567,9 +568,10 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
  * (dtype), dw = x^T dy in w's layout (fp32), db [n] = the sum of dy's rows (fp32, in a fixed
  * order); NULL skips one. Where x is activation(pre) of the layer before, give its pre [m, k]:
  * dx is then the gradient of pre, dy w^T * activation'(pre), ready as that layer's dy.
- * accumulate != 0 adds dw and db to what is there (dx is always overwritten); with m = 0 they
- * are zero. The gradient of the residual is dy itself. ld*, pointers, scratch and status as
- * in pb_linear. Results overlap nothing else. */
+ * accumulate != 0 adds dw and db to what is there (dx is always overwritten; a value below
+ * 2^-126 may count as zero in dw's addition); with m = 0 they are zero. The gradient of the
+ * residual is dy itself. ld*, pointers, scratch and status as in pb_linear. Results overlap
+ * nothing else. */
 typedef struct pb_linear_grads {
   int32_t m, n, k;
   int32_t dtype;

@@ -131,3 +131,100 @@ def test_several_host_threads_at_once():
     for t in threads:
         t.join()
     assert not wrong
+
+
+# Every call for the first time in a process while a graph is captured, behind a copy and a
+# join of two streams; then the graph twice against the same calls without one.
+FIRST_IN_CAPTURE = """
+import torch
+from transformer_block_gb300 import pb
+torch.manual_seed(0)
+dev = "cuda"
+bf = torch.bfloat16
+x = torch.randn(333, 1032, device=dev).to(bf); w = torch.randn(1032, 264, device=dev).to(bf)
+src = torch.randn_like(x); one = x[:3]
+q = torch.randn(2, 65, 4, 64, device=dev).to(bf); gamma = torch.rand(64, device=dev).to(bf)
+n = 70001
+p = torch.randn(n, device=dev); grad = torch.randn(n, device=dev)
+opt = pb.AdamW([dict(param=p, grad=grad, **pb.adamw_states(p))])
+rope = pb.Rope(64)
+scratch = torch.empty(pb.linear_scratch_bytes(), dtype=torch.uint8, device=dev)
+d_step = torch.ones(1, dtype=torch.int32, device=dev)
+start = p.clone()
+
+def calls():
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    x.copy_(src)
+    with torch.cuda.stream(side):
+        k = pb.qk_norm_rope(rope, q, q, None, gamma, gamma)[1]
+    torch.cuda.current_stream().wait_stream(side)
+    back = pb.qk_norm_rope_backward(rope, q, None, None, k, None, gamma)
+    y = pb.linear(x, w, activation="gelu", scratch=scratch)
+    z = pb.linear(one, w)
+    g = pb.linear_backward(y, x, w, bias=True, scratch=scratch)
+    a = pb.activation_backward(y, y, "silu")
+    norm = opt.grad_norm(1.0)
+    opt.step(lr=1e-3, d_step=d_step, grad_scale=norm[1:])
+    return [k, back[0], back[2], y, z, *g, a, norm]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = calls()
+for _ in range(2):
+    for t in out:
+        t.fill_(float("nan"))
+    x.zero_()
+    graph.replay()
+torch.cuda.synchronize()
+got, stepped = [t.clone() for t in out], p.clone()
+p.copy_(start); opt.tensors[0]["m"].zero_(); opt.tensors[0]["v"].zero_()
+for _ in range(2):
+    want = calls()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+assert torch.equal(stepped, p)
+print("equal")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-3000:]
+
+
+def test_two_graphs_on_two_streams_with_scratches_of_their_own():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(333, 4104, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(4104, 520, generator=g, device="cuda").to(torch.bfloat16)
+    few = x[:20]
+    graphs, outs, streams = [], [], []
+    for _ in range(2):
+        scratch = torch.empty(pb.linear_scratch_bytes(), dtype=torch.uint8, device="cuda")
+        want = [pb.linear(x, w, scratch=scratch), pb.linear(few, w, scratch=scratch),
+                pb.linear_backward(want_dy(333, 520), x, w, scratch=scratch)[1]]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = [pb.linear(x, w, scratch=scratch), pb.linear(few, w, scratch=scratch),
+                   pb.linear_backward(want_dy(333, 520), x, w, scratch=scratch)[1]]
+        graphs.append((graph, scratch))
+        outs.append(out)
+        streams.append(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (graph, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def want_dy(m, n):
+    i = torch.arange(m * n, device="cuda", dtype=torch.float32)
+    return torch.sin(i).view(m, n).to(torch.bfloat16)

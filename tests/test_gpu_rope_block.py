@@ -393,3 +393,26 @@ def test_guarded_buffers():
     torch.cuda.synchronize()
     for i, buf in enumerate(bufs):
         assert (buf[:G] == C).all() and (buf[-G:] == C).all(), i
+
+
+def test_block_rotation_gradients_apart():
+    wl, _ = CASES[0]
+    _, _, block = make(wl)
+    d = block.dims
+    n = d.batch * d.seq * d.hidden * 4
+    gamma = torch.ones(d.head_dim, dtype=torch.bfloat16, device="cuda")
+    grads = torch.zeros(2 * d.head_dim, dtype=torch.float32, device="cuda")
+    saved = torch.empty(n, dtype=torch.uint8, device="cuda")
+    at, g = grads.data_ptr(), gamma.data_ptr()
+
+    def refused(dgq, dgk):
+        r = pb.pb_block_rope(pb.Rope(d.head_dim).plan, g, g, 1e-6, None, saved.data_ptr(), n, dgq,
+                             dgk)
+        with pytest.raises(pb.PbError, match="apart"):
+            pb._check("pb_set_qk_norm_rope",
+                      pb.lib().pb_set_qk_norm_rope(block.handle, pb.ctypes.byref(r)))
+
+    refused(at, at)
+    refused(at, at + 4 * d.head_dim - 4)
+    refused(saved.data_ptr() + n - 4, at)
+    refused(at, saved.data_ptr())

@@ -259,3 +259,81 @@ def test_grad_norm_refused(lib):
 
 def test_block_rotation_needs_a_handle(lib):
     assert lib.pb_set_qk_norm_rope(None, None) == 6
+
+
+# --------------------------------------------------------------------------- overlaps, extremes
+
+def rope_back2(lib, plan, gq, gk, dgq, dgk, scratch, pos=None, out=P + 0x2000000, accumulate=1):
+    """The backward pass of q and k (its views lie between P and P + 0x4000000)."""
+    return lib.pb_qk_norm_rope_backward(
+        ctypes.byref(plan), 2, 8, heads(P), heads(P + 0x800000), gq, gk, 1e-6, pos,
+        heads(P + 0x1000000), heads(P + 0x1800000), heads(out), heads(out + 0x800000), dgq, dgk,
+        accumulate, scratch, pb.qk_norm_rope_scratch_bytes(), None)
+
+
+def test_rotation_gradients_of_gammas_apart(lib):
+    plan = init(lib)[1]
+    g, d, w = P + 0x4000000, P + 0x5000000, P + 0x6000000
+    for kw in (dict(dgk=d),                                 # one buffer for both sums
+               dict(dgk=d + 508), dict(dgk=w + 4096),       # part of it, in scratch
+               dict(dgk=g), dict(dgk=P), dict(dgk=P + 0x1000000), dict(dgk=P + 0x2800000),
+               dict(scratch=P), dict(scratch=P + 0x1800000), dict(scratch=P + 0x2000000),
+               dict(scratch=g), dict(pos=d + 64), dict(pos=w), dict(pos=P + 0x2000000),
+               dict(gq=P + 0x2000000), dict(gk=P + 0x2800000 + 256)):
+        args = dict(gq=g, gk=g, dgq=d, dgk=d + 512, scratch=w) | kw
+        assert rope_back2(lib, plan, **args) == 1, kw
+        assert "overlaps" in message(lib), kw
+    # the forward call
+    for kw in (dict(gq=P + 0x1000000), dict(gk=P + 0x1000000 + 64, k=heads(P + 0x100000),
+                                            ko=heads(P + 0x2000000)), dict(pos=P + 0x1000040)):
+        assert rope_call(lib, plan, q=heads(), qo=heads(P + 0x1000000), **kw) == 1, kw
+        assert "overlaps" in message(lib), kw
+
+
+def test_linear_extremes_refused(lib):
+    top = 2 ** 31 - 1
+    for kw in (dict(n=top, ldw=2 ** 31, ldy=2 ** 31), dict(m=top), dict(k=top, ldx=2 ** 31),
+               dict(k=2 ** 31 - 1024, ldx=2 ** 31)):
+        assert linear(lib, **kw) == 2, kw
+        assert "2^31" in message(lib)
+    assert linear_back(lib, n=top, lddy=2 ** 31, ldw=2 ** 31, lddw=2 ** 31) == 2
+    # a stride and a number of rows whose product passes 64 bits in bytes
+    assert linear(lib, m=1 << 30, ldx=1 << 33) == 2 and "2^48" in message(lib)
+    assert lib.pb_activation_backward((1 << 40) - 1, 64, 0, 1, P, 1 << 34, P, 1 << 34, P,
+                                      1 << 34, None) == 2
+
+
+def test_adamw_scalars_and_norm_apart(lib):
+    for name in ("d_lr", "d_step", "d_grad_scale"):
+        for at in (P, P + 0x20000 + 396, P + 0x30000):       # param, m, v
+            assert adamw(lib, **{name: at}) == 1 and "overlaps" in message(lib)
+    arr = (pb.pb_adamw_tensor * 2)(tensor(n=0), tensor())
+    n = ctypes.c_size_t()
+    lib.pb_grad_norm_scratch_bytes(2, ctypes.byref(n))
+    far = P + 0x1000000
+    for out, scratch in ((P + 0x10000 + 3996, far), (P, P + 0x10000), (far, far),
+                         (far + n.value - 4, far), (P, P + 0x10000 - 256)):
+        assert lib.pb_grad_norm(2, arr, 2, 1.0, out, scratch, n.value, None) == 1
+        assert "overlaps" in message(lib)
+
+
+def test_positions_in_another_order_refused():
+    import torch
+    three = pb.Rope(64, sections=[16, 8, 8])
+    one = pb.Rope(64)
+
+    def pos(*shape):
+        return torch.zeros(*shape, dtype=torch.int32)
+
+    for rope, good, bad in ((three, [(3, 2, 5), (30,)], [(2, 3, 5), (2, 5, 3), (3, 5, 2), (3, 10)]),
+                            (one, [(1, 2, 5), (2, 5), (10,), (2, 5, 1)], [(5, 2), (1, 5, 2)])):
+        for shape in good:
+            assert pb._positions(rope, pos(*shape), 2, 5) is not None
+        for shape in bad:
+            with pytest.raises(ValueError, match="positions"):
+                pb._positions(rope, pos(*shape), 2, 5)
+    assert pb._positions(three, pos(3, 5), 1, 5) is not None      # one sequence
+    assert pb._positions(three, pos(3, 2), 2, 1) is not None      # one token each
+    for p in (pos(3, 2, 4), pos(31), pos(3, 2, 5).long()):
+        with pytest.raises(ValueError):
+            pb._positions(three, p, 2, 5)

@@ -515,7 +515,7 @@ pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_
   if (s != PB_OK) return s;
   std::vector<Span> spans;
   try {
-    spans.reserve(size_t(n_tensors) * 7);
+    spans.reserve(size_t(n_tensors) * 7 + 3);
   } catch (...) {
     return record_error(PB_ERR_INVALID_ARG, "host allocation for the checks failed");
   }
@@ -558,13 +558,21 @@ pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_
       add(t.v_scale, blocks * 4, true);
     }
   }
+  for (const void* p : scalars)
+    if (p != nullptr) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      spans.push_back(Span{at, at + 4, -1, false});
+    }
   // No written buffer shares bytes with another one: blocks work on all tensors at once, and
   // a tensor that is listed twice would be stepped twice in no order.
   std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
   uintptr_t written_to = 0, any_to = 0;
   for (const Span& x : spans) {
     if (x.a < written_to || (x.written && x.a < any_to))
-      return bad(PB_ERR_INVALID_ARG, x.tensor, "a buffer that the step writes overlaps another");
+      return x.tensor < 0 ? record_error(PB_ERR_INVALID_ARG,
+                                         "d_lr, d_step or d_grad_scale overlaps a tensor")
+                          : bad(PB_ERR_INVALID_ARG, x.tensor,
+                                "a buffer that the step writes overlaps another");
     any_to = std::max(any_to, x.b);
     if (x.written) written_to = std::max(written_to, x.b);
   }
@@ -627,6 +635,15 @@ pb_status pb_grad_norm(int32_t n_tensors, const pb_adamw_tensor* tensors, int32_
     return record_error(PB_ERR_INVALID_ARG, "scratch must be a 256-byte aligned device pointer");
   if (scratch_bytes < need)
     return record_error(PB_ERR_WORKSPACE, "scratch is smaller than pb_grad_norm_scratch_bytes");
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), w = reinterpret_cast<uintptr_t>(scratch);
+  if (o < w + need && w < o + 8)
+    return record_error(PB_ERR_INVALID_ARG, "out overlaps scratch");
+  for (int i = 0; i < n_tensors; ++i) {
+    const uintptr_t g = reinterpret_cast<uintptr_t>(tensors[i].grad);
+    const uintptr_t end = g + uintptr_t(tensors[i].n) * (grad_dtype == PB_DTYPE_BF16 ? 2 : 4);
+    if (tensors[i].n > 0 && ((g < o + 8 && o < end) || (g < w + need && w < end)))
+      return bad(PB_ERR_INVALID_ARG, i, "grad overlaps out or scratch");
+  }
   int sms = 0;
   s = sm_count(&sms);
   if (s != PB_OK) return s;

@@ -884,6 +884,8 @@ pb_status check_matrix(const Matrix& m, const char* name) {
                 name, (long long)m.cols, (long long)(16 / m.esz));
   if (m.ld > (int64_t(1) << 34))  // a tensor map's stride has 40 bits
     return fail(PB_ERR_UNSUPPORTED, "%s: the row stride is beyond 2^34", name);
+  if (m.rows > (int64_t(1) << 48) / m.ld)  // byte offsets stay in 64 bits
+    return fail(PB_ERR_UNSUPPORTED, "%s: more than 2^48 values from the first to the last", name);
   return PB_OK;
 }
 
@@ -902,6 +904,10 @@ pb_status check_linear_sizes(int32_t m, int32_t n, int32_t k, int32_t dtype, int
     return fail(PB_ERR_INVALID_ARG, "w_layout %d is not a pb_weight_layout", layout);
   if (act < PB_ACT_NONE || act > PB_ACT_RELU)
     return fail(PB_ERR_INVALID_ARG, "activation %d is not a pb_activation", act);
+  // tiles end up to 256 rows or columns behind the matrix, in 32-bit coordinates
+  const int32_t longest = 0x7fffffff - 1024;
+  if (m > longest || n > longest || k > longest)
+    return fail(PB_ERR_UNSUPPORTED, "m, n or k is beyond 2^31 - 1025");
   // the GEMM counts its 256 x 256 tiles in 32 bits
   const int64_t big = (int64_t(1) << 30) * 65536;
   if (int64_t(m) * n > big || int64_t(m) * k > big || int64_t(n) * k > big)
@@ -1396,6 +1402,12 @@ pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r) {
   if (s != PB_OK) return s;
   if (!aligned(r->dgamma_q, 4) || !aligned(r->dgamma_k, 4))
     return fail(PB_ERR_INVALID_ARG, "dgamma_q and dgamma_k must be 4-byte aligned");
+  const size_t dg = size_t(h->d.head_dim) * 4;
+  if ((r->dgamma_q != nullptr && r->dgamma_k != nullptr &&
+       overlap(r->dgamma_q, dg, r->dgamma_k, dg)) ||
+      (r->saved != nullptr && ((r->dgamma_q != nullptr && overlap(r->dgamma_q, dg, r->saved, need)) ||
+                               (r->dgamma_k != nullptr && overlap(r->dgamma_k, dg, r->saved, need)))))
+    return fail(PB_ERR_INVALID_ARG, "dgamma_q, dgamma_k and saved must be apart");
   h->rope = *r;
   h->has_rope = true;
   return PB_OK;

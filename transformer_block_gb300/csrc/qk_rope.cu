@@ -554,6 +554,23 @@ bool disjoint(const pb_heads& a, const pb_heads& b, int batch, int seq, int dh) 
   return false;
 }
 
+// A vector argument beside the views.
+struct Flat {
+  const void* p;
+  size_t bytes;
+};
+
+bool apart(const Flat& f, const Flat& g) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(f.p), b = reinterpret_cast<uintptr_t>(g.p);
+  return f.p == nullptr || g.p == nullptr || a + f.bytes <= b || b + g.bytes <= a;
+}
+// From the view's first value to its last.
+bool apart(const Flat& f, const pb_heads* v, int batch, int seq, int dh) {
+  if (v == nullptr) return true;
+  Dim d[3];
+  return apart(f, Flat{v->ptr, size_t(extent(*v, batch, seq, dh, d)) * 2});
+}
+
 pb_status check_view(const pb_heads* v, const char* what, int batch, int seq, int dh, bool out) {
   if (v->heads < 1) return bad(PB_ERR_INVALID_ARG, "%s: heads must be >= 1", what);
   if (v->ptr == nullptr || !aligned16(v->ptr))
@@ -752,6 +769,13 @@ pb_status pb_qk_norm_rope(const pb_rope* rope, int32_t batch, int32_t seq, const
     }
   if (q_out != nullptr && k_out != nullptr && !disjoint(*q_out, *k_out, batch, seq, dh))
     return record_error(PB_ERR_INVALID_ARG, "q_out and k_out overlap");
+  const Flat read[3] = {{gamma_q, size_t(dh) * 2},
+                        {gamma_k, size_t(dh) * 2},
+                        {positions, size_t(rope->axes) * batch * seq * 4}};
+  for (const Flat& r : read)
+    for (int t = 0; t < 2; ++t)
+      if (!apart(r, out[t], batch, seq, dh))
+        return bad(PB_ERR_INVALID_ARG, "%s overlaps a gamma or the positions", out_name[t]);
 
   Params p{};
   int sms = 0;
@@ -847,6 +871,28 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
         return record_error(PB_ERR_WORKSPACE,
                             "scratch is smaller than pb_qk_norm_rope_scratch_bytes");
     }
+  }
+  // the gammas' gradients and the scratch: apart from one another and from all else
+  const Flat written[3] = {{dgamma_q, size_t(dh) * 4},
+                           {dgamma_k, size_t(dh) * 4},
+                           {sums ? scratch : nullptr, kPartialBytes}};
+  const Flat read[3] = {{gamma_q, size_t(dh) * 2},
+                        {gamma_k, size_t(dh) * 2},
+                        {positions, none ? 0 : size_t(rope->axes) * batch * seq * 4}};
+  for (int i = 0; i < 3; ++i) {
+    bool clear = true;
+    for (int o = 0; o < 3; ++o)
+      clear = clear && apart(written[i], read[o]) && (o == i || apart(written[i], written[o]));
+    for (int t = 0; t < 2 && !none; ++t) {
+      clear = clear && apart(written[i], dy[t], batch, seq, dh) &&
+              apart(written[i], out[t], batch, seq, dh) &&
+              (dy[t] == nullptr || gamma[t] == nullptr || apart(written[i], x[t], batch, seq, dh));
+      if (!apart(read[i], out[t], batch, seq, dh))
+        return bad(PB_ERR_INVALID_ARG, "%s overlaps a gamma or the positions", out_name[t]);
+    }
+    if (!clear)
+      return record_error(PB_ERR_INVALID_ARG,
+                          "dgamma_q, dgamma_k or scratch overlaps another argument");
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (none) {  // no tokens: the sums over them are zero

@@ -685,6 +685,10 @@ def _heads(t, head_dim: int, b: int, s: int, what: str):
 def _positions(rope, positions, b: int, s: int):
     if positions is None:
         return None
+    # the same values in another order have as many: an order shows in the lengths beyond 1
+    if positions.dim() > 1 and [n for n in positions.shape if n != 1] != \
+            [n for n in (rope.axes, b, s) if n != 1]:
+        raise ValueError(f"positions must be [{rope.axes}, {b}, {s}] (axes, batch, seq)")
     return _flat(positions, rope.axes * b * s, torch.int32, "positions ([axes, batch, seq])")
 
 
@@ -777,7 +781,8 @@ def linear(x, w, bias=None, residual=None, activation: str = "none",
            status=None, stream=None):
     """``pb_linear``: ``activation(x @ w + bias) + residual`` for ``x`` [m, k] and ``w`` [k, n]
     (or [n, k], ``PB_WEIGHT_OUT_IN``), bf16 or fp16; ``out_dtype`` (or ``out``'s) is theirs or
-    fp32. ``pre`` (a [m, n] tensor of their type) receives ``x @ w + bias``. ``scratch`` (a
+    fp32, and a new one's rows start on 16-byte boundaries (a view where n is odd). ``pre`` (a
+    [m, n] tensor of their type) receives ``x @ w + bias``. ``scratch`` (a
     uint8 CUDA tensor of ``linear_scratch_bytes()``) lets the product be split along k."""
     if stream is not None:
         return _run_on(stream, linear, x, w, bias, residual, activation, layout, out, out_dtype,
