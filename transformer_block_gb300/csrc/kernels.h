@@ -213,10 +213,18 @@ struct LinearProduct {
   bool a_mn, b_mn;
   LinearEpi epi;
 };
-// One product, or two at once (that depend on nothing of one another). scratch:
-// kLinearScratchBytes, 256-byte aligned, or null: every tile is computed whole.
-cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, void* scratch,
-                          int* status, uint64_t limit_ns, cudaStream_t stream);
+// out [cols] (+)= the sums of the columns of m [rows, cols] (linear.cu).
+struct RowSums {
+  const void* m;  // null: none
+  int64_t rows, cols, ld;
+  float* out;
+  bool accumulate;
+};
+// One product, or two at once (that depend on nothing of one another), and beside them row sums
+// that do not depend on them either. scratch: kLinearScratchBytes, 256-byte aligned, or null:
+// every tile is computed whole.
+cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, const RowSums& sums,
+                          void* scratch, int* status, uint64_t limit_ns, cudaStream_t stream);
 
 // linear.cu
 // Few rows of A: D = A * B^T with B [N, K] or, b_mn, stored [K, N]. tmA: A
@@ -244,8 +252,7 @@ cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, 
                                 int64_t ld_out, cudaStream_t stream);
 // out[c] (+)= sum over rows of m[r, c] (16-bit values, 16-byte rows, any cols), in a fixed
 // order.
-cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols, int64_t ld,
-                            float* out, bool accumulate, cudaStream_t stream);
+cudaError_t launch_row_sums(OpType op, const RowSums& sums, bool beside, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention (swa.cu)
 struct SwaParams {

@@ -106,12 +106,12 @@ struct FewGeo {
 
 // Up to 8 values of 16 bits, the first n of them; zero behind.
 __device__ __forceinline__ uint4 ld_part(const uint16_t* p, int n) {
-  if (n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
+  if (n >= 8) return __ldcg(reinterpret_cast<const uint4*>(p));
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = (2 * i < n ? uint32_t(__ldg(p + 2 * i)) : 0u) |
-           (2 * i + 1 < n ? uint32_t(__ldg(p + 2 * i + 1)) << 16 : 0u);
+    w[i] = (2 * i < n ? uint32_t(__ldcg(p + 2 * i)) : 0u) |
+           (2 * i + 1 < n ? uint32_t(__ldcg(p + 2 * i + 1)) << 16 : 0u);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -493,13 +493,20 @@ __global__ void __launch_bounds__(256)
 // Cluster: 64 columns; its CTAs: equal parts of the rows; 8 threads across (16 bytes each), 32
 // rows at a time, four such loads of a thread in flight. Sums over a CTA's threads, then over
 // the cluster in distributed shared memory, in a fixed order.
+//
+// beside: the launch before on the stream is linear_kernel, of which the sums need
+// nothing. Its blocks have all passed their pdl_wait when this one begins, so everything before
+// it is complete; it itself is only waited for at the end, so that this launch is not complete
+// before it. The sums then fill SMs that its last tiles leave idle (777 x 4104 x 2056 backward:
+// 7.1 us in front of it, 1.3 beside). Values are read from the L2 cache, where all that
+// is complete has arrived.
 constexpr int SUM_COLS = 64;
 template <bool F16>
 __global__ void __launch_bounds__(256)
     row_sum_kernel(const uint16_t* m, int64_t rows, int64_t cols, int64_t ld, int parts, float* out,
-                   bool accumulate) {
+                   bool accumulate, bool beside) {
   __shared__ float red[8][SUM_COLS];
-  pdl_wait();
+  if (!beside) pdl_wait();
   pdl_trigger();
   const int tx = int(threadIdx.x) & 7, ty = int(threadIdx.x) >> 3;
   const int rank = int(blockIdx.x) % parts;
@@ -557,7 +564,8 @@ __global__ void __launch_bounds__(256)
     cluster_sync();  // no CTA leaves while its sums may still be read
   }
   if (rank == 0 && threadIdx.x < SUM_COLS && c0 + threadIdx.x < cols)
-    out[c0 + threadIdx.x] = accumulate ? out[c0 + threadIdx.x] + v : v;
+    out[c0 + threadIdx.x] = accumulate ? __ldcg(out + c0 + threadIdx.x) + v : v;
+  if (beside) pdl_wait();
 }
 
 }  // namespace
@@ -588,15 +596,15 @@ cudaError_t launch_act_backward(OpType op, int act, int64_t rows, int64_t cols, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_row_sums(OpType op, const void* m, int64_t rows, int64_t cols, int64_t ld,
-                            float* out, bool accumulate, cudaStream_t stream) {
-  if (rows < 1 || cols < 1) return cudaSuccess;
+cudaError_t launch_row_sums(OpType op, const RowSums& s, bool beside, cudaStream_t stream) {
+  if (s.rows < 1 || s.cols < 1) return cudaSuccess;
   // up to eight CTAs share a cluster's rows, 128 rows each at least
-  const int parts = rows >= 1024 ? 8 : rows <= 128 ? 1 : int(rows / 128);
-  const dim3 grid(unsigned((cols + SUM_COLS - 1) / SUM_COLS) * unsigned(parts), 1, 1);
+  const int parts = s.rows >= 1024 ? 8 : s.rows <= 128 ? 1 : int(s.rows / 128);
+  const dim3 grid(unsigned((s.cols + SUM_COLS - 1) / SUM_COLS) * unsigned(parts), 1, 1);
   return launch_dependent(op == kOpF16 ? row_sum_kernel<true> : row_sum_kernel<false>, grid,
                           dim3(256, 1, 1), 0, unsigned(parts), stream,
-                          static_cast<const uint16_t*>(m), rows, cols, ld, parts, out, accumulate);
+                          static_cast<const uint16_t*>(s.m), s.rows, s.cols, s.ld, parts, s.out,
+                          s.accumulate, beside);
 }
 
 }  // namespace pb

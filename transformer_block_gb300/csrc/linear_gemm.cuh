@@ -4,18 +4,17 @@
 // division of the work.
 //
 // * One launch may hold two products (the backward pass's dx and dW), so the tiles of one fill
-//   the waves of the other: apart, 36 tiles of 65 k-blocks and 153 of 13 took 24 + 9 us (split
-//   along K, and summed) and 25 us.
+//   the waves of the other (36 tiles of 65 k-blocks and 153 of 13: 33 us; apart 25, split along K
+//   and summed, and 22).
 // * Tiles that would leave pairs idle are split along K; the parts' sums go to scratch and a
 //   second launch over all SMs adds them up in a fixed order and finishes the tiles. Nothing
 //   waits inside a launch, whatever else runs on the GPU.
 // * fp32 results: the tensor core cuts its sums off instead of rounding them, which leaves 1.0e-6
 //   of relative error at K = 1024 and, growing with K, 8.6e-6 at 8192, against 0.3e-6 and 1.1e-6
 //   of a chain of fp32 fused multiply-adds. So an accumulator sums 896 k at most, and the
-//   epilogue warps add such segments up in registers, rounding, while the products go on in the other
-//   accumulator. Reading one costs the products about 0.4 us (2048 x 2048 x 8192: 45.1 us in one
-//   chain, 46.9 in segments of 2048 k, 48.5 of 1024). A 16-bit result rounds at 2^-9 and is
-//   summed in one chain.
+//   epilogue warps add such segments up in registers, rounding, while the products go on in the
+//   other accumulator (2048 x 2048 x 8192: 42.8 us in one chain, 43.3 in segments of 1792 k, 44.9
+//   of 896). A 16-bit result rounds at 2^-9 and is summed in one chain.
 // * Eight epilogue warps, each quarter of the tensor memory's lanes shared by two: four do not
 //   hide a pre-activation's loads and GeLU' behind a main loop of K = 2048 (8192 x 8192 x 2048:
 //   224 us with four, 176 with eight).
@@ -23,7 +22,8 @@
 // Bound by the tensor rate for many tokens: 8192 x 20480 x 5120 with GeLU and the stored
 // pre-activation runs at 1870 TFLOP/s in short bursts (95 % of cuBLAS's measured 1967), 1560 over
 // seconds, where the power limit holds both down. A single wave costs 6.5 us (launch, first
-// loads, epilogue, stores) and 0.28 us a k-block.
+// loads, epilogue, stores) and 0.27 us a k-block for one pair; with all pairs at work and operands
+// read for the first time 0.33 to 0.41, the memory's latency and rate.
 
 namespace {
 
@@ -221,10 +221,10 @@ __device__ __forceinline__ void load_row16(const void* src, int n, float (&v)[32
   }
 }
 
-// Without TMA: fp32 result of a warp's 32 x 32 chunk at y (row stride ld), of which `rows` rows and n columns
-// are inside the matrix: through shared memory, so that a store instruction writes whole 128-byte
-// rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q of row r sits at piece q
-// ^ (r & 7), so neither the rows' writes nor the reads meet a bank twice.
+// Without TMA: fp32 result of a warp's 32 x 32 chunk at y (row stride ld), of which `rows` rows
+// and n columns are inside the matrix: through shared memory, so that a store instruction writes
+// whole 128-byte rows. stage: the warp's 4 KB (its TMA-store buffers); 16-byte piece q of row r
+// sits at piece q ^ (r & 7), so neither the rows' writes nor the reads meet a bank twice.
 __device__ __forceinline__ void linear_store_f32(float* y, int64_t ld, int rows, int n,
                                                  bool accumulate, const float (&v)[32],
                                                  uint32_t stage) {
@@ -815,8 +815,8 @@ LinearClass split_class(int job, int first_tile, int tiles, int num_kb, int pair
 }
 
 template <bool F16>
-cudaError_t launch_linear_work(LinearWork& w, int jobs, float* scratch, int* status,
-                               uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_linear_work(LinearWork& w, int jobs, const RowSums& sums, float* scratch,
+                               int* status, uint64_t limit_ns, cudaStream_t stream) {
   static PerDeviceInit setup;  // per device: shared-memory opt-in and co-resident pairs
   int pairs = 0;
   const cudaError_t err = per_device_init(
@@ -895,6 +895,8 @@ cudaError_t launch_linear_work(LinearWork& w, int jobs, float* scratch, int* sta
   }
   cudaError_t e = launch_dependent(linear_kernel<F16>, dim3(grid, 1, 1), dim3(LIN_THREADS, 1, 1),
                                    LIN_SMEM, 2, stream, w, status, limit_ns);
+  if (e == cudaSuccess && sums.m != nullptr)
+    e = launch_row_sums(F16 ? kOpF16 : kOpBf16, sums, true, stream);
   for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
     const LinearClass& c = w.cls[k];
     if (c.split < 2) continue;
@@ -908,8 +910,8 @@ cudaError_t launch_linear_work(LinearWork& w, int jobs, float* scratch, int* sta
 
 }  // namespace
 
-cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, void* scratch,
-                          int* status, uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, const RowSums& sums,
+                          void* scratch, int* status, uint64_t limit_ns, cudaStream_t stream) {
   if (count < 1 || count > 2) return cudaErrorInvalidValue;
   LinearWork w{};
   for (int j = 0; j < count; ++j) {
@@ -933,6 +935,6 @@ cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, v
     jb.b_mn = p.b_mn;
   }
   float* s = static_cast<float*>(scratch);
-  return op == kOpF16 ? launch_linear_work<true>(w, count, s, status, limit_ns, stream)
-                      : launch_linear_work<false>(w, count, s, status, limit_ns, stream);
+  return op == kOpF16 ? launch_linear_work<true>(w, count, sums, s, status, limit_ns, stream)
+                      : launch_linear_work<false>(w, count, sums, s, status, limit_ns, stream);
 }

@@ -1673,7 +1673,7 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
   if (s == PB_OK && a.pre != nullptr)
     s = make_store_map(&p.tm_pre, a.pre, pre.rows, pre.cols, pre.ld, op == pb::kOpF16);
   if (s != PB_OK) return s;
-  PB_CUDA(pb::launch_linear(op, &p, 1, scratch, status, kDefaultLimitNs, st), "linear launch");
+  PB_CUDA(pb::launch_linear(op, &p, 1, pb::RowSums{}, scratch, status, kDefaultLimitNs, st), "linear launch");
   return PB_OK;
 }
 
@@ -1729,9 +1729,8 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     }
     return PB_OK;
   }
-  if (a.db != nullptr)
-    PB_CUDA(pb::launch_row_sums(op, a.dy, a.m, a.n, a.lddy, a.db, a.accumulate != 0, st),
-            "bias gradient launch");
+  const pb::RowSums sums{a.db != nullptr ? a.dy : nullptr, a.m, a.n, a.lddy, a.db,
+                         a.accumulate != 0};
   pb::LinearProduct p[2] = {};
   int count = 0;
   if (a.dx != nullptr) {
@@ -1791,8 +1790,10 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
     ++count;
   }
   if (count > 0)
-    PB_CUDA(pb::launch_linear(op, p, count, scratch, status, kDefaultLimitNs, st),
+    PB_CUDA(pb::launch_linear(op, p, count, sums, scratch, status, kDefaultLimitNs, st),
             "linear backward launch");
+  else if (sums.m != nullptr)
+    PB_CUDA(pb::launch_row_sums(op, sums, false, st), "bias gradient launch");
   return PB_OK;
 }
 

@@ -160,7 +160,9 @@ __device__ __forceinline__ void cluster_sync() {
 // Dependent launches (launch_dependent in kernels.h): a kernel so launched may begin while the
 // one before it on the stream still runs, once all of that one's blocks have begun and called
 // pdl_trigger (or ended), and must call pdl_wait, which returns when that kernel is complete
-// and its writes are visible, before it reads or writes memory.
+// and its writes are visible, before it reads or writes memory that that kernel writes or reads.
+// pdl_wait comes before pdl_trigger, so that what has begun has everything but the kernel just
+// before it behind itself, and a launch that is complete has all before it complete.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
