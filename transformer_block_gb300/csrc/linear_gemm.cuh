@@ -20,10 +20,12 @@
 //   224 us with four, 176 with eight).
 //
 // Bound by the tensor rate for many tokens: 8192 x 20480 x 5120 with GeLU and the stored
-// pre-activation runs at 1870 TFLOP/s in short bursts (95 % of cuBLAS's measured 1967), 1560 over
+// pre-activation runs at 1870 TFLOP/s in short bursts (98 % of cuBLAS's measured 1904), 1630 over
 // seconds, where the power limit holds both down. A single wave costs 6.5 us (launch, first
-// loads, epilogue, stores) and 0.27 us a k-block for one pair; with all pairs at work and operands
-// read for the first time 0.33 to 0.41, the memory's latency and rate.
+// loads, epilogue, stores) and 0.27 us a k-block for one pair, near the 0.25 that an SM takes for
+// its 32 KB of operands from the L2 cache; with all pairs at work and operands that come from
+// memory 0.33 to 0.41. Fetching them into the L2 cache ahead of the loads costs that path twice
+// (2056 x 4104 for 777 rows: 25 us without, 34 with).
 
 namespace {
 

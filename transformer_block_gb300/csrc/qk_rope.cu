@@ -24,6 +24,11 @@
 // more groups. Three heads ahead of the one at work are on their way by asynchronous copies
 // into shared memory that only the lane itself reads back (no barrier): registers would hold
 // one.
+//
+// Measured: forward, 32,760 tokens of 32 + 32 heads of 128, 164 us (6.5 TB/s, 96 % of a plain
+// copy); a decoding step of 64 tokens, 32 + 8 heads, 2.2 us in a graph. Backward, 8192 tokens of
+// 16 + 16 heads, 36.9 us (5.5 TB/s): bound by the instructions of a value's two sums and turn as
+// much as by memory (issue slots 55 % busy).
 #include <cuda_bf16.h>
 
 #include <algorithm>
