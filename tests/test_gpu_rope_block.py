@@ -416,3 +416,26 @@ def test_block_rotation_gradients_apart():
     refused(at, at + 4 * d.head_dim - 4)
     refused(saved.data_ptr() + n - 4, at)
     refused(at, saved.data_ptr())
+
+
+def test_block_rotation_saves_one_forward():
+    # what the norm's backward reads is the last forward's: an earlier one's scratch is refused
+    wl, kind = CASES[0]
+    x, _, block = make(wl, seed=12)
+    rope = plan_of(wl, kind)
+    (gq, gk), pos = extras(wl, rope, 13)
+    block.set_qk_norm_rope(rope, gq, gk, 1e-5, pos, training=True)
+    one, two = pb.new_train_scratch(block.dims), pb.new_train_scratch(block.dims)
+    block.forward_train(x, one)
+    block.forward_train(x, two)
+    with pytest.raises(pb.PbError, match="another scratch"):
+        block.backward(x, x.clone(), one)
+    last = block.backward(x, x.clone(), two)["dw1"]
+    block.forward_train(x, one)
+    assert torch.equal(block.backward(x, x.clone(), one)["dw1"], last)
+    # without a norm nothing is kept, and forwards may be in flight together
+    block.set_qk_norm_rope(rope, positions=pos, training=True)
+    block.forward_train(x, one)
+    block.forward_train(x, two)
+    block.backward(x, x.clone(), one)
+    assert block.status() == 0

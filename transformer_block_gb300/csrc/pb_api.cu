@@ -55,6 +55,7 @@ struct pb_handle {
   cudaEvent_t copy_ev[6];
   bool has_rope;        // pb_set_qk_norm_rope
   pb_block_rope rope;
+  const void* saved_for;  // the scratch of the forward whose q and k rope.saved holds, or null
 };
 
 namespace {
@@ -1180,6 +1181,7 @@ pb_status pb_forward_train(pb_handle* h, const void* x, void* y, void* scratch,
     return fail(PB_ERR_INVALID_ARG, "x or y overlaps the scratch buffer");
   s = check_rope_saved(h, x, y, scratch, L.train_total);
   if (s != PB_OK) return s;
+  h->saved_for = rope_saves(h) ? scratch : nullptr;
   return run_block(h, x, false, y, false, static_cast<uint8_t*>(scratch),
                    static_cast<cudaStream_t>(stream), true);
 }
@@ -1213,6 +1215,9 @@ pb_status pb_backward(pb_handle* h, const void* x, const void* dy, const pb_grad
     return fail(PB_ERR_INVALID_ARG, "dx or dy overlaps the scratch buffer");
   s = check_rope_saved(h, grads->dx, dy, scratch, L.train_total);
   if (s != PB_OK) return s;
+  if (rope_saves(h) && h->saved_for != nullptr && h->saved_for != scratch)
+    return fail(PB_ERR_INVALID_ARG,
+                "pb_block_rope.saved holds the q and k of a forward with another scratch");
   return run_backward(h, x, dy, *grads, accumulate != 0, static_cast<uint8_t*>(scratch),
                       static_cast<cudaStream_t>(stream));
 }
@@ -1410,6 +1415,7 @@ pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r) {
     return fail(PB_ERR_INVALID_ARG, "dgamma_q, dgamma_k and saved must be apart");
   h->rope = *r;
   h->has_rope = true;
+  h->saved_for = nullptr;
   return PB_OK;
 }
 

@@ -392,8 +392,8 @@ class ParallelBlock:
         """``pb_set_qk_norm_rope``: q and k are normed (where there is a gamma) and rotated at
         ``positions`` (int32 [axes, batch, seq], or None) before the attention, in every call
         from now on; ``rope=None`` takes that out. The tensors are kept and read by each call.
-        ``training`` allocates what ``forward_train`` keeps and the gradients ``self.rope_grads``
-        (``dgamma_q``, ``dgamma_k``: fp32, written by ``backward``)."""
+        ``training`` allocates what ``forward_train`` keeps (of its last call) and the gradients
+        ``self.rope_grads`` (``dgamma_q``, ``dgamma_k``: fp32, written by ``backward``)."""
         if rope is None:
             _check("pb_set_qk_norm_rope", self._lib.pb_set_qk_norm_rope(self.handle, None))
             self._rope, self.rope_grads = None, {}
