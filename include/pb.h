@@ -412,7 +412,7 @@ pb_status pb_swa_attention(const pb_dims* dims, const void* qk, const void* vt, 
  *   n = x / sqrt(mean x^2 + eps) * gamma               (skipped where gamma is NULL)
  *   (a, b) -> (a cos t - b sin t, a sin t + b cos t)   for every rotated pair of n,
  * t = position on the pair's axis x the pair's frequency. Computed in fp32, rounded once to
- * bf16; the angle's place in its turn is exact to 2^-33 at any position.
+ * bf16; with frequencies up to 1 the angle is off by 2^-24 of a turn at most, at any position.
  * ---------------------------------------------------------------------------------- */
 
 #define PB_ROPE_MAX_AXES 4

@@ -10,9 +10,10 @@
 //   dx = rstd (d gamma - x rstd mean(d gamma x rstd))
 //
 // The angle only matters modulo a turn. A frequency is held as a 64-bit binary fraction of a
-// turn per position, so position times frequency, wrapped to 64 bits, is the angle's place in
-// its turn to 2^-33 at any 32-bit position (negative ones too); a product in fp32 would be off
-// by 0.06 radian at position 10^6. The top 32 bits, in radians, go to the fast sine and cosine.
+// turn per position (up to frequency 1 off by 2^-56 at most), so position times frequency, wrapped
+// to 64 bits, is the angle's place in its turn to 2^-33 up to position 2^23 and to 2^-25 at any
+// 32-bit one (negative ones too); a product in fp32 would be off by 0.06 radian at position 10^6.
+// The top 32 bits, in radians, go to the fast sine and cosine.
 //
 // Both passes are bound by memory: 4 bytes a value forward, 6 backward (the norm's backward
 // reads x again and recomputes rstd, which costs less than storing it). A head belongs to dh /
