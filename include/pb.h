@@ -492,11 +492,14 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
  * (device, 256-byte aligned, batch * seq * 2 * hidden * 2 bytes) keeps the projection's q and k
  * between pb_forward_train and pb_backward, as their scratch does the rest; dgamma_q and
  * dgamma_k (fp32 [head_dim], or NULL) receive the gammas' gradients, by pb_backward's
- * accumulate. `saved` belongs to one forward at a time: pb_backward refuses the scratch of an
- * earlier one (two forwards in flight: two handles, or this call with another `saved` before
- * each). The struct is copied; what it points to must stay valid until the calls are done, and
- * the same from pb_forward_train to its pb_backward. NULL takes the step out again. In
- * pb_trace_read its time counts with the attention. */
+ * accumulate. `saved` belongs to one forward at a time. The handle remembers which `saved` and
+ * which scratch every forward filled, whatever is set afterwards, and pb_backward through a norm
+ * is refused where the current `saved` holds no forward, one with another scratch, or one of
+ * which a later forward has overwritten either (two forwards in flight: two handles, or this
+ * call with another `saved` before each forward and each backward; a captured forward counts
+ * when it is captured). The struct is copied; what it points to must stay valid until the calls
+ * are done, and the same from pb_forward_train to its pb_backward. NULL takes the step out
+ * again. In pb_trace_read its time counts with the attention. */
 typedef struct pb_block_rope {
   pb_rope rope;
   const void* gamma_q;

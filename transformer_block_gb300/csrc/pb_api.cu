@@ -3,6 +3,7 @@
 //   LN -> GEMM [Wqkv | W1] (+GeLU) -> sliding-window attention -> GEMM [Wo ; W2] (+x)
 // (MegaScale reading notes, section 1.1, eq. (4)). All device memory belongs to the
 // caller; this file allocates none.
+#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -20,6 +21,13 @@
 #include "kernels.h"
 
 using pb::EpiParams;
+
+// A forward pass whose q and k (before their norm) a pb_block_rope.saved buffer holds, and the
+// scratch that holds the rest of it.
+struct SavedForward {
+  const void* saved;
+  const void* scratch;
+};
 
 struct pb_handle {
   uint32_t magic;
@@ -55,7 +63,9 @@ struct pb_handle {
   cudaEvent_t copy_ev[6];
   bool has_rope;        // pb_set_qk_norm_rope
   pb_block_rope rope;
-  const void* saved_for;  // the scratch of the forward whose q and k rope.saved holds, or null
+  // one for every `saved` buffer that holds a forward of this handle; pb_set_qk_norm_rope keeps
+  // room for one more, so that a forward allocates nothing
+  std::vector<SavedForward> forwards;
 };
 
 namespace {
@@ -418,6 +428,32 @@ pb_status check_rope_saved(const pb_handle* h, const void* x, const void* y, con
       overlap(h->rope.saved, n, y, n / 2))
     return fail(PB_ERR_INVALID_ARG, "pb_block_rope.saved overlaps another argument");
   return PB_OK;
+}
+
+// A training forward begins: what it writes over is no earlier forward's any more.
+void forget_forwards(pb_handle* h, const void* scratch, size_t scratch_bytes) {
+  const size_t n = size_t(h->d.batch) * h->d.seq * h->d.hidden * 4;
+  const void* saved = rope_saves(h) ? h->rope.saved : nullptr;
+  auto& f = h->forwards;
+  f.erase(std::remove_if(f.begin(), f.end(),
+                         [&](const SavedForward& e) {
+                           return overlap(e.scratch, scratch_bytes, scratch, scratch_bytes) ||
+                                  (saved != nullptr && overlap(e.saved, n, saved, n));
+                         }),
+          f.end());
+}
+// A backward pass through a norm reads the q and k of the forward that filled `scratch`.
+pb_status check_saved_forward(const pb_handle* h, const void* scratch) {
+  if (!rope_saves(h)) return PB_OK;
+  for (const SavedForward& e : h->forwards)
+    if (e.saved == h->rope.saved)
+      return e.scratch == scratch
+                 ? PB_OK
+                 : fail(PB_ERR_INVALID_ARG,
+                        "pb_block_rope.saved holds the q and k of a forward with another scratch");
+  return fail(PB_ERR_INVALID_ARG,
+              "pb_block_rope.saved holds the q and k of no forward (or of one whose scratch or "
+              "saved a later forward has written)");
 }
 
 // One block from x to y (each bf16, or fp32 inside a stack's residual stream),
@@ -1181,9 +1217,11 @@ pb_status pb_forward_train(pb_handle* h, const void* x, void* y, void* scratch,
     return fail(PB_ERR_INVALID_ARG, "x or y overlaps the scratch buffer");
   s = check_rope_saved(h, x, y, scratch, L.train_total);
   if (s != PB_OK) return s;
-  h->saved_for = rope_saves(h) ? scratch : nullptr;
-  return run_block(h, x, false, y, false, static_cast<uint8_t*>(scratch),
-                   static_cast<cudaStream_t>(stream), true);
+  forget_forwards(h, scratch, L.train_total);
+  s = run_block(h, x, false, y, false, static_cast<uint8_t*>(scratch),
+                static_cast<cudaStream_t>(stream), true);
+  if (s == PB_OK && rope_saves(h)) h->forwards.push_back(SavedForward{h->rope.saved, scratch});
+  return s;
 }
 
 pb_status pb_backward(pb_handle* h, const void* x, const void* dy, const pb_grads* grads,
@@ -1215,9 +1253,8 @@ pb_status pb_backward(pb_handle* h, const void* x, const void* dy, const pb_grad
     return fail(PB_ERR_INVALID_ARG, "dx or dy overlaps the scratch buffer");
   s = check_rope_saved(h, grads->dx, dy, scratch, L.train_total);
   if (s != PB_OK) return s;
-  if (rope_saves(h) && h->saved_for != nullptr && h->saved_for != scratch)
-    return fail(PB_ERR_INVALID_ARG,
-                "pb_block_rope.saved holds the q and k of a forward with another scratch");
+  s = check_saved_forward(h, scratch);
+  if (s != PB_OK) return s;
   return run_backward(h, x, dy, *grads, accumulate != 0, static_cast<uint8_t*>(scratch),
                       static_cast<cudaStream_t>(stream));
 }
@@ -1413,9 +1450,13 @@ pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r) {
       (r->saved != nullptr && ((r->dgamma_q != nullptr && overlap(r->dgamma_q, dg, r->saved, need)) ||
                                (r->dgamma_k != nullptr && overlap(r->dgamma_k, dg, r->saved, need)))))
     return fail(PB_ERR_INVALID_ARG, "dgamma_q, dgamma_k and saved must be apart");
+  try {
+    h->forwards.reserve(h->forwards.size() + 1);
+  } catch (...) {
+    return fail(PB_ERR_INVALID_ARG, "host allocation for the saved forwards failed");
+  }
   h->rope = *r;
   h->has_rope = true;
-  h->saved_for = nullptr;
   return PB_OK;
 }
 

@@ -319,6 +319,7 @@ class ParallelBlock:
                                                       self.workspace.numel(), _stream(stream),
                                                       ctypes.byref(h)))
         self.handle = h
+        self._rope, self._rope_saved, self.rope_grads = None, None, {}
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None,
                 scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -388,22 +389,33 @@ class ParallelBlock:
         return g
 
     def set_qk_norm_rope(self, rope: "Rope | None", gamma_q=None, gamma_k=None,
-                         eps: float = 1e-6, positions=None, training: bool = False):
+                         eps: float = 1e-6, positions=None, training: bool = False, saved=None):
         """``pb_set_qk_norm_rope``: q and k are normed (where there is a gamma) and rotated at
         ``positions`` (int32 [axes, batch, seq], or None) before the attention, in every call
         from now on; ``rope=None`` takes that out. The tensors are kept and read by each call.
-        ``training`` allocates what ``forward_train`` keeps (of its last call) and the gradients
-        ``self.rope_grads`` (``dgamma_q``, ``dgamma_k``: fp32, written by ``backward``)."""
+        ``training`` makes the gradients ``self.rope_grads`` (``dgamma_q``, ``dgamma_k``: fp32,
+        written by ``backward``). What ``forward_train`` keeps of its last call is in a buffer of
+        the block's, the same for every such call; for several forwards in flight give each a
+        ``saved`` of its own (a uint8 CUDA tensor of batch * seq * hidden * 4 bytes), set before
+        it and again before its ``backward``. Between the two, gammas, positions and eps are the
+        caller's to keep the same; a ``backward`` whose q and k are no longer kept is refused."""
         if rope is None:
             _check("pb_set_qk_norm_rope", self._lib.pb_set_qk_norm_rope(self.handle, None))
             self._rope, self.rope_grads = None, {}
             return
         d = self.dims
-        _here(gamma_q, gamma_k, positions, self.workspace)
-        saved, grads = None, {}
+        _here(gamma_q, gamma_k, positions, saved, self.workspace)
+        n, grads = d.batch * d.seq * d.hidden * 4, {}
+        if saved is not None:
+            _is(training, "saved goes with training")
+            _is(saved.dtype is torch.uint8 and saved.is_contiguous() and saved.numel() >= n,
+                f"saved must be {n} contiguous bytes (uint8)")
         if training and (gamma_q is not None or gamma_k is not None):
-            saved = torch.empty(d.batch * d.seq * d.hidden * 4, dtype=torch.uint8,
-                                device=self.workspace.device)
+            if saved is None:
+                if self._rope_saved is None:
+                    self._rope_saved = torch.empty(n, dtype=torch.uint8,
+                                                   device=self.workspace.device)
+                saved = self._rope_saved
             for name, g in (("dgamma_q", gamma_q), ("dgamma_k", gamma_k)):
                 if g is not None:
                     grads[name] = torch.zeros(d.head_dim, dtype=torch.float32, device=g.device)
