@@ -525,7 +525,9 @@ typedef enum pb_dtype { PB_DTYPE_BF16 = 0, PB_DTYPE_FP16 = 1, PB_DTYPE_FP32 = 2 
 typedef enum pb_weight_layout { PB_WEIGHT_IN_OUT = 0, PB_WEIGHT_OUT_IN = 1 } pb_weight_layout;
 
 /* GELU: z Phi(z). GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. SILU: z / (1 +
- * e^-z). RELU: max(z, 0), with derivative 0 at 0. */
+ * e^-z). RELU: max(z, 0), with derivative 0 at 0. Computed in fp32. GELU: Phi(z) is off by (1.5 z^2
+ * + 24) 2^-24 of itself at most, in its left tail too; by 5e-7 where the result is bf16 and has
+ * more than 32 rows (5e-4 of GELU's value at z = -4, an eighth of the result's rounding). */
 typedef enum pb_activation {
   PB_ACT_NONE = 0,
   PB_ACT_GELU = 1,

@@ -3,10 +3,10 @@
 //   LN -> GEMM [Wqkv | W1] (+GeLU) -> sliding-window attention -> GEMM [Wo ; W2] (+x)
 // (MegaScale reading notes, section 1.1, eq. (4)). All device memory belongs to the
 // caller; this file allocates none.
-#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
