@@ -14,7 +14,9 @@
 //   of a chain of fp32 fused multiply-adds. So an accumulator sums 896 k at most, and the
 //   epilogue warps add such segments up in registers, rounding, while the products go on in the
 //   other accumulator (2048 x 2048 x 8192: 42.8 us in one chain, 43.3 in segments of 1792 k, 44.9
-//   of 896). A 16-bit result rounds at 2^-9 and is summed in one chain.
+//   of 896). 16-bit results take longer segments: the cut, 1.05e-9 of the sum for each k, stays
+//   below 1/64 of half a step (fp16 2^-11: 7,168 k; bf16 2^-8: 57,344 k). In one chain a result lost
+//   1.4e-4 of itself at K = 131,072 (fp16) and 5.4e-4 at 524,288 (bf16).
 // * Eight epilogue warps, each quarter of the tensor memory's lanes shared by two: four do not
 //   hide a pre-activation's loads and GeLU' behind a main loop of K = 2048 (8192 x 8192 x 2048:
 //   224 us with four, 176 with eight).
@@ -40,8 +42,8 @@ constexpr size_t LIN_OUT_OFF =
 constexpr size_t LIN_SMEM = 1024 + LIN_OUT_OFF + LIN_EPI * 4096;
 static_assert(LIN_SMEM <= 227 * 1024, "shared memory of the linear kernel");
 
-// k-blocks (of 64) that one accumulator sums where the result is fp32.
-constexpr int kLinearSegment = 14;
+// k-blocks (of 64) that one accumulator sums at most, for each type of result.
+constexpr int kLinearSegment = 14, kLinearSegmentF16 = 112, kLinearSegmentBf16 = 896;
 // k-blocks (0.28 us each) that a part of a split tile has at least, and that splitting has to
 // save at least: partial sums and second launch cost 5 to 10 us (saving 53 of 80 took 333 x
 // 2504 x 5120 from 27.9 to 19.6 us, saving 16 of 32 took 256 x 8192 x 2048 from 15.4 to 19.2).
@@ -993,9 +995,12 @@ cudaError_t launch_linear(OpType op, const LinearProduct* products, int count, c
     jb.num_m = (p.M + PM - 1) / PM;
     jb.num_n = (p.N + BN - 1) / BN;
     jb.num_kb = (p.K + BK - 1) / BK;
-    // fp32 results: segments of about one length, kLinearSegment k-blocks at most
-    const int segments = (jb.num_kb + kLinearSegment - 1) / kLinearSegment;
-    jb.seg = p.epi.y32 != nullptr ? (jb.num_kb + segments - 1) / segments : jb.num_kb;
+    // segments of about one length
+    const int longest = p.epi.y32 != nullptr ? kLinearSegment
+                        : op == kOpF16       ? kLinearSegmentF16
+                                             : kLinearSegmentBf16;
+    const int segments = (jb.num_kb + longest - 1) / longest;
+    jb.seg = (jb.num_kb + segments - 1) / segments;
     jb.a_mn = p.a_mn;
     jb.b_mn = p.b_mn;
   }
