@@ -566,7 +566,8 @@ typedef struct pb_linear_args {
 
 /* `scratch` (device, 256-byte aligned, >= pb_linear_scratch_bytes, or NULL) lets products be
  * split along k where their tiles do not fill the GPU; with NULL every tile is computed whole.
- * It needs no preparation. Calls that share one must not overlap on the GPU. `status` as in
+ * It needs no preparation; no operand or result may lie in it. Calls that share one must not
+ * overlap on the GPU. `status` as in
  * pb_gemm_bf16. */
 pb_status pb_linear_scratch_bytes(size_t* bytes);
 pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_bytes, int* status,

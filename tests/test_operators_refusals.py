@@ -1,0 +1,55 @@
+"""More arguments of the operators around the block that are refused on the host, before anything
+is enqueued (CPU only; the pointers are made up and never read)."""
+
+import ctypes
+
+import pytest
+
+from transformer_block_gb300 import build, pb
+
+P = 0x10000000
+W = P + (8 << 24)  # scratch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return pb.lib()
+
+
+def message(lib):
+    return lib.pb_last_error_message().decode()
+
+
+def linear(lib, **kw):
+    a = pb.pb_linear_args(40, 64, 128, 0, 0, 0, P, 128, P + (1 << 24), 64, None, None, 0, 0, None,
+                          0, P + (2 << 24), 64, 0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return lib.pb_linear(ctypes.byref(a), W, pb.linear_scratch_bytes(), None, None)
+
+
+def linear_back(lib, **kw):
+    a = pb.pb_linear_grads(40, 64, 128, 0, 0, 0, 0, P, 64, P + (1 << 24), 128, P + (2 << 24), 64,
+                           None, 0, P + (3 << 24), 128, P + (4 << 24), 64, None)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return lib.pb_linear_backward(ctypes.byref(a), W, pb.linear_scratch_bytes(), None, None)
+
+
+def test_linear_operands_in_scratch(lib):
+    # split products write their partial sums there while the operands are read
+    end = W + pb.linear_scratch_bytes()
+    for at in (W, W + 4096, end - 16):
+        for kw in (dict(x=at), dict(w=at), dict(bias=at), dict(residual=at, ldr=64),
+                   dict(pre=at, ldp=64), dict(y=at)):
+            assert linear(lib, **kw) == 1, kw
+            assert "overlap" in message(lib) and "scratch" in message(lib), kw
+        for kw in (dict(dy=at), dict(x=at), dict(w=at), dict(activation=1, pre=at, ldp=128),
+                   dict(dx=at), dict(dw=at), dict(db=at)):
+            assert linear_back(lib, **kw) == 1, kw
+            assert "overlap" in message(lib) and "scratch" in message(lib), kw
+    # what a call does not read may be anywhere: x without dw, w without dx, no tokens
+    assert linear_back(lib, x=W, dw=None) != 1
+    assert linear_back(lib, w=W, dx=None) != 1
+    assert linear(lib, m=0, x=W) == 0

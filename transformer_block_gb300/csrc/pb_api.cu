@@ -932,6 +932,17 @@ pb_status check_apart(const Matrix& out, const char* name, const Matrix& other) 
   return PB_OK;
 }
 
+// Split products write partial sums to scratch while other tiles read and write the matrices.
+template <int N>
+pb_status check_apart_from_scratch(const Matrix& scratch, const Matrix* const (&m)[N],
+                                   const char* const (&names)[N]) {
+  for (int i = 0; i < N; ++i)
+    if (scratch.p != nullptr && m[i]->p != nullptr && m[i]->rows > 0 &&
+        overlap(scratch.p, scratch.bytes(), m[i]->p, m[i]->bytes()))
+      return fail(PB_ERR_INVALID_ARG, "%s overlaps scratch", names[i]);
+  return PB_OK;
+}
+
 pb_status check_linear_sizes(int32_t m, int32_t n, int32_t k, int32_t dtype, int32_t layout,
                              int32_t act) {
   if (m < 0 || n < 1 || k < 1) return fail(PB_ERR_INVALID_ARG, "need m >= 0, n >= 1, k >= 1");
@@ -1665,7 +1676,11 @@ pb_status pb_linear(const pb_linear_args* args, void* scratch, size_t scratch_by
   if (s != PB_OK) return s;
   if (!aligned(a.bias, 16)) return fail(PB_ERR_INVALID_ARG, "bias must be 16-byte aligned");
   const bool in_place = r.p == y.p && r.ld == y.ld && r.esz == y.esz;
-  const Matrix* others[5] = {&x, &w, &bias, &pre, &work};
+  const Matrix* all[6] = {&x, &w, &bias, &r, &pre, &y};
+  static const char* const names[6] = {"x", "w", "bias", "residual", "pre", "y"};
+  s = check_apart_from_scratch(work, all, names);
+  if (s != PB_OK) return s;
+  const Matrix* others[4] = {&x, &w, &bias, &pre};
   for (const Matrix* o : others) {
     s = check_apart(y, "y", *o);
     if (s != PB_OK) return s;
@@ -1755,7 +1770,10 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
   if (!aligned(a.db, 4)) return fail(PB_ERR_INVALID_ARG, "db must be 4-byte aligned");
   const Matrix* outs[3] = {&dx, &dw, &db};
   const char* const names[3] = {"dx", "dw", "db"};
-  const Matrix* all[8] = {&dy, &x, &w, &pre, &dx, &dw, &db, &work};
+  const Matrix* all[7] = {&dy, &x, &w, &pre, &dx, &dw, &db};
+  static const char* const all_names[7] = {"dy", "x", "w", "pre", "dx", "dw", "db"};
+  s = check_apart_from_scratch(work, all, all_names);
+  if (s != PB_OK) return s;
   for (int i = 0; i < 3; ++i) {
     if (outs[i]->p == nullptr || (i == 0 && a.m == 0)) continue;
     for (const Matrix* o : all) {
