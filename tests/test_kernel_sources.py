@@ -25,3 +25,13 @@ def test_normal_tail_fit():
     assert np.abs(t * p / want - 1).max() <= 5.7e-8 + 7.3e-8
     half = float(re.search(r"kHalfLog2e = ([0-9.]+)f", body)[1])
     assert np.float32(half) == np.float32(np.log2(np.e) / 2)
+
+
+@pytest.mark.parametrize("name", ["qk_rope.cu", "linear.cu", "linear_gemm.cuh", "adamw.cu"])
+def test_dependent_launches_read_coherently(name):
+    # These kernels may begin while the launch before them still writes what they read. A load
+    # through the read-only path is defined only for what nothing writes while the kernel lives.
+    body = open(os.path.join(os.path.dirname(SRC), name)).read()
+    assert "launch_dependent(" in body
+    for word in ("__ldg", "ld.global.nc", "__restrict__"):
+        assert word not in body, (name, word)
