@@ -474,7 +474,8 @@ pb_status pb_qk_norm_rope(const pb_rope* rope, int32_t batch, int32_t seq, const
  * 256-byte aligned, >= pb_qk_norm_rope_scratch_bytes) is needed where there is a gamma and
  * must not be used by another call that may run concurrently. dgamma_q, dgamma_k and scratch
  * overlap nothing else (one gamma for both: two gradients, added by the caller). Sums over
- * tokens and heads are taken in a fixed order. batch or seq 0 gives zero sums. */
+ * tokens and heads are taken in a fixed order. batch or seq 0 gives zero sums. With a gamma eps is
+ * 2^-80 at least (rstd^3 has to stay in fp32's range for a head of zeros). */
 pb_status pb_qk_norm_rope_scratch_bytes(size_t* bytes);
 pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t seq,
                                    const pb_heads* q, const pb_heads* k, const void* gamma_q,

@@ -53,3 +53,31 @@ def test_linear_operands_in_scratch(lib):
     assert linear_back(lib, x=W, dw=None) != 1
     assert linear_back(lib, w=W, dx=None) != 1
     assert linear(lib, m=0, x=W) == 0
+
+
+# --------------------------------------------------------------------------- rotation
+
+def plan(lib, dh=128):
+    p = pb.pb_rope()
+    assert lib.pb_rope_init(dh, dh, 0, 1, None, 0, 1e4, None, ctypes.byref(p)) == 0
+    return p
+
+
+def heads(ptr=P, n=4, b=8 * 512, s=512, h=128):
+    return ctypes.byref(pb.pb_heads(ptr, n, b, s, h))
+
+
+def rope_back(lib, eps, gamma=P + (4 << 24)):
+    return lib.pb_qk_norm_rope_backward(
+        ctypes.byref(plan(lib)), 2, 8, heads(P), None, gamma, None, eps, None,
+        heads(P + (1 << 24)), None, heads(P + (2 << 24)), None, P + (5 << 24), None, 0, W,
+        pb.qk_norm_rope_scratch_bytes(), None)
+
+
+def test_backward_of_a_norm_with_a_vanishing_eps(lib):
+    # The norm's backward takes rstd^3: for a head of zeros eps^(-3/2), which passes fp32's range
+    # from eps = 2e-26 down, and infinity times the head's zero sum is NaN.
+    for eps in (1e-30, 1e-40, 2.0 ** -81):
+        assert rope_back(lib, eps) == 1, eps
+        assert "2^-80" in message(lib)
+    assert rope_back(lib, 2.0 ** -80) != 1

@@ -424,6 +424,13 @@ pb_status check_rope_saved(const pb_handle* h, const void* x, const void* y, con
   const size_t n = size_t(h->d.batch) * h->d.seq * h->d.hidden * 4;
   if (h->rope.saved == nullptr)
     return fail(PB_ERR_WORKSPACE, "training with a query or key norm needs pb_block_rope.saved");
+  // on no tokens: what the backward call would refuse in the middle of the pass
+  const pb_block_rope& r = h->rope;
+  const pb_heads none{};
+  const pb_status s = pb_qk_norm_rope_backward(&r.rope, 0, h->d.seq, &none, &none, r.gamma_q,
+                                               r.gamma_k, r.eps, r.positions, &none, &none, &none,
+                                               &none, nullptr, nullptr, 1, nullptr, 0, nullptr);
+  if (s != PB_OK) return s;
   if (overlap(h->rope.saved, n, scratch, scratch_bytes) || overlap(h->rope.saved, n, x, n / 2) ||
       overlap(h->rope.saved, n, y, n / 2))
     return fail(PB_ERR_INVALID_ARG, "pb_block_rope.saved overlaps another argument");

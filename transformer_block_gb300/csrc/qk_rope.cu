@@ -49,6 +49,8 @@ namespace {
 constexpr uint32_t kRopeMagic = 0x45504F52u;  // "ROPE"
 constexpr int THREADS = 256;
 constexpr int kMaxDh = 256;
+// The norm's backward takes rstd^3, up to eps^(-3/2): in fp32's range with room for the sums.
+constexpr float kLeastEpsBackward = 0x1p-80f;
 // Blocks of the backward pass that leave a partial sum of dgamma for one tensor.
 constexpr int kMaxPartials = 1024;
 constexpr size_t kPartialBytes = size_t(2) * kMaxPartials * kMaxDh * sizeof(float);
@@ -823,6 +825,8 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
                                    void* scratch, size_t scratch_bytes, void* stream) {
   pb_status s = check_common(rope, batch, seq, eps, gamma_q, gamma_k, positions);
   if (s != PB_OK) return s;
+  if ((gamma_q != nullptr || gamma_k != nullptr) && eps < kLeastEpsBackward)
+    return record_error(PB_ERR_INVALID_ARG, "eps must be >= 2^-80 for the norm's backward");
   const pb_heads* x[2] = {q, k};
   const pb_heads* dy[2] = {dq, dk};
   const pb_heads* out[2] = {dq_out, dk_out};
