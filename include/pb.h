@@ -446,8 +446,9 @@ pb_status pb_rope_init(int32_t head_dim, int32_t rot_dim, int32_t pairing, int32
 
 /* The heads of every token, bf16: value d of head h at (b, s) is ptr[b batch_stride + s
  * seq_stride + h head_stride + d]. Strides in elements, multiples of 8, >= 0; ptr 16-byte
- * aligned. [B, S, heads, dh], [B, heads, S, dh] and the q or k columns of a [q | k | v] or
- * of the scratch layout's [q | k] buffer are such views. */
+ * aligned; 2^48 values at most from the first to the last. [B, S, heads, dh], [B, heads, S, dh]
+ * and the q or k columns of a [q | k | v] or of the scratch layout's [q | k] buffer are such
+ * views. */
 typedef struct pb_heads {
   void* ptr;
   int32_t heads;

@@ -81,3 +81,17 @@ def test_backward_of_a_norm_with_a_vanishing_eps(lib):
         assert rope_back(lib, eps) == 1, eps
         assert "2^-80" in message(lib)
     assert rope_back(lib, 2.0 ** -80) != 1
+
+
+def test_views_beyond_all_memory(lib):
+    # strides are below 2^40 and tokens below 2^31, but their products pass 64 bits, and the checks
+    # for overlaps with them
+    far, big = P + (1 << 40), 1 << 40
+    p = plan(lib)
+    for b, s, kw in ((1 << 15, 1 << 15, dict(b=big)), (1, 1 << 30, dict(s=big)),
+                     (1, 4, dict(n=(1 << 31) - 1, h=big))):
+        for q, o in ((kw, {}), ({}, kw), (kw, kw)):
+            got = lib.pb_qk_norm_rope(ctypes.byref(p), b, s, heads(P, **q), None, None, None, 1e-6,
+                                      None, heads(far, **({"s": 4096 * 512, "b": 0} | o)), None,
+                                      None)
+            assert got == 2 and "2^48" in message(lib), (b, s, q, o, message(lib))

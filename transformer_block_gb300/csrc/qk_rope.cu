@@ -588,6 +588,11 @@ pb_status check_view(const pb_heads* v, const char* what, int batch, int seq, in
   for (int64_t k : st)
     if (k < 0 || k % 8 != 0 || k > (int64_t(1) << 40))
       return bad(PB_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, >= 0", what);
+  // so that offsets, in bytes too, and the sums of the checks below stay within 64 bits
+  const int64_t steps[3] = {int64_t(batch) - 1, int64_t(seq) - 1, int64_t(v->heads) - 1};
+  for (int i = 0; i < 3; ++i)
+    if (steps[i] > 0 && st[i] > (int64_t(1) << 48) / steps[i])
+      return bad(PB_ERR_UNSUPPORTED, "%s: more than 2^48 values from the first to the last", what);
   if (out && !distinct(*v, batch, seq, dh))
     return bad(PB_ERR_INVALID_ARG, "%s: the strides make values of the result overlap", what);
   return PB_OK;
