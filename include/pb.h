@@ -494,7 +494,7 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
  * (device, 256-byte aligned, batch * seq * 2 * hidden * 2 bytes) keeps the projection's q and k
  * between pb_forward_train and pb_backward, as their scratch does the rest; dgamma_q and
  * dgamma_k (fp32 [head_dim], or NULL) receive the gammas' gradients, by pb_backward's
- * accumulate. `saved` belongs to one forward at a time. The handle remembers which `saved` and
+ * accumulate. These three overlap nothing else of a training step. `saved` belongs to one forward at a time. The handle remembers which `saved` and
  * which scratch every forward filled, whatever is set afterwards, and pb_backward through a norm
  * is refused where the current `saved` holds no forward, one with another scratch, or one of
  * which a later forward has overwritten either (two forwards in flight: two handles, or this

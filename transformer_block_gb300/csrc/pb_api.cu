@@ -1273,6 +1273,14 @@ pb_status pb_backward(pb_handle* h, const void* x, const void* dy, const pb_grad
   if (s != PB_OK) return s;
   s = check_saved_forward(h, scratch);
   if (s != PB_OK) return s;
+  if (h->has_rope)
+    for (const float* g : {h->rope.dgamma_q, h->rope.dgamma_k}) {
+      const size_t dg = size_t(d.head_dim) * 4;
+      if (g != nullptr && (overlap(g, dg, x, n) || overlap(g, dg, dy, n) ||
+                           overlap(g, dg, grads->dx, n) || overlap(g, dg, scratch, L.train_total)))
+        return fail(PB_ERR_INVALID_ARG,
+                    "dgamma_q or dgamma_k of pb_block_rope overlaps x, dy, dx or the scratch");
+    }
   return run_backward(h, x, dy, *grads, accumulate != 0, static_cast<uint8_t*>(scratch),
                       static_cast<cudaStream_t>(stream));
 }
@@ -1462,12 +1470,19 @@ pb_status pb_set_qk_norm_rope(pb_handle* h, const pb_block_rope* r) {
   if (s != PB_OK) return s;
   if (!aligned(r->dgamma_q, 4) || !aligned(r->dgamma_k, 4))
     return fail(PB_ERR_INVALID_ARG, "dgamma_q and dgamma_k must be 4-byte aligned");
+  // what training writes, apart from one another and from what it reads
   const size_t dg = size_t(h->d.head_dim) * 4;
-  if ((r->dgamma_q != nullptr && r->dgamma_k != nullptr &&
-       overlap(r->dgamma_q, dg, r->dgamma_k, dg)) ||
-      (r->saved != nullptr && ((r->dgamma_q != nullptr && overlap(r->dgamma_q, dg, r->saved, need)) ||
-                               (r->dgamma_k != nullptr && overlap(r->dgamma_k, dg, r->saved, need)))))
-    return fail(PB_ERR_INVALID_ARG, "dgamma_q, dgamma_k and saved must be apart");
+  const struct {
+    const void* p;
+    size_t bytes;
+  } b[6] = {{r->dgamma_q, dg},    {r->dgamma_k, dg},
+            {r->saved, need},     {r->gamma_q, dg / 2},
+            {r->gamma_k, dg / 2}, {r->positions, size_t(r->rope.axes) * h->d.batch * h->d.seq * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (b[i].p != nullptr && b[j].p != nullptr && overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
+        return fail(PB_ERR_INVALID_ARG,
+                    "dgamma_q, dgamma_k and saved must be apart, and from gammas and positions");
   try {
     h->forwards.reserve(h->forwards.size() + 1);
   } catch (...) {
