@@ -833,15 +833,20 @@ def linear_backward(dy, x, w, pre=None, activation: str = "none", layout: int = 
                     dw=None, db=None, accumulate: bool = False, scratch=None, status=None,
                     stream=None):
     """``pb_linear_backward``: ``(dx, dw, db)`` of ``x @ w + bias`` for ``dy`` [m, n]; dx in the
-    operands' type, dw (``w``'s layout) and db fp32, None where not wanted. ``pre`` and
-    ``activation``: ``x`` is ``activation(pre)``, and dx is the gradient of ``pre``.
-    ``accumulate`` adds to the given ``dw`` and ``db``."""
+    operands' type, dw (``w``'s layout) and db fp32, None where not wanted (``x`` is read for dw and
+    ``w`` for dx: None without those). ``pre`` and ``activation``: ``x`` is ``activation(pre)``,
+    and dx is the gradient of ``pre``. ``accumulate`` adds to the given ``dw`` and ``db``."""
     if stream is not None:
         return _run_on(stream, linear_backward, dy, x, w, pre, activation, layout, need_dx, need_dw,
                        bias, dx, dw, db, accumulate, scratch, status)
     m, n = dy.shape
     in_out = layout == PB_WEIGHT_IN_OUT
-    k = (x if x is not None else w).shape[1 if x is not None or not in_out else 0]
+    if x is None and w is None:
+        _is(not need_dx and dx is None, "dx needs w")
+        _is(not need_dw and dw is None, "dw needs x")
+        k = 1  # nothing of it is read
+    else:
+        k = (x if x is not None else w).shape[1 if x is not None or not in_out else 0]
     dt, dev = dy.dtype, dy.device
     _is(dt in (torch.bfloat16, torch.float16), "dy must be torch.bfloat16 or torch.float16")
     w_shape = (k, n) if in_out else (n, k)
