@@ -661,7 +661,9 @@ typedef struct pb_adamw_args {
 /* One AdamW step over all tensors (host array, read before the call returns):
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   param -= lr (weight_decay param + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
- * in fp32, with m and v unrounded in the step that computes them. No buffer that is written
+ * in fp32, with m and v unrounded in the step that computes them. A gradient that is not finite, or
+ * whose square is not (beyond 1.8e19), spoils its own value; the 8-bit states of the 255 that share
+ * its scale then lose their smaller magnitudes, as next to any large value. No buffer that is written
  * may overlap another one (PB_ERR_INVALID_ARG: a tensor listed twice, too). */
 pb_status pb_adamw(const pb_adamw_args* args, int32_t n_tensors, const pb_adamw_tensor* tensors,
                    void* stream);

@@ -206,7 +206,9 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int n, float scale,
 }
 
 // Warp-wide: the codes of the block's values and its scale. A block whose largest magnitude is
-// below 2^-100 is held as zeros (448 divided by it would overflow).
+// below 2^-100 is held as zeros (448 divided by it would overflow). Magnitudes beyond 2^63
+// are held as that, where the square of sqrt(v) is in range: an infinite scale would make every
+// other value of the block NaN, and m beside a sqrt(v) that is held lower a step of any size.
 template <bool SECOND>
 __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int n, float (&f)[8]) {
   float top = 0.f;
@@ -214,6 +216,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int n, flo
   for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
   // magnitudes compare as their bits
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  top = fminf(top, 0x1p63f);
   const bool zero = top < 7.888609052210118e-31f;
   const float inv = zero ? 0.f : __fdividef(kE4m3Max, top);
   float q[8];
@@ -312,8 +315,8 @@ __global__ void __launch_bounds__(THREADS, EIGHT ? 5 : 4)
 
 constexpr int kNormBlocks = 1024;  // partial sums of one launch
 
-// Sum of squares of the block's chunks. fp32 within a thread (some thousand values at most
-// per 2^33 gradients), double between threads and blocks, in a fixed order. A thread has the
+// Sum of squares of the block's chunks. fp32 within a thread (four sums, each of some 9,000 of
+// 2^33 gradients on 152 SMs), double between threads and blocks, in a fixed order. A thread has the
 // loads of four pieces of 8 gradients in flight.
 constexpr int NORM_PIECES = 4;
 constexpr int NORM_CHUNK = CHUNK * NORM_PIECES;
