@@ -413,6 +413,8 @@ pb_status pb_swa_attention(const pb_dims* dims, const void* qk, const void* vt, 
  *   (a, b) -> (a cos t - b sin t, a sin t + b cos t)   for every rotated pair of n,
  * t = position on the pair's axis x the pair's frequency. Computed in fp32, rounded once to
  * bf16; with frequencies up to 1 the angle is off by 2^-24 of a turn at most, at any position.
+ * A normed head whose sum of squares passes fp32's range (values of 1e18 and more) comes out as
+ * zero.
  * ---------------------------------------------------------------------------------- */
 
 #define PB_ROPE_MAX_AXES 4
@@ -529,7 +531,9 @@ typedef enum pb_weight_layout { PB_WEIGHT_IN_OUT = 0, PB_WEIGHT_OUT_IN = 1 } pb_
 /* GELU: z Phi(z). GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. SILU: z / (1 +
  * e^-z). RELU: max(z, 0), with derivative 0 at 0. Computed in fp32. GELU: Phi(z) is off by (1.5 z^2
  * + 24) 2^-24 of itself at most, in its left tail too; by 5e-7 where the result is bf16 and has
- * more than 32 rows (5e-4 of GELU's value at z = -4, an eighth of the result's rounding). */
+ * more than 32 rows (5e-4 of GELU's value at z = -4, an eighth of the result's rounding).
+ * GELU_TANH and SILU: off by (8 |s| + 9) 2^-24 and (1.5 |z| + 9) 2^-24 of the value at most, s =
+ * 2 sqrt(2/pi) (z + 0.044715 z^3). */
 typedef enum pb_activation {
   PB_ACT_NONE = 0,
   PB_ACT_GELU = 1,

@@ -88,3 +88,26 @@ def test_gelu_derivative_fp16(m):
     err = (dx.double() - ref).abs()
     bad = (err > room).any(0)
     assert not bad.any(), (int(bad.sum()), zd[bad][:5], err.max(0).values[bad][:5])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("m", [1, 32, 33, 300])
+def test_sigmoid_forms_relative_to_their_size(m, act):
+    # z sigmoid(s), s = z or 2 sqrt(2 / pi) (z + 0.044715 z^3). Units of 2^-24 of the value: the
+    # exponential's argument -s log2(e) is off by 1.5 of itself for SiLU, where s is exact, and by 8 for
+    # the tanh form (six products and sums, four rounded constants at half): times |s|, from the exponent
+    # on; the exponential's 4, the sum's 1, the reciprocal's 2, the last product's 1.
+    z = torch.cat([every(torch.bfloat16, -20 if act == "silu" else -5, -2.0 ** -10),
+                   every(torch.bfloat16, 2.0 ** -10, 20)])
+    n = z.numel()
+    x = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(64, n + -n % 8, dtype=torch.bfloat16, device="cuda")[:, :n]
+    y = pb.linear(x, w, z, activation=act, out_dtype=torch.float32)
+    zd = z.double()
+    s = zd if act == "silu" else math.sqrt(8 / math.pi) * (zd + 0.044715 * zd ** 3)
+    ref = zd * torch.sigmoid(s)
+    room = ((1.5 if act == "silu" else 8) * s.abs() + 9) * 2.0 ** -24 * ref.abs()
+    room = torch.where(zd > 0, 9 * 2.0 ** -24 * ref.abs() + room * torch.exp(-s.abs()), room)
+    err = (y.double() - ref).abs()
+    bad = (err > room).any(0)
+    assert not bad.any(), (int(bad.sum()), zd[bad][:5], (err / ref.abs()).max(0).values[bad][:5])
