@@ -84,9 +84,13 @@ __device__ __forceinline__ uint16_t from_float(float x) {
 
 // ------------------------------------------------------------------ few tokens
 
-// Values of W that equal shares have to take off the longest one for their second launch
-// (98,304 do: 2048 x 2048 for 32 tokens 10.0 -> 7.4 us; 81,920 do not: 8192 x 8192 for one
-// token 23.3 -> 28.4).
+// Values of W that equal shares have to take off the longest one for their second launch. Measured
+// on 14 shapes for 1, 8 and 32 rows, equal shares against whole tiles: from 340,000 on they gain
+// (10240 x 2048, 376,832: 11.1 against 12.8 us for one row, 15.8 against 21.7 for 32), at 81,920 they
+// lose (8192 x 8192: 26.6 against 22.2, 30.3 against 26.2). Between, the row counts differ: 32 rows
+// gain from 147,456 on (5120 x 5120: 15.9 against 17.1), 1 and 8 rows lose up to a fifth on two
+// waves of tiles (20480 x 1024, 114,688: 10.9 against 9.1) and gain on one (2048 x 2048, 98,304: 4.8
+// against 5.7; 1024 x 4096, 229,376: 4.1 against 9.5).
 constexpr int64_t kFewMinGain = 3 << 15;
 // A wide tile (eight multiplying warps) or a narrow one (four): where narrow tiles give the SMs
 // one each at most, whole tiles need no second launch, and fewer SMs than all still draw the

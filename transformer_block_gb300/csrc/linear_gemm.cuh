@@ -22,12 +22,12 @@
 //   224 us with four, 176 with eight).
 //
 // Bound by the tensor rate for many tokens: 8192 x 20480 x 5120 with GeLU and the stored
-// pre-activation runs at 1870 TFLOP/s in short bursts (98 % of cuBLAS's measured 1904), 1630 over
-// seconds, where the power limit holds both down. A single wave costs 6.5 us (launch, first
-// loads, epilogue, stores) and 0.27 us a k-block for one pair, near the 0.25 that an SM takes for
-// its 32 KB of operands from the L2 cache; with all pairs at work and operands that come from
-// memory 0.33 to 0.41. Fetching them into the L2 cache ahead of the loads costs that path twice
-// (2056 x 4104 for 777 rows: 25 us without, 34 with).
+// pre-activation runs at 1790 to 1885 TFLOP/s in short bursts (94 to 99 % of cuBLAS's measured
+// 1904), 1570 to 1630 over seconds, where the power limit holds both down. A single wave costs
+// 6.5 us (launch, first loads, epilogue, stores) and 0.27 us a k-block for one pair, near the 0.25
+// that an SM takes for its 32 KB of operands from the L2 cache; with all pairs at work and operands
+// that come from memory 0.33 to 0.41. Fetching them into the L2 cache ahead of the loads costs that
+// path twice (2056 x 4104 for 777 rows: 25 us without, 34 with).
 
 namespace {
 
@@ -45,8 +45,11 @@ static_assert(LIN_SMEM <= 227 * 1024, "shared memory of the linear kernel");
 // k-blocks (of 64) that one accumulator sums at most, for each type of result.
 constexpr int kLinearSegment = 14, kLinearSegmentF16 = 112, kLinearSegmentBf16 = 896;
 // k-blocks (0.28 us each) that a part of a split tile has at least, and that splitting has to
-// save at least: partial sums and second launch cost 5 to 10 us (saving 53 of 80 took 333 x
-// 2504 x 5120 from 27.9 to 19.6 us, saving 16 of 32 took 256 x 8192 x 2048 from 15.4 to 19.2).
+// save at least: partial sums and second launch cost 3 to 15 us. Measured over k for 100 to 500 rows
+// on 1024 to 8192 features, split against whole: eight parts even at a saving of 25 (256 x 2048 x
+// 2048, saving 28: 13.3 against 14.3 us), four at 22, three at 23 (100 x 6144 x 2560, saving 26:
+// 16.4 against 16.9), two only at 40 to 60 (256 x 8192 x 3584, saving 28: 24.0 against 21.6; x 8192,
+// saving 64: 38.2 against 40.8).
 constexpr int kLinearMinBlocks = 4, kLinearMinGain = 28;
 
 // One product D[M, N] = A B^T and its epilogue.
