@@ -496,14 +496,15 @@ pb_status pb_qk_norm_rope_backward(const pb_rope* rope, int32_t batch, int32_t s
  * (device, 256-byte aligned, batch * seq * 2 * hidden * 2 bytes) keeps the projection's q and k
  * between pb_forward_train and pb_backward, as their scratch does the rest; dgamma_q and
  * dgamma_k (fp32 [head_dim], or NULL) receive the gammas' gradients, by pb_backward's
- * accumulate. These three overlap nothing else of a training step. `saved` belongs to one forward at a time. The handle remembers which `saved` and
- * which scratch every forward filled, whatever is set afterwards, and pb_backward through a norm
- * is refused where the current `saved` holds no forward, one with another scratch, or one of
- * which a later forward has overwritten either (two forwards in flight: two handles, or this
- * call with another `saved` before each forward and each backward; a captured forward counts
- * when it is captured). The struct is copied; what it points to must stay valid until the calls
- * are done, and the same from pb_forward_train to its pb_backward. NULL takes the step out
- * again. In pb_trace_read its time counts with the attention. */
+ * accumulate. These three overlap nothing else of a training step. `saved` belongs to one
+ * forward at a time. The handle remembers which `saved` and which scratch every forward filled,
+ * whatever is set afterwards, and pb_backward through a norm is refused where the current
+ * `saved` holds no forward, one with another scratch, or one of which a later forward has
+ * overwritten either (two forwards in flight: two handles, or this call with another `saved`
+ * before each forward and each backward; a captured forward counts when it is captured). The
+ * struct is copied; what it points to must stay valid until the calls are done, and the same
+ * from pb_forward_train to its pb_backward. NULL takes the step out again. In pb_trace_read its
+ * time counts with the attention. */
 typedef struct pb_block_rope {
   pb_rope rope;
   const void* gamma_q;
@@ -531,7 +532,7 @@ typedef enum pb_weight_layout { PB_WEIGHT_IN_OUT = 0, PB_WEIGHT_OUT_IN = 1 } pb_
 /* GELU: z Phi(z). GELU_TANH: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. SILU: z / (1 +
  * e^-z). RELU: max(z, 0), with derivative 0 at 0. Computed in fp32. GELU: Phi(z) is off by (1.5 z^2
  * + 24) 2^-24 of itself at most, in its left tail too; by 5e-7 where the result is bf16 and has
- * more than 32 rows (5e-4 of GELU's value at z = -4, an eighth of the result's rounding).
+ * more than 32 rows (of GELU's value 5e-4 at z = -4, an eighth of its rounding, 1.6e-3 at -5).
  * GELU_TANH and SILU: off by (8 |s| + 9) 2^-24 and (1.5 |z| + 9) 2^-24 of the value at most, s =
  * 2 sqrt(2/pi) (z + 0.044715 z^3). */
 typedef enum pb_activation {

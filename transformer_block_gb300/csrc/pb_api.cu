@@ -1773,7 +1773,7 @@ pb_status pb_linear_backward(const pb_linear_grads* args, void* scratch, size_t 
   const int64_t wr = in_out ? a.k : a.n, wc = in_out ? a.n : a.k;
   const Matrix dy{a.dy, a.m, a.n, a.lddy, 2};
   const Matrix x{a.dw != nullptr ? a.x : nullptr, a.m, a.k, a.ldx, 2};
-  const Matrix w{a.dx != nullptr ? a.w : nullptr, wr, wc, a.ldw, 2};
+  const Matrix w{a.dx != nullptr && a.m > 0 ? a.w : nullptr, wr, wc, a.ldw, 2};
   const Matrix pre{mul ? a.pre : nullptr, a.m, a.k, a.ldp, 2};
   const Matrix dx{a.dx, a.m, a.k, a.lddx, 2};
   const Matrix dw{a.dw, wr, wc, a.lddw, 4};
