@@ -95,3 +95,11 @@ def test_views_beyond_all_memory(lib):
                                       None, heads(far, **({"s": 4096 * 512, "b": 0} | o)), None,
                                       None)
             assert got == 2 and "2^48" in message(lib), (b, s, q, o, message(lib))
+
+
+def test_no_tokens_read_no_weights(lib):
+    # accumulating over no tokens leaves everything as it is, wherever the weights lie
+    dw = P + (4 << 24)
+    assert linear_back(lib, m=0, accumulate=1, w=dw) == 0
+    assert linear_back(lib, m=0, accumulate=1, w=W) == 0
+    assert linear_back(lib, m=0, accumulate=1, dw=W) == 1  # a result in scratch
