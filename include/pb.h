@@ -619,6 +619,44 @@ pb_status pb_activation_backward(int64_t rows, int64_t cols, int32_t dtype, int3
                                  void* out, int64_t ldo, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * Serving: attention of packed prompts of different lengths, and of new tokens over a paged cache.
+ * ---------------------------------------------------------------------------------- */
+
+/* Causal attention of packed prompts. q and out [tokens, q.heads, head_dim], k and v [tokens,
+ * k.heads, head_dim], bf16 views (batch_stride is not read); q.heads is a multiple of k.heads, and
+ * head h of q reads head h / (q.heads / k.heads) of k and v, for at most 128 heads of q each.
+ * Sequence s holds the tokens starts[s] <= i < starts[s + 1]: starts is a device array of sequences
+ * + 1 int32 that do not fall, read when the call runs; lengths of zero are allowed, and NULL is one
+ * sequence of all tokens. Token i sees the tokens i - window < j <= i of its sequence:
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j.
+ * Scores, softmax and sums in fp32, its weights rounded to bf16 for the product with v, out
+ * rounded once. Rows of out in no sequence are left as they were, and what q, k and v hold there, or
+ * in another sequence, reaches no result. Within a sequence a v that is not finite makes results of
+ * earlier tokens NaN too (those that share a tile of 128 keys with it). A start outside [0, tokens] is
+ * moved to the nearest end; starts that fall give some rows of out no defined value.
+ * head_dim 64 or 128. Strides of q, k and v of dimensions beyond 1: head_dim at least, below 2^38.
+ * out overlaps nothing else. tokens or sequences 0 does nothing. */
+typedef struct pb_prompt_args {
+  int32_t tokens;
+  int32_t sequences;
+  int32_t head_dim;
+  int32_t window; /* 0: all earlier tokens */
+  float scale;    /* 0: 1 / sqrt(head_dim) */
+  pb_heads q;
+  pb_heads k;
+  pb_heads v;
+  pb_heads out;
+  const int32_t* starts;
+} pb_prompt_args;
+
+/* `scratch` (device, 256-byte aligned, >= pb_prompt_attention_scratch_bytes of the call's tokens
+ * and sequences) needs no preparation and must not be used by another call that may run
+ * concurrently. `status` as in pb_gemm_bf16. */
+pb_status pb_prompt_attention_scratch_bytes(int32_t tokens, int32_t sequences, size_t* bytes);
+pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t scratch_bytes,
+                              int* status, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Optimiser: what follows pb_backward in a training step.
  * ---------------------------------------------------------------------------------- */
 

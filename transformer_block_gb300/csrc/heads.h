@@ -1,7 +1,8 @@
 // heads.h — checks of the arguments that the entry points around the block share: views of heads
-// (pb_heads), vectors beside them, and what they must not overlap.
+// (pb_heads), vectors beside them, what they must not overlap; and their tensor maps.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -12,6 +13,10 @@
 
 namespace pb {
 pb_status record_error(pb_status s, const char* message);
+// Tensor map of one batch entry's heads, [tokens, heads, dh] with the view's strides, read in boxes
+// of 64 values x box_heads x box_tokens with 128-byte swizzle (pb_api.cu).
+pb_status make_heads_map(CUtensorMap* m, const pb_heads& v, int32_t tokens, int32_t dh,
+                         uint32_t box_heads, uint32_t box_tokens);
 
 inline pb_status bad(pb_status s, const char* fmt, const char* what) {
   char msg[200];

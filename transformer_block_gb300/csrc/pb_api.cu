@@ -1001,6 +1001,16 @@ pb_status run_stack(pb_handle* const* layers, int32_t n, const void* x, void* y,
 namespace pb {
 // Records a failure of an entry point defined in another file of the library.
 pb_status record_error(pb_status s, const char* message) { return fail(s, "%s", message); }
+
+pb_status make_heads_map(CUtensorMap* m, const pb_heads& v, int32_t tokens, int32_t dh,
+                         uint32_t box_heads, uint32_t box_tokens) {
+  const uint64_t dims[3] = {uint64_t(dh), uint64_t(v.heads), uint64_t(tokens)};
+  // a dimension of one has no stride of its own
+  const uint64_t strides[2] = {2 * uint64_t(v.heads > 1 ? v.head_stride : dh),
+                               2 * uint64_t(tokens > 1 ? v.seq_stride : int64_t(v.heads) * dh)};
+  const uint32_t box[3] = {64, box_heads, box_tokens};
+  return make_map(m, v.ptr, 3, dims, strides, box);
+}
 }  // namespace pb
 
 extern "C" {

@@ -1,0 +1,717 @@
+// prompt.cu — causal attention of packed prompts of different lengths, with grouped heads, on the
+// tensor cores.
+//
+// Sequence s holds the tokens starts[s] <= i < starts[s + 1]; query head h reads key head h / g.
+//   o_i = sum_{k in s, 0 <= i - k < w} softmax_k(scale q_i . k_k) v_k
+//
+// Rows. The g heads of a key head read the same keys, so a tile of 128 rows holds T = 128 / g
+// (rounded down) tokens with all their g heads: row r is head r mod g of token r / g. One TMA box of
+// 64 columns x g heads x T tokens writes it. Each tile then needs one key head's keys up to its last
+// token, whatever g is, and a short prompt fills its rows with heads instead of padding.
+//
+// Items. An item is two such tiles that follow one another in a sequence (2 T tokens) and share
+// every key and value tile. How many items there are is known on the device only (starts): a first
+// launch lists them, longest first (by the first token's place in its sequence, counted into
+// buckets), and the main launch, one block an SM, deals the list out in rounds of alternating
+// direction. The second launch's set-up runs beside the first.
+//
+// Inside a block, as in swa.cu: warp 0 loads by TMA (K 3 stages, V 2), warp 1's first thread issues
+// the products in the order S0, S1, then O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of the next
+// tile; warp 2 folds the landings of V and of the next K into P0's barrier; two groups of four warps
+// take the softmax, a row a thread. P (bf16, as all attention of the library; its error averages
+// over the keys) lies over S in tensor memory. The softmax's maximum, its sum and O are fp32; O is
+// rescaled only where a maximum grows by more than 2^8. V comes as it is stored, [keys, head_dim]: the
+// product reads it as an MN-major operand, so no transposed copy is made.
+//
+// A key tile at a sequence's end holds rows of the next sequence, or of nothing. Their scores are
+// replaced, not added to; their values would still meet P = 0, and 0 x NaN is NaN, so warp 2 writes
+// zeros over those rows of V before the product reads them. Nothing of another sequence reaches a
+// result.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "heads.h"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace pb {
+namespace {
+
+constexpr int BQ = 128, BKV = 128;
+constexpr int THREADS = 384;
+// Registers a thread: at launch (the most 384 threads may have), then per warpgroup.
+constexpr uint32_t kRegsLaunch = 168, kRegsControl = 96, kRegsSoftmax = 200;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= THREADS * kRegsLaunch,
+              "register split exceeds the launch allocation");
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int BOX = 128 * 64 * 2;          // 128 rows x 64 columns of 16 bits
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr uint64_t kLimitNs = 2000000000ull;
+constexpr int kBuckets = 2048;
+
+// Scratch: the number of entries, then the entries: a pair of tiles of a sequence (every key head
+// has one item for it).
+struct Entry {
+  int first;  // the sequence's first token
+  int n;      // its length
+  int q0;     // the pair's first token, counted from the sequence's
+  int pad;
+};
+constexpr size_t kHeaderBytes = 256;
+
+struct Params {
+  int tokens, sequences;
+  int kv_heads, group, tile_tokens;
+  int window;  // at least 1
+  float scale_log2;
+  int shift;      // bucket = pair index >> shift
+  int capacity;   // entries that scratch holds
+  const int* starts;  // or null: one sequence
+  __nv_bfloat16* out;
+  int64_t out_ss, out_hs;
+};
+
+__device__ __forceinline__ int2 sequence(const Params& p, int s) {
+  if (p.starts == nullptr) return make_int2(0, p.tokens);
+  const int a = min(max(p.starts[s], 0), p.tokens);
+  return make_int2(a, max(min(max(p.starts[s + 1], 0), p.tokens) - a, 0));
+}
+
+// Lists the pairs of all sequences, later ones of a sequence (more keys) first.
+__global__ void __launch_bounds__(1024) list_kernel(const Params p, int* count, Entry* entries,
+                                                    int* status) {
+  __shared__ int at[kBuckets];
+  __shared__ int sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  for (int b = tid; b < kBuckets; b += 1024) at[b] = 0;
+  __syncthreads();
+  const int pair_tokens = 2 * p.tile_tokens;
+  for (int s = warp; s < p.sequences; s += 32) {
+    const int pairs = (sequence(p, s).y + pair_tokens - 1) / pair_tokens;
+    for (int i = lane; i < pairs; i += 32) atomicAdd(&at[i >> p.shift], 1);
+  }
+  __syncthreads();
+  // bucket b starts behind all buckets above it: thread t takes buckets kBuckets - 1 - 2t, - 2t - 1
+  const int b1 = kBuckets - 1 - 2 * tid, b0 = b1 - 1;
+  const int n1 = at[b1], n0 = at[b0];
+  int x = n1 + n0;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < warp; ++i) before += sums[i];
+  x += before;
+  at[b1] = x - n1 - n0;
+  at[b0] = x - n0;
+  if (tid == 1023) {
+    *count = min(x, p.capacity);
+    // falling starts: sequences that overlap, more pairs than tokens allow
+    if (x > p.capacity && status != nullptr) atomicCAS(status, 0, int(PB_ERR_INVALID_ARG));
+  }
+  __syncthreads();
+  for (int s = warp; s < p.sequences; s += 32) {
+    const int2 q = sequence(p, s);
+    const int pairs = (q.y + pair_tokens - 1) / pair_tokens;
+    for (int i = lane; i < pairs; i += 32) {
+      const int e = atomicAdd(&at[i >> p.shift], 1);
+      if (e < p.capacity) entries[e] = Entry{q.x, q.y, i * pair_tokens, 0};
+    }
+  }
+}
+
+// One softmax row of a tile: p_k = 2^(s_k c - m) rounded to bf16 into tensor memory at t_s
+// (column m holds keys 2m and 2m + 1); returns the fp32 sum of the unrounded p_k.
+__device__ __forceinline__ float probs_to_tmem(const float (&s)[BKV], float c, float m,
+                                               uint32_t t_s) {
+  const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
+  uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int ch = 0; ch < BKV / 32; ++ch) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t x2 = f2_fma(f2(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]), c2, nm2);
+      float x0, x1;
+      f2_split(x2, x0, x1);
+      const uint64_t a2 = f2(ex2_approx(x0), ex2_approx(x1));
+      acc[e & 3] = f2_add(acc[e & 3], a2);
+      float a0, a1;
+      f2_split(a2, a0, a1);
+      pk[e] = pack_bf16x2(a0, a1);
+    }
+    tmem_st16(t_s + uint32_t(ch * 16), pk);
+  }
+  const uint64_t t = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+  float lo, hi;
+  f2_split(t, lo, hi);
+  return lo + hi;
+}
+
+template <int DH>
+struct Layout {
+  static constexpr int Q_TILE = BQ * DH * 2;
+  static constexpr int KV_BYTES = BKV * DH * 2;
+  static constexpr int K_STAGES = 3, V_STAGES = 2;
+  static constexpr int K_OFF = 2 * Q_TILE;
+  static constexpr int V_OFF = K_OFF + K_STAGES * KV_BYTES;
+  static constexpr int BAR_OFF = V_OFF + V_STAGES * KV_BYTES;
+  static constexpr int NUM_BARS = 19;
+  static constexpr size_t NEED = size_t(BAR_OFF) + NUM_BARS * 8 + 16 + 1024;
+  // so much that one block fits an SM: it takes all 512 columns of tensor memory
+  static constexpr size_t SMEM = NEED > 200 * 1024 ? NEED : 200 * 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory layout");
+};
+
+struct Item {
+  int kv;                  // key head
+  int first, n, q0;        // as in Entry
+  int kb0, ke0, kb1, ke1;  // key tiles [kb, ke] of row tile 0 / 1 (none: ke < kb)
+  int U;                   // tiles from kb0 to the last one
+};
+
+__device__ __forceinline__ Item make_item(const Params& p, const Entry* entries, int r) {
+  Item it;
+  const int e = r / p.kv_heads;
+  it.kv = r - e * p.kv_heads;
+  const int4 v = *reinterpret_cast<const int4*>(entries + e);
+  it.first = v.x;
+  it.n = v.y;
+  it.q0 = v.z;
+  int kb[2], ke[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int qb = it.q0 + h * p.tile_tokens;
+    kb[h] = qb < it.n ? max(0, qb - p.window + 1) / BKV : 1;
+    ke[h] = qb < it.n ? (min(qb + p.tile_tokens, it.n) - 1) / BKV : 0;
+  }
+  it.kb0 = kb[0];
+  it.ke0 = ke[0];
+  it.kb1 = kb[1];
+  it.ke1 = ke[1];
+  it.U = max(ke[0], ke[1]) - kb[0] + 1;
+  return it;
+}
+
+__device__ __forceinline__ bool item_needs(const Item& it, int h, int j) {
+  return h ? (j >= it.kb1 && j <= it.ke1) : (j >= it.kb0 && j <= it.ke0);
+}
+
+__device__ __forceinline__ int item_index(int n, int c, int G) {
+  return n * G + ((n & 1) ? G - 1 - c : c);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(THREADS, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const Params p, const int* count,
+                  const Entry* entries, int* status) {
+  using L = Layout<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  const uint32_t q_full = smem_u32(bars + 0);
+  const uint32_t q_empty = smem_u32(bars + 1);    // the item's last S products are done
+  const uint32_t k_full0 = smem_u32(bars + 2);    // [3]
+  const uint32_t k_empty0 = smem_u32(bars + 5);   // [3]
+  const uint32_t v_full0 = smem_u32(bars + 8);    // [2]
+  const uint32_t v_empty0 = smem_u32(bars + 10);  // [2]
+  const uint32_t s_full0 = smem_u32(bars + 12);   // [2] per row tile
+  const uint32_t p_full0 = smem_u32(bars + 14);   // [2] per row tile (4 warps each)
+  const uint32_t o_final0 = smem_u32(bars + 16);  // [2] per row tile: the item's last PV is done
+  const uint32_t drain_bar = smem_u32(bars + 18);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int G = int(gridDim.x), cta = int(blockIdx.x);
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(k_full0 + 8 * s, 1);
+      mbar_init(k_empty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(v_full0 + 8 * s, 1);
+      mbar_init(v_empty0 + 8 * s, 1);
+      mbar_init(s_full0 + 8 * s, 1);
+      mbar_init(p_full0 + 8 * s, s == 0 ? 5 : 4);  // row tile 0: and warp 2
+      mbar_init(o_final0 + 8 * s, 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // the list is written, and what the launches before it wrote
+  const int num_items = *count * p.kv_heads;
+  const WaitCtl wc{abort_flag, status, kLimitNs};
+  const uint64_t drain_ns = kLimitNs > kDrainFloorNs ? kLimitNs : kDrainFloorNs;
+  const uint32_t sQ = smem_u32(smem);
+  const uint32_t sK = smem_u32(smem + L::K_OFF);
+  const uint32_t sV = smem_u32(smem + L::V_OFF);
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsControl>();
+    if (warp == 0) {
+      if (lane == 0) {
+        // -------------------------------------------------------------- producer
+        // K and V rings run on across items. Per stage: parity of its last load (bit s), ever
+        // loaded.
+        const uint32_t q_bytes = uint32_t(2 * (DH / 64) * 128) * uint32_t(p.group * p.tile_tokens);
+        uint32_t kc = 0, vc = 0;
+        uint32_t k_par = 0, v_par = 0, k_used = 0, v_used = 0;
+        int n_done = 0;
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+          const int r = item_index(n, cta, G);
+          if (r >= num_items) break;
+          const Item it = make_item(p, entries, r);
+          // the Q tiles of the previous item are free once its last S products completed
+          if (!mbar_wait(q_empty, (n & 1) ^ 1, wc, 20)) break;
+          mbar_arrive_expect_tx(q_full, q_bytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int hb = 0; hb < DH / 64; ++hb)
+              tma_load_3d(sQ + h * L::Q_TILE + hb * BOX, &tmQ, q_full, hb * 64, it.kv * p.group,
+                          it.first + it.q0 + h * p.tile_tokens);
+          n_done = n + 1;
+          auto load_k = [&](int idx) -> bool {
+            const uint32_t g = kc + uint32_t(idx);
+            const uint32_t st = g % 3, par = (g / 3) & 1;
+            if (!mbar_wait(k_empty0 + 8 * st, par ^ 1, wc, 11)) return false;
+            mbar_arrive_expect_tx(k_full0 + 8 * st, L::KV_BYTES);
+#pragma unroll
+            for (int hb = 0; hb < DH / 64; ++hb)
+              tma_load_3d(sK + st * L::KV_BYTES + hb * BOX, &tmK, k_full0 + 8 * st, hb * 64, it.kv,
+                          it.first + (it.kb0 + idx) * BKV);
+            k_par = (k_par & ~(1u << st)) | (par << st);
+            k_used |= 1u << st;
+            return true;
+          };
+          auto load_v = [&](int idx) -> bool {
+            const uint32_t g = vc + uint32_t(idx);
+            const uint32_t st = g & 1, par = (g >> 1) & 1;
+            if (!mbar_wait(v_empty0 + 8 * st, par ^ 1, wc, 10)) return false;
+            mbar_arrive_expect_tx(v_full0 + 8 * st, L::KV_BYTES);
+#pragma unroll
+            for (int hb = 0; hb < DH / 64; ++hb)
+              tma_load_3d(sV + st * L::KV_BYTES + hb * BOX, &tmV, v_full0 + 8 * st, hb * 64, it.kv,
+                          it.first + (it.kb0 + idx) * BKV);
+            v_par = (v_par & ~(1u << st)) | (par << st);
+            v_used |= 1u << st;
+            return true;
+          };
+          // K runs one tile ahead of V: the next tile's S is issued before this one's P V
+          ok = load_k(0);
+          for (int idx = 0; ok && idx < it.U; ++idx) {
+            if (idx + 1 < it.U) ok = load_k(idx + 1);
+            if (ok) ok = load_v(idx);
+          }
+          kc += uint32_t(it.U);
+          vc += uint32_t(it.U);
+        }
+        if (n_done > 0) mbar_wait_drain(q_full, uint32_t(n_done - 1) & 1, drain_ns);
+        for (uint32_t s = 0; s < 3; ++s)
+          if (k_used & (1u << s)) mbar_wait_drain(k_full0 + 8 * s, (k_par >> s) & 1u, drain_ns);
+        for (uint32_t s = 0; s < 2; ++s)
+          if (v_used & (1u << s)) mbar_wait_drain(v_full0 + 8 * s, (v_par >> s) & 1u, drain_ns);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // -------------------------------------------------------------- products
+        const uint32_t id_s = idesc_bf16_f32(BQ, BKV);
+        const uint32_t id_o = idesc_f32acc(BQ, DH, false, false, true);
+        const uint64_t dQ = sdesc_kmajor_sw128(sQ), dK = sdesc_kmajor_sw128(sK),
+                       dV = sdesc_mnmajor_sw128(sV, BOX);
+        uint32_t kc = 0, vc = 0, tb = 0;  // K, V tiles and tiles of the pair consumed so far
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+          const int r = item_index(n, cta, G);
+          if (r >= num_items) break;
+          const Item it = make_item(p, entries, r);
+          // S_h = Q_h K^T for the pair's tile idx (nothing where row tile h does not need it);
+          // the item's last S products read Q for the last time
+          auto issue_s = [&](int h, int idx) {
+            const uint32_t st = (kc + uint32_t(idx)) % 3;
+            if (item_needs(it, h, it.kb0 + idx)) {
+              const uint64_t da = dQ + uint64_t((h * L::Q_TILE) >> 4);
+              const uint64_t db = dK + uint64_t((st * L::KV_BYTES) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint64_t off = uint64_t(((kk >> 2) * BOX) >> 4) + 2 * (kk & 3);
+                mma_f16kind_ss(tmem_base + uint32_t(h * BKV), da + off, db + off, id_s,
+                               kk > 0 ? 1u : 0u);
+              }
+            }
+            mma_commit(s_full0 + 8 * h);
+            if (h == 1) {
+              mma_commit(k_empty0 + 8 * st);  // both S products have K
+              if (idx + 1 == it.U) mma_commit(q_empty);
+            }
+          };
+          if (!mbar_wait(q_full, uint32_t(n) & 1, wc, 12) ||
+              !mbar_wait(k_full0 + 8 * (kc % 3), (kc / 3) & 1, wc, 14))
+            break;
+          tc_fence_after();
+          issue_s(0, 0);
+          issue_s(1, 0);
+          uint32_t pv_started = 0;  // bit h: O_h holds this item's partial sum
+          for (int idx = 0; ok && idx < it.U; ++idx) {
+            const int j = it.kb0 + idx;
+            const uint32_t gv = vc + uint32_t(idx);
+            const uint64_t dv = dV + uint64_t(((gv & 1) * L::KV_BYTES) >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // P_0's phase also says that V tile gv and the next K tile have landed (warp 2)
+              if (!mbar_wait(p_full0 + 8 * h, (tb + uint32_t(idx)) & 1, wc, 13)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (item_needs(it, h, j)) {
+                const uint32_t t_p = tmem_base + uint32_t(h * BKV);
+                const uint32_t t_o = tmem_base + 256u + uint32_t(h * 128);
+#pragma unroll
+                for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: two 8-row atoms of 1024 bytes
+                  mma_f16kind_ts(t_o, t_p + uint32_t(kk * 8), dv + uint64_t((kk * 2048) >> 4), id_o,
+                                 ((pv_started >> h) & 1u) | (kk > 0 ? 1u : 0u));
+                pv_started |= 1u << h;
+              }
+              if (h == 1) mma_commit(v_empty0 + 8 * (gv & 1));  // both PV products have V
+              if (idx + 1 == it.U) mma_commit(o_final0 + 8 * h);  // once an item
+              if (idx + 1 < it.U) issue_s(h, idx + 1);
+            }
+          }
+          kc += uint32_t(it.U);
+          vc += uint32_t(it.U);
+          tb += uint32_t(it.U);
+        }
+        mma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0, drain_ns);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- landings
+      // Waits for the V tile of each step and the K tile of the next one, writes zeros over V's
+      // rows behind the sequence, and arrives on row tile 0's P barrier. A stage cannot be
+      // refilled before that phase completes: the products read it only afterwards.
+      uint32_t kc = 0, vc = 0, tb = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int r = item_index(n, cta, G);
+        if (r >= num_items) break;
+        const Item it = make_item(p, entries, r);
+        for (int idx = 0; idx < it.U; ++idx) {
+          const uint32_t gv = vc + uint32_t(idx), gk = kc + uint32_t(idx + 1);
+          if (!mbar_wait_warp(v_full0 + 8 * (gv & 1), (gv >> 1) & 1, wc, 17) ||
+              (idx + 1 < it.U &&
+               !mbar_wait_warp(k_full0 + 8 * (gk % 3), (gk / 3) & 1, wc, 15))) {
+            ok = false;
+            break;
+          }
+          const int live = it.n - (it.kb0 + idx) * BKV;  // rows of the tile in the sequence
+          if (live < BKV) {
+            uint8_t* v = smem + L::V_OFF + (gv & 1) * L::KV_BYTES;
+#pragma unroll 1
+            for (int hb = 0; hb < DH / 64; ++hb)
+#pragma unroll 4
+              for (int b = live * 128 + int(lane) * 16; b < BKV * 128; b += 512)
+                *reinterpret_cast<uint4*>(v + hb * BOX + b) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full0);
+          if (!mbar_wait_warp(p_full0, (tb + uint32_t(idx)) & 1, wc, 19)) {
+            ok = false;
+            break;
+          }
+        }
+        kc += uint32_t(it.U);
+        vc += uint32_t(it.U);
+        tb += uint32_t(it.U);
+      }
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------------ softmax
+    const int h = (warp >= 8) ? 1 : 0;  // row tile of this warpgroup
+    const uint32_t quad = warp & 3;
+    const int row = int(quad * 32 + lane);  // = lane of tensor memory
+    const int tok = row / p.group, head = row - tok * p.group;
+    const uint32_t lane_addr = (quad * 32u) << 16;
+    const uint32_t t_s = tmem_base + lane_addr + uint32_t(h * BKV);
+    const uint32_t t_o = tmem_base + lane_addr + 256u + uint32_t(h * 128);
+    const uint32_t s_full = s_full0 + 8 * h, p_full = p_full0 + 8 * h;
+    const float c = p.scale_log2;
+    uint32_t tb = 0;  // tiles of earlier items
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int ri = item_index(n, cta, G);
+      if (ri >= num_items) break;
+      const Item it = make_item(p, entries, ri);
+      const int qb = it.q0 + h * p.tile_tokens;
+      const int i = qb + tok;  // place in the sequence
+      const int kb_h = h ? it.kb1 : it.kb0, ke_h = h ? it.ke1 : it.ke0;
+      float m_used = -INFINITY, l = 0.f;
+      bool has_o = false;
+      for (int idx = 0; idx < it.U; ++idx) {
+        const int j = it.kb0 + idx;
+        if (!mbar_wait_warp(s_full, (tb + uint32_t(idx)) & 1, wc, 16)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (j >= kb_h && j <= ke_h) {
+          uint32_t u[BKV];
+#pragma unroll
+          for (int ch = 0; ch < BKV / 32; ++ch)
+            tmem_ld32(t_s + uint32_t(ch * 32), *reinterpret_cast<uint32_t(*)[32]>(u + ch * 32));
+          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(u));
+          tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 32));
+          tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 64));
+          tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 96));
+          float s[BKV];
+#pragma unroll
+          for (int e = 0; e < BKV; ++e) s[e] = __uint_as_float(u[e]);
+          const int k0 = j * BKV;
+          const bool whole =
+              (k0 + BKV - 1 <= qb) && (qb + p.tile_tokens - 1 - k0 < p.window);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < BKV; ++e)  // 0 <= i - k < window in one comparison
+              if (uint32_t(i - (k0 + e)) >= uint32_t(p.window)) s[e] = -INFINITY;
+          }
+          float mx4[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float a = s[32 * q];
+#pragma unroll
+            for (int e = 1; e < 31; e += 2) a = max3f(a, s[32 * q + e], s[32 * q + e + 1]);
+            mx4[q] = fmaxf(a, s[32 * q + 31]);
+          }
+          const float mx = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
+          const float mxs = mx * c;
+          // the reference maximum moves only when the row's grew by more than 2^8 (from -inf, any
+          // finite one does); O is rescaled below, after P is stored
+          const bool grow = mxs > m_used + kRescaleThreshold;
+          const float alpha = grow ? ex2_approx(m_used - mxs) : 1.f;
+          if (grow) {
+            l *= alpha;
+            m_used = mxs;
+          }
+          const float m_eff = (m_used == -INFINITY) ? 0.f : m_used;
+          l += probs_to_tmem(s, c, m_eff, t_s);
+          tmem_st_wait();
+          if (has_o && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+            for (int ch = 0; ch < DH / 32; ++ch) {
+              uint32_t w[32];
+              tmem_ld32(t_o + uint32_t(ch * 32), w);
+              tmem_ld_wait(w);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+              tmem_st32(t_o + uint32_t(ch * 32), w);
+            }
+            tmem_st_wait();
+          }
+          has_o = true;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      tb += uint32_t(it.U);
+      if (has_o && !mbar_wait_warp(o_final0 + 8 * h, uint32_t(n) & 1, wc, 18)) break;
+      if (has_o) {
+        tc_fence_after();
+        const float inv_l = 1.f / l;
+        const bool live = tok < p.tile_tokens && i < it.n;
+        __nv_bfloat16* dst =
+            p.out + int64_t(it.first + i) * p.out_ss + int64_t(it.kv * p.group + head) * p.out_hs;
+#pragma unroll
+        for (int ch = 0; ch < DH / 32; ++ch) {
+          uint32_t u[32];
+          tmem_ld32(t_o + uint32_t(ch * 32), u);
+          tmem_ld_wait(u);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[8 * q + e]) * inv_l;
+              reinterpret_cast<uint4*>(dst + ch * 32)[q] =
+                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            }
+          }
+        }
+      }
+    }  // items
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+int64_t most_entries(int64_t tokens, int64_t sequences, int tile_tokens) {
+  return tokens / (2 * tile_tokens) + sequences;
+}
+
+template <int DH>
+cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   const Params& p, void* scratch, int* status, cudaStream_t stream) {
+  using L = Layout<DH>;
+  static PerDeviceInit setup;  // per device: the shared-memory opt-in, and the number of SMs
+  int sms = 0;
+  cudaError_t e = per_device_init(
+      setup,
+      [](int dev, int* value) {
+        const cudaError_t a = cudaFuncSetAttribute(
+            prompt_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::SMEM));
+        return a != cudaSuccess
+                   ? a
+                   : cudaDeviceGetAttribute(value, cudaDevAttrMultiProcessorCount, dev);
+      },
+      &sms);
+  if (e != cudaSuccess) return e;
+  int* count = static_cast<int*>(scratch);
+  Entry* entries = reinterpret_cast<Entry*>(static_cast<uint8_t*>(scratch) + kHeaderBytes);
+  e = launch_dependent(list_kernel, dim3(1), dim3(1024), 0, 1, stream, p, count, entries, status);
+  if (e != cudaSuccess) return e;
+  const int64_t items = int64_t(p.capacity) * p.kv_heads;
+  return launch_dependent(prompt_kernel<DH>, dim3(unsigned(items < sms ? items : sms)),
+                          dim3(THREADS), L::SMEM, 1, stream, tmQ, tmK, tmV, p,
+                          static_cast<const int*>(count), static_cast<const Entry*>(entries), status);
+}
+
+}  // namespace
+}  // namespace pb
+
+using namespace pb;
+
+extern "C" {
+
+pb_status pb_prompt_attention_scratch_bytes(int32_t tokens, int32_t sequences, size_t* bytes) {
+  if (bytes == nullptr) return record_error(PB_ERR_INVALID_ARG, "bytes is NULL");
+  if (tokens < 0 || sequences < 0)
+    return record_error(PB_ERR_INVALID_ARG, "tokens and sequences must be >= 0");
+  *bytes = kHeaderBytes + size_t(most_entries(tokens, sequences, 1)) * sizeof(Entry);
+  return PB_OK;
+}
+
+pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t scratch_bytes,
+                              int* status, void* stream) {
+  if (args == nullptr) return record_error(PB_ERR_INVALID_ARG, "args is NULL");
+  const pb_prompt_args& a = *args;
+  if (a.tokens < 0 || a.sequences < 0)
+    return record_error(PB_ERR_INVALID_ARG, "tokens and sequences must be >= 0");
+  if (a.head_dim != 64 && a.head_dim != 128)
+    return record_error(PB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (a.window < 0) return record_error(PB_ERR_INVALID_ARG, "window must be >= 0");
+  if (!(a.scale >= 0.f && std::isfinite(a.scale)))
+    return record_error(PB_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (a.tokens > 0x7fffffff - 1024)  // tiles end up to 256 rows behind the last token
+    return record_error(PB_ERR_UNSUPPORTED, "more than 2^31 - 1025 tokens");
+  if (a.sequences > (1 << 24))
+    return record_error(PB_ERR_UNSUPPORTED, "more than 2^24 sequences");
+  if (a.tokens == 0 || a.sequences == 0) return PB_OK;
+  if (a.starts == nullptr && a.sequences != 1)
+    return record_error(PB_ERR_INVALID_ARG, "starts may be NULL for one sequence only");
+  if ((reinterpret_cast<uintptr_t>(a.starts) & 3) != 0)
+    return record_error(PB_ERR_INVALID_ARG, "starts must be 4-byte aligned");
+  const pb_heads* view[4] = {&a.q, &a.k, &a.v, &a.out};
+  static const char* const name[4] = {"q", "k", "v", "out"};
+  for (int i = 0; i < 4; ++i) {
+    pb_status s = check_view(view[i], name[i], 1, a.tokens, a.head_dim, i == 3);
+    if (s != PB_OK) return s;
+  }
+  if (a.k.heads != a.v.heads)
+    return record_error(PB_ERR_INVALID_ARG, "k and v have different numbers of heads");
+  if (a.q.heads != a.out.heads)
+    return record_error(PB_ERR_INVALID_ARG, "q and out have different numbers of heads");
+  if (a.q.heads % a.k.heads != 0)
+    return record_error(PB_ERR_INVALID_ARG, "q's heads must be a multiple of k's");
+  const int group = a.q.heads / a.k.heads;
+  if (group > BQ)
+    return record_error(PB_ERR_UNSUPPORTED, "more than 128 heads of q for one of k");
+  for (int i = 0; i < 3; ++i)  // a tensor map's strides have 40 bits; broadcast views have none
+    if ((a.tokens > 1 && (view[i]->seq_stride < a.head_dim ||
+                          view[i]->seq_stride >= (int64_t(1) << 38))) ||
+        (view[i]->heads > 1 && (view[i]->head_stride < a.head_dim ||
+                                view[i]->head_stride >= (int64_t(1) << 38))))
+      return bad(PB_ERR_UNSUPPORTED, "%s: strides must be head_dim at least, and below 2^38",
+                 name[i]);
+  for (int i = 0; i < 3; ++i)
+    if (!disjoint(a.out, *view[i], 1, a.tokens, a.head_dim))
+      return bad(PB_ERR_INVALID_ARG, "out overlaps %s", name[i]);
+  const int tile_tokens = BQ / group;
+  const int64_t capacity = most_entries(a.tokens, a.sequences, tile_tokens);
+  const size_t need = kHeaderBytes + size_t(capacity) * sizeof(Entry);
+  if (scratch == nullptr || (reinterpret_cast<uintptr_t>(scratch) & 255) != 0)
+    return record_error(PB_ERR_INVALID_ARG, "scratch must be a 256-byte aligned device pointer");
+  if (scratch_bytes < need)
+    return record_error(PB_ERR_WORKSPACE, "scratch is smaller than pb_prompt_attention_scratch_bytes");
+  if (capacity * a.k.heads > 0x7fffffff - 65536)
+    return record_error(PB_ERR_UNSUPPORTED, "more than 2^31 items of work");
+  const Flat scr{scratch, need}, starts{a.starts, a.starts ? (size_t(a.sequences) + 1) * 4 : 0};
+  for (int i = 0; i < 4; ++i)
+    if (!apart(scr, view[i], 1, a.tokens, a.head_dim))
+      return bad(PB_ERR_INVALID_ARG, "%s overlaps scratch", name[i]);
+  if (!apart(starts, &a.out, 1, a.tokens, a.head_dim) || !apart(starts, scr))
+    return record_error(PB_ERR_INVALID_ARG, "starts overlaps out or scratch");
+
+  CUtensorMap tm[3];
+  const uint32_t box[3][2] = {{uint32_t(group), uint32_t(tile_tokens)}, {1, BKV}, {1, BKV}};
+  for (int i = 0; i < 3; ++i) {
+    const pb_status s = make_heads_map(&tm[i], *view[i], a.tokens, a.head_dim, box[i][0], box[i][1]);
+    if (s != PB_OK) return s;
+  }
+  Params p{};
+  p.tokens = a.tokens;
+  p.sequences = a.sequences;
+  p.kv_heads = a.k.heads;
+  p.group = group;
+  p.tile_tokens = tile_tokens;
+  p.window = a.window == 0 ? 0x7fffffff : a.window;
+  const double scale = a.scale == 0.f ? 1.0 / std::sqrt(double(a.head_dim)) : double(a.scale);
+  p.scale_log2 = float(1.4426950408889634 * scale);
+  while (((a.tokens / (2 * tile_tokens)) >> p.shift) >= kBuckets) ++p.shift;
+  p.capacity = int(capacity);
+  p.starts = a.starts;
+  p.out = static_cast<__nv_bfloat16*>(a.out.ptr);
+  p.out_ss = a.tokens > 1 ? a.out.seq_stride : 0;
+  p.out_hs = a.out.heads > 1 ? a.out.head_stride : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a.head_dim == 128 ? launch<128>(tm[0], tm[1], tm[2], p, scratch, status, st)
+                                          : launch<64>(tm[0], tm[1], tm[2], p, scratch, status, st);
+  return e == cudaSuccess ? PB_OK : cuda_failed(e, "prompt attention launch");
+}
+
+}  // extern "C"

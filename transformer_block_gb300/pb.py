@@ -127,6 +127,12 @@ class pb_adamw_args(ctypes.Structure):
         ("d_grad_scale", ctypes.c_void_p)]
 
 
+class pb_prompt_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "sequences", "head_dim", "window")] + [
+        ("scale", ctypes.c_float)] + [(n, pb_heads) for n in ("q", "k", "v", "out")] + [
+        ("starts", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes); every function of include/pb.h
 _P, _S, _I32, _I64, _U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, \
     ctypes.c_uint64
@@ -179,6 +185,8 @@ SIGNATURES = {
     "pb_linear_backward": (ctypes.c_int, [_P, _P, _S, _P, _P]),
     "pb_activation_backward": (ctypes.c_int, [_I64, _I64, _I32, _I32, _P, _I64, _P, _I64, _P,
                                               _I64, _P]),
+    "pb_prompt_attention_scratch_bytes": (ctypes.c_int, [_I32, _I32, ctypes.POINTER(_S)]),
+    "pb_prompt_attention": (ctypes.c_int, [_P, _P, _S, _P, _P]),
     "pb_adamw": (ctypes.c_int, [_P, _I32, _P, _P]),
     "pb_grad_norm_scratch_bytes": (ctypes.c_int, [_I32, ctypes.POINTER(_S)]),
     "pb_grad_norm": (ctypes.c_int, [_I32, _P, _I32, ctypes.c_float, _P, _P, _S, _P]),
@@ -892,6 +900,79 @@ def activation_backward(dy, pre, activation: str, out=None, stream=None):
         _rows(dy, rows, cols, dy.dtype, "dy"), _ptr(pre),
         _rows(pre, rows, cols, dy.dtype, "pre"), _ptr(out),
         _rows(out, rows, cols, dy.dtype, "out"), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------- attention of packed prompts
+
+def _token_heads(t, tokens: int, heads: int | None, dh: int, what: str):
+    """The fields of ``pb_heads`` of a [tokens, heads, head_dim] bf16 view."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{what} must be a bfloat16 [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n != tokens or d != dh or (heads is not None and h != heads) or (s2 != 1 and d > 1):
+        raise ValueError(f"{what} must be [{tokens}, {'heads' if heads is None else heads}, {dh}], "
+                         "a head's values contiguous")
+    return t.data_ptr(), h, 0, s0 if n > 1 else 0, s1 if h > 1 else 0
+
+
+# pb_prompt_args as bytes
+_PROMPT_FORMAT = "@4if" + "Piqqq" * 4 + "P"
+_pack_prompt = struct.Struct(_PROMPT_FORMAT).pack
+assert struct.calcsize(_PROMPT_FORMAT) == ctypes.sizeof(pb_prompt_args)
+
+
+@functools.cache
+def prompt_attention_scratch_bytes(tokens: int, sequences: int) -> int:
+    n = ctypes.c_size_t()
+    _check("pb_prompt_attention_scratch_bytes",
+           lib().pb_prompt_attention_scratch_bytes(tokens, sequences, ctypes.byref(n)))
+    return n.value
+
+
+def _sequences(starts, what: str = "starts") -> int:
+    """The number of sequences of an int32 [sequences + 1] tensor of their first tokens."""
+    _is(starts.dtype is torch.int32 and starts.dim() == 1 and starts.numel() > 0
+        and starts.is_contiguous(), f"{what} must be a contiguous int32 [sequences + 1]")
+    return starts.numel() - 1
+
+
+def _window(window) -> int:
+    _is(window is None or window > 0, "window must be positive, or None")
+    return 0 if window is None else min(int(window), 2 ** 31 - 1)
+
+
+def _scale(scale) -> float:
+    _is(scale is None or scale > 0, "scale must be positive, or None")
+    return 0.0 if scale is None else float(scale)
+
+
+def prompt_attention(q, k, v, starts=None, window=None, scale=None, out=None, scratch=None,
+                     status=None, stream=None):
+    """``pb_prompt_attention``: causal attention of packed prompts, ``q`` [tokens, heads, head_dim],
+    ``k`` and ``v`` [tokens, key heads, head_dim] (bf16 views). ``starts``: int32 [sequences + 1],
+    the first token of each sequence and the end of the last (None: one sequence). A token sees
+    ``window`` tokens, itself included (None: all before it); ``scale`` is 1 / sqrt(head_dim) unless
+    given. Rows of ``out`` in no sequence stay as they are: give ``out`` where there are such rows
+    (a new one holds anything there)."""
+    if stream is not None:
+        return _run_on(stream, prompt_attention, q, k, v, starts, window, scale, out, scratch, status)
+    tokens, _, d = q.shape
+    n = 1 if starts is None else _sequences(starts)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if scratch is None:
+        scratch = torch.empty(prompt_attention_scratch_bytes(tokens, n), dtype=torch.uint8,
+                              device=q.device)
+    _here(q, k, v, starts, out, scratch, status)
+    hq, hk = q.size(1), k.size(1)
+    args = _pack_prompt(
+        tokens, n, d, _window(window), _scale(scale), *_token_heads(q, tokens, hq, d, "q"),
+        *_token_heads(k, tokens, hk, d, "k"), *_token_heads(v, tokens, hk, d, "v"),
+        *_token_heads(out, tokens, hq, d, "out"), 0 if starts is None else starts.data_ptr())
+    _check("pb_prompt_attention", lib().pb_prompt_attention(
+        args, _ptr(scratch), scratch.numel(), _ptr(status), _stream(stream)))
     return out
 
 
