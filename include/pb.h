@@ -49,8 +49,10 @@ typedef enum pb_status {
   PB_ERR_CUDA = 4,            /* a CUDA runtime/driver call failed (message has why)   */
   PB_ERR_DEVICE_TIMEOUT = 5,  /* a kernel's bounded wait expired; results are invalid  */
   PB_ERR_BAD_HANDLE = 6,      /* NULL, destroyed or foreign handle, or wrong device    */
-  PB_ERR_RANGE = 7            /* PB_OPERANDS_FP16 only: a weight or an activation that */
+  PB_ERR_RANGE = 7,           /* PB_OPERANDS_FP16 only: a weight or an activation that */
                               /* feeds a GEMM exceeded the fp16 range (|v| > 65504)    */
+  PB_ERR_CACHE = 8            /* pb_cache, in its status word only: no free pages, or a */
+                              /* call's slots, lengths or pages do not fit the cache    */
 } pb_status;
 
 /*
@@ -655,6 +657,107 @@ typedef struct pb_prompt_args {
 pb_status pb_prompt_attention_scratch_bytes(int32_t tokens, int32_t sequences, size_t* bytes);
 pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t scratch_bytes,
                               int* status, void* stream);
+
+/* A paged cache of keys and values, a plain value in host memory whose buffers are the caller's
+ * (device). Token t of the sequence in slot s is row t % page_size of page table[s, t / page_size];
+ * the layers share the table. Before the first call lengths, refs and status are zero; the table
+ * and the pages hold anything. Entries of the table behind a sequence's last page, rows of a page
+ * behind its last token, and pages with refs 0 hold anything at any time.
+ *
+ * What a call is told on the device (slots, starts, paths) is checked there. pb_cache_extend, _keep,
+ * _fork and _truncate change nothing where something in the call is at fault, pb_cache_write and
+ * pb_cache_attention leave out the sequence at fault (and may leave out others), and each records
+ * PB_ERR_CACHE + 256 x the reason in *status: 1 not enough free pages, 2 a sequence beyond slot_pages,
+ * 3 a slot that is none or listed twice, 4 starts that fall or leave the call's tokens, or more
+ * tokens than the sequence has, 5 a page or a length that is none, 6 a path that does not rise within
+ * the new tokens, 7 kept tokens to be moved in a page that several sequences use. From then on calls
+ * on the cache do nothing, until the caller writes 0 to status. Calls on one cache must not overlap
+ * on the GPU, but for pb_cache_attention calls among themselves. */
+typedef struct pb_cache {
+  int32_t layers;
+  int32_t pages;     /* 2^20 at most */
+  int32_t page_size; /* tokens of a page */
+  int32_t kv_heads;
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t slots;      /* sequences, 2^18 at most */
+  int32_t slot_pages; /* pages of a sequence at most; slot_pages * page_size <= 2^30 */
+  void* k;            /* bf16 [layers, pages, kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v;
+  int32_t* table;   /* [slots, slot_pages] */
+  int32_t* lengths; /* [slots] */
+  int32_t* refs;    /* [pages]: sequences that use the page, 0: free */
+  int32_t* status;
+} pb_cache;
+
+/* The calls below take n sequences, slots[n] (device int32, all different; n <= cache->slots), and
+ * for their new tokens starts[n + 1] (device int32): sequence i has the rows starts[i] <= t <
+ * starts[i + 1] of the call's tensors. `scratch` (device, 256-byte aligned, >= the bytes given here)
+ * needs no preparation and must not be used by another call that may run concurrently. */
+pb_status pb_cache_scratch_bytes(const pb_cache* cache, size_t* bytes);
+
+/* Room for starts[i + 1] - starts[i] more tokens of every sequence, whose lengths grow by them: the
+ * free pages of lowest number, in the sequences' order. A last page that is partly filled and that
+ * other sequences use too is replaced by a copy of its rows first, in all layers (each of the
+ * sequences in the call that share it gets its own); its page counts among the new ones, before
+ * the others of its sequence. */
+pb_status pb_cache_extend(const pb_cache* cache, int32_t n, const int32_t* slots,
+                          const int32_t* starts, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Writes k and v of the last starts[i + 1] - starts[i] tokens of every sequence (those that
+ * pb_cache_extend made room for), into `layers` layers from `layer` on. k, v: bf16 views [layers,
+ * tokens, kv_heads, head_dim] (batch_stride is the layers' stride). Rows in no sequence are not
+ * read. */
+pb_status pb_cache_write(const pb_cache* cache, int32_t layer, int32_t layers, int32_t n,
+                         const int32_t* slots, const int32_t* starts, int32_t tokens,
+                         const pb_heads* k, const pb_heads* v, void* stream);
+
+/* Of the last starts[i + 1] - starts[i] tokens of every sequence only kept[i] stay: those with the
+ * numbers path[starts[i]] < path[starts[i] + 1] < ... < path[starts[i] + kept[i] - 1] (counted from
+ * 0), moved together in all layers. The others' pages are released. path: device int32 [tokens],
+ * kept: device int32 [n]. */
+pb_status pb_cache_keep(const pb_cache* cache, int32_t n, const int32_t* slots,
+                        const int32_t* starts, int32_t tokens, const int32_t* path,
+                        const int32_t* kept, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The sequence in slot to[i] becomes that of slot from[i], as it was before the call, sharing its
+ * pages; what to[i] held is released. to: all different; from: any, to's slots among them. */
+pb_status pb_cache_fork(const pb_cache* cache, int32_t n, const int32_t* from, const int32_t* to,
+                        void* scratch, size_t scratch_bytes, void* stream);
+
+/* Every sequence is cut to lengths[i] tokens (device int32 [n]; longer or equal: as it is; below
+ * zero counts as zero), and its pages behind them are released: 0 frees the slot. */
+pb_status pb_cache_truncate(const pb_cache* cache, int32_t n, const int32_t* slots,
+                            const int32_t* lengths, void* scratch, size_t scratch_bytes,
+                            void* stream);
+
+/* Attention of the last starts[i + 1] - starts[i] tokens of every sequence over the cache, one layer:
+ * q and out [tokens, q heads, head_dim], bf16 views (batch_stride is not read); the cache holds the
+ * new tokens' k and v already. parents NULL: the tokens follow one another, and each sees all
+ * before it and itself. Else parents is a device int32 [tokens] and the new tokens are a tree, at
+ * most 64 of a sequence (more: reason 4): parents[t] is the number of the token that t follows,
+ * counted from 0 within its sequence's new tokens and below its own, or -1 for the last token before
+ * them (as any other value is); a token sees the tokens before the new ones, its ancestors and itself.
+ * Places count along the path: of those a token sees the last `window` (0: all). Query heads and key
+ * heads, scale, and the roundings as in pb_prompt_attention. Rows of out in no sequence are left as
+ * they were; rows of the cache behind a sequence reach no result. Within a sequence a v that is
+ * not finite may make results of tokens NaN that do not see it, by a tile of 64 keys. Any number of
+ * new tokens, without parents; from about 64 / (q heads / kv_heads) on a sequence's cache is read
+ * several times. */
+typedef struct pb_cache_attention_args {
+  int32_t layer;
+  int32_t sequences;
+  int32_t tokens;
+  int32_t window; /* 0: all */
+  float scale;    /* 0: 1 / sqrt(head_dim) */
+  pb_heads q;
+  pb_heads out;
+  const int32_t* slots;
+  const int32_t* starts;
+  const int32_t* parents;
+} pb_cache_attention_args;
+pb_status pb_cache_attention_scratch_bytes(const pb_cache* cache, size_t* bytes);
+pb_status pb_cache_attention(const pb_cache* cache, const pb_cache_attention_args* args,
+                             void* scratch, size_t scratch_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Optimiser: what follows pb_backward in a training step.

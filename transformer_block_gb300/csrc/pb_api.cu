@@ -1025,6 +1025,7 @@ const char* pb_status_string(pb_status s) {
     case PB_ERR_DEVICE_TIMEOUT: return "PB_ERR_DEVICE_TIMEOUT";
     case PB_ERR_BAD_HANDLE: return "PB_ERR_BAD_HANDLE";
     case PB_ERR_RANGE: return "PB_ERR_RANGE";
+    case PB_ERR_CACHE: return "PB_ERR_CACHE";
   }
   return "unknown pb_status";
 }

@@ -20,9 +20,10 @@ from .configs import Workload
 PB_OK = 0
 PB_ERR_DEVICE_TIMEOUT = 5
 PB_ERR_RANGE = 7
+PB_ERR_CACHE = 8
 STATUS_NAMES = {0: "PB_OK", 1: "PB_ERR_INVALID_ARG", 2: "PB_ERR_UNSUPPORTED",
                 3: "PB_ERR_WORKSPACE", 4: "PB_ERR_CUDA", 5: "PB_ERR_DEVICE_TIMEOUT",
-                6: "PB_ERR_BAD_HANDLE", 7: "PB_ERR_RANGE"}
+                6: "PB_ERR_BAD_HANDLE", 7: "PB_ERR_RANGE", 8: "PB_ERR_CACHE"}
 PB_OPERANDS_BF16, PB_OPERANDS_FP16, PB_OPERANDS_FP8 = 0, 1, 2
 PB_DTYPE_BF16, PB_DTYPE_FP16, PB_DTYPE_FP32 = 0, 1, 2
 PB_WEIGHT_IN_OUT, PB_WEIGHT_OUT_IN = 0, 1
@@ -133,6 +134,18 @@ class pb_prompt_args(ctypes.Structure):
         ("starts", ctypes.c_void_p)]
 
 
+class pb_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "pages", "page_size", "kv_heads",
+                                              "head_dim", "slots", "slot_pages")] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "table", "lengths", "refs", "status")]
+
+
+class pb_cache_attention_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layer", "sequences", "tokens", "window")] + [
+        ("scale", ctypes.c_float), ("q", pb_heads), ("out", pb_heads)] + [
+        (n, ctypes.c_void_p) for n in ("slots", "starts", "parents")]
+
+
 # name -> (restype, argtypes); every function of include/pb.h
 _P, _S, _I32, _I64, _U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, \
     ctypes.c_uint64
@@ -187,6 +200,14 @@ SIGNATURES = {
                                               _I64, _P]),
     "pb_prompt_attention_scratch_bytes": (ctypes.c_int, [_I32, _I32, ctypes.POINTER(_S)]),
     "pb_prompt_attention": (ctypes.c_int, [_P, _P, _S, _P, _P]),
+    "pb_cache_scratch_bytes": (ctypes.c_int, [_P, ctypes.POINTER(_S)]),
+    "pb_cache_extend": (ctypes.c_int, [_P, _I32, _P, _P, _P, _S, _P]),
+    "pb_cache_write": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P]),
+    "pb_cache_keep": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _P, _P, _S, _P]),
+    "pb_cache_fork": (ctypes.c_int, [_P, _I32, _P, _P, _P, _S, _P]),
+    "pb_cache_truncate": (ctypes.c_int, [_P, _I32, _P, _P, _P, _S, _P]),
+    "pb_cache_attention_scratch_bytes": (ctypes.c_int, [_P, ctypes.POINTER(_S)]),
+    "pb_cache_attention": (ctypes.c_int, [_P, _P, _P, _S, _P]),
     "pb_adamw": (ctypes.c_int, [_P, _I32, _P, _P]),
     "pb_grad_norm_scratch_bytes": (ctypes.c_int, [_I32, ctypes.POINTER(_S)]),
     "pb_grad_norm": (ctypes.c_int, [_I32, _P, _I32, ctypes.c_float, _P, _P, _S, _P]),
@@ -974,6 +995,154 @@ def prompt_attention(q, k, v, starts=None, window=None, scale=None, out=None, sc
     _check("pb_prompt_attention", lib().pb_prompt_attention(
         args, _ptr(scratch), scratch.numel(), _ptr(status), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------- paged cache
+
+# pb_cache_attention_args as bytes
+_CACHE_ATTENTION_FORMAT = "@4if" + "Piqqq" * 2 + "3P"
+_pack_cache_attention = struct.Struct(_CACHE_ATTENTION_FORMAT).pack
+assert struct.calcsize(_CACHE_ATTENTION_FORMAT) == ctypes.sizeof(pb_cache_attention_args)
+
+
+def _ints(t, n: int, what: str):
+    """A contiguous int32 [n]; returns its address."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 [{n}]")
+    return t.data_ptr()
+
+
+class Cache:
+    """A paged cache of keys and values (``pb_cache``) in the tensors given: ``k`` and ``v`` bf16
+    [layers, pages, kv_heads, page_size, head_dim], ``table`` int32 [slots, slot_pages], ``lengths``
+    int32 [slots], ``refs`` int32 [pages], ``status`` int32 [1] (a new one unless given).
+    ``Cache.empty`` makes them. ``slots`` in a call is an int32 tensor of different sequences, and
+    ``starts`` an int32 [len(slots) + 1]: sequence i has the rows starts[i] to starts[i + 1] of the
+    call's tensors. What is wrong in them shows in ``status`` when the call runs (see
+    ``pb_cache``): ``fault()`` reads it. Calls on one cache run one after another."""
+
+    def __init__(self, k, v, table, lengths, refs, status=None):
+        _is(k.dim() == 5 and v.shape == k.shape, "k and v must be [layers, pages, kv_heads, "
+            "page_size, head_dim]")
+        _is(table.dim() == 2, "table must be [slots, slot_pages]")
+        layers, pages, heads, page, d = k.shape
+        slots, slot_pages = table.shape
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        for t in (v, table, lengths, refs, status):
+            _is(t.device == k.device, f"a tensor is on {t.device}, k is on {k.device}")
+        self.k, self.v, self.table, self.lengths, self.refs, self.status = \
+            k, v, table, lengths, refs, status
+        self.kv_heads, self.head_dim, self.slots = heads, d, slots
+        n = k.numel()
+        self.plan = pb_cache(
+            layers, pages, page, heads, d, slots, slot_pages, _flat(k, n, torch.bfloat16, "k"),
+            _flat(v, n, torch.bfloat16, "v"), _flat(table, table.numel(), torch.int32, "table"),
+            _ints(lengths, slots, "lengths"), _ints(refs, pages, "refs"),
+            _ints(status, 1, "status"))
+        self._plan = ctypes.addressof(self.plan)
+        self.scratch_bytes = self._bytes("pb_cache_scratch_bytes")
+        self.attention_scratch_bytes = self._bytes("pb_cache_attention_scratch_bytes")
+        # of the calls that change the cache, which run one after another
+        self.scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=k.device)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, slots: int,
+              slot_pages: int, device="cuda") -> "Cache":
+        """A cache without sequences."""
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+
+        k = torch.empty(layers, pages, kv_heads, page_size, head_dim, dtype=torch.bfloat16,
+                        device=device)
+        return cls(k, torch.empty_like(k), ints(slots, slot_pages), ints(slots), ints(pages))
+
+    def _bytes(self, name: str) -> int:
+        n = ctypes.c_size_t()
+        _check(name, getattr(lib(), name)(self._plan, ctypes.byref(n)))
+        return n.value
+
+    def _call(self, name: str, *args, stream=None):
+        _check(name, getattr(lib(), name)(self._plan, *args, _stream(stream)))
+
+    def fault(self) -> int:
+        """0, or what a call recorded: ``PB_ERR_CACHE`` + 256 x the reason. Waits for the GPU."""
+        return int(self.status.item())
+
+    def extend(self, slots, starts, stream=None):
+        """``pb_cache_extend``: room for starts[i + 1] - starts[i] more tokens of every sequence."""
+        _here(self.k, slots, starts)
+        n = slots.numel()
+        self._call("pb_cache_extend", n, _ints(slots, n, "slots"), _ints(starts, n + 1, "starts"),
+                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+
+    def write(self, k, v, slots, starts, layer: int = 0, stream=None):
+        """``pb_cache_write``: ``k`` and ``v`` of the sequences' last tokens, [tokens, kv_heads,
+        head_dim] of one layer, or [layers, tokens, kv_heads, head_dim] of those from ``layer``
+        on."""
+        _here(self.k, k, v, slots, starts)
+        n = slots.numel()
+        if k.dim() == 3:
+            k = k.unsqueeze(0)
+        if v.dim() == 3:
+            v = v.unsqueeze(0)
+        _is(k.dim() == 4, "k must be [tokens, kv_heads, head_dim] or [layers, ...]")
+        layers, tokens = k.size(0), k.size(1)
+        self._call("pb_cache_write", layer, layers, n, _ints(slots, n, "slots"),
+                   _ints(starts, n + 1, "starts"), tokens,
+                   _heads(k, self.head_dim, layers, tokens, "k"),
+                   _heads(v, self.head_dim, layers, tokens, "v"), stream=stream)
+
+    def keep(self, slots, starts, path, kept, stream=None):
+        """``pb_cache_keep``: of the sequences' last tokens only the numbers path[starts[i]] ... <
+        path[starts[i] + kept[i]] stay."""
+        _here(self.k, slots, starts, path, kept)
+        n, tokens = slots.numel(), path.numel()
+        self._call("pb_cache_keep", n, _ints(slots, n, "slots"), _ints(starts, n + 1, "starts"),
+                   tokens, _ints(path, tokens, "path"), _ints(kept, n, "kept"), _ptr(self.scratch),
+                   self.scratch_bytes, stream=stream)
+
+    def fork(self, src, dst, stream=None):
+        """``pb_cache_fork``: slot dst[i] becomes the sequence of slot src[i]."""
+        _here(self.k, src, dst)
+        n = dst.numel()
+        self._call("pb_cache_fork", n, _ints(src, n, "src"), _ints(dst, n, "dst"),
+                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+
+    def truncate(self, slots, lengths, stream=None):
+        """``pb_cache_truncate``: sequences cut to ``lengths`` tokens (0 frees their slots)."""
+        _here(self.k, slots, lengths)
+        n = slots.numel()
+        self._call("pb_cache_truncate", n, _ints(slots, n, "slots"), _ints(lengths, n, "lengths"),
+                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+
+    def attention(self, q, slots, starts, parents=None, layer: int = 0, window=None, scale=None,
+                  out=None, scratch=None, stream=None):
+        """``pb_cache_attention``: attention of the sequences' last tokens, ``q`` [tokens, heads,
+        head_dim] (a bf16 view), over the cache. ``parents`` (int32 [tokens]): the new tokens of a
+        sequence are a tree, parents[t] the number of the one that t follows, -1 for the token before
+        them (None: each follows the one before). ``window`` and ``scale`` as in
+        ``prompt_attention``. ``scratch`` (a uint8 CUDA tensor of ``attention_scratch_bytes``) is
+        allocated unless given. Rows of ``out`` in no sequence stay as they are."""
+        if stream is not None:
+            return _run_on(stream, self.attention, q, slots, starts, parents, layer, window, scale,
+                           out, scratch)
+        tokens, heads, d = q.shape
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if scratch is None:
+            scratch = torch.empty(self.attention_scratch_bytes, dtype=torch.uint8, device=q.device)
+        _here(self.k, q, slots, starts, parents, out, scratch)
+        n = slots.numel()
+        args = _pack_cache_attention(
+            layer, n, tokens, _window(window), _scale(scale),
+            *_token_heads(q, tokens, heads, self.head_dim, "q"),
+            *_token_heads(out, tokens, heads, self.head_dim, "out"), _ints(slots, n, "slots"),
+            _ints(starts, n + 1, "starts"),
+            0 if parents is None else _ints(parents, tokens, "parents"))
+        _check("pb_cache_attention", lib().pb_cache_attention(
+            self._plan, args, _ptr(scratch), scratch.numel(), _stream(None)))
+        return out
 
 
 # ------------------------------------------------------------------- AdamW
