@@ -126,18 +126,19 @@ __global__ void __launch_bounds__(1024) list_kernel(const Params p, int* count, 
   }
 }
 
-// One softmax row of a tile: p_k = 2^(s_k c - m) rounded to bf16 into tensor memory at t_s
-// (column m holds keys 2m and 2m + 1); returns the fp32 sum of the unrounded p_k.
-__device__ __forceinline__ float probs_to_tmem(const float (&s)[BKV], float c, float m,
-                                               uint32_t t_s) {
+// Half a softmax row of a tile (64 keys from column `first` of s on): p_k = 2^(s_k c - m) rounded to
+// bf16 into tensor memory at t_p (column m holds keys 2m and 2m + 1); the fp32 sum of the unrounded
+// p_k is added to acc, in four parts of pairs.
+__device__ __forceinline__ void probs_to_tmem(const float (&s)[BKV], int first, float c, float m,
+                                              uint32_t t_p, uint64_t (&acc)[4]) {
   const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
-  uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int ch = 0; ch < BKV / 32; ++ch) {
+  for (int ch = 0; ch < 2; ++ch) {
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const uint64_t x2 = f2_fma(f2(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]), c2, nm2);
+      const int k = first + ch * 32 + 2 * e;
+      const uint64_t x2 = f2_fma(f2(s[k], s[k + 1]), c2, nm2);
       float x0, x1;
       f2_split(x2, x0, x1);
       const uint64_t a2 = f2(ex2_approx(x0), ex2_approx(x1));
@@ -146,12 +147,66 @@ __device__ __forceinline__ float probs_to_tmem(const float (&s)[BKV], float c, f
       f2_split(a2, a0, a1);
       pk[e] = pack_bf16x2(a0, a1);
     }
-    tmem_st16(t_s + uint32_t(ch * 16), pk);
+    tmem_st16(t_p + uint32_t(ch * 16), pk);
   }
-  const uint64_t t = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
-  float lo, hi;
-  f2_split(t, lo, hi);
-  return lo + hi;
+}
+
+// Transposes 16-byte pieces (4 words) inside each group of 4 lanes: piece c of lane l becomes
+// piece l of lane c, so that 4 lanes store 64 bytes of one row.
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[16]) {
+  const uint32_t lane = lane_id();
+  const bool hi = (lane & 2) != 0, odd = (lane & 1) != 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, hi ? w[4 * s + e] : w[4 * (2 + s) + e], 2);
+      if (hi)
+        w[4 * s + e] = y;
+      else
+        w[4 * (2 + s) + e] = y;
+    }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t y =
+          __shfl_xor_sync(0xffffffffu, odd ? w[4 * (2 * c) + e] : w[4 * (2 * c + 1) + e], 1);
+      if (odd)
+        w[4 * (2 * c) + e] = y;
+      else
+        w[4 * (2 * c + 1) + e] = y;
+    }
+}
+
+// Products issued by the elected lane of a converged warp, descriptors in 32-bit halves (the upper one
+// is the same for all operands of a kind): the issuing of a product then costs less than its 64 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 template <int DH>
@@ -162,7 +217,7 @@ struct Layout {
   static constexpr int K_OFF = 2 * Q_TILE;
   static constexpr int V_OFF = K_OFF + K_STAGES * KV_BYTES;
   static constexpr int BAR_OFF = V_OFF + V_STAGES * KV_BYTES;
-  static constexpr int NUM_BARS = 19;
+  static constexpr int NUM_BARS = 23;
   static constexpr size_t NEED = size_t(BAR_OFF) + NUM_BARS * 8 + 16 + 1024;
   // so much that one block fits an SM: it takes all 512 columns of tensor memory
   static constexpr size_t SMEM = NEED > 200 * 1024 ? NEED : 200 * 1024;
@@ -224,9 +279,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t v_full0 = smem_u32(bars + 8);    // [2]
   const uint32_t v_empty0 = smem_u32(bars + 10);  // [2]
   const uint32_t s_full0 = smem_u32(bars + 12);   // [2] per row tile
-  const uint32_t p_full0 = smem_u32(bars + 14);   // [2] per row tile (4 warps each)
-  const uint32_t o_final0 = smem_u32(bars + 16);  // [2] per row tile: the item's last PV is done
-  const uint32_t drain_bar = smem_u32(bars + 18);
+  const uint32_t s_free = smem_u32(bars + 14);    // S has been read (4 warps, the row tiles in turn)
+  const uint32_t p_half0 = smem_u32(bars + 15);   // [2] per row tile: P of the first 64 keys
+  const uint32_t p_full0 = smem_u32(bars + 17);   // [2] and of the others
+  const uint32_t o_done0 = smem_u32(bars + 19);   // [2] per row tile: the step's PV is done
+  const uint32_t drain0 = smem_u32(bars + 21);    // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int G = int(gridDim.x), cta = int(blockIdx.x);
@@ -243,10 +300,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(v_full0 + 8 * s, 1);
       mbar_init(v_empty0 + 8 * s, 1);
       mbar_init(s_full0 + 8 * s, 1);
-      mbar_init(p_full0 + 8 * s, s == 0 ? 5 : 4);  // row tile 0: and warp 2
-      mbar_init(o_final0 + 8 * s, 1);
+      mbar_init(p_half0 + 8 * s, s == 0 ? 5 : 4);  // row tile 0: and warp 2
+      mbar_init(p_full0 + 8 * s, 4);
+      mbar_init(o_done0 + 8 * s, 1);
     }
-    mbar_init(drain_bar, 1);
+    mbar_init(s_free, 4);
+    mbar_init(drain0, 1);
+    mbar_init(drain0 + 8, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -322,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             v_used |= 1u << st;
             return true;
           };
-          // K runs one tile ahead of V: the next tile's S is issued before this one's P V
+          // K runs one tile ahead of V: S runs ahead of P V
           ok = load_k(0);
           for (int idx = 0; ok && idx < it.U; ++idx) {
             if (idx + 1 < it.U) ok = load_k(idx + 1);
@@ -338,101 +398,126 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (v_used & (1u << s)) mbar_wait_drain(v_full0 + 8 * s, (v_par >> s) & 1u, drain_ns);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        // -------------------------------------------------------------- products
-        const uint32_t id_s = idesc_bf16_f32(BQ, BKV);
-        const uint32_t id_o = idesc_f32acc(BQ, DH, false, false, true);
-        const uint64_t dQ = sdesc_kmajor_sw128(sQ), dK = sdesc_kmajor_sw128(sK),
-                       dV = sdesc_mnmajor_sw128(sV, BOX);
-        uint32_t kc = 0, vc = 0, tb = 0;  // K, V tiles and tiles of the pair consumed so far
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-          const int r = item_index(n, cta, G);
-          if (r >= num_items) break;
-          const Item it = make_item(p, entries, r);
-          // S_h = Q_h K^T for the pair's tile idx (nothing where row tile h does not need it);
-          // the item's last S products read Q for the last time
-          auto issue_s = [&](int h, int idx) {
-            const uint32_t st = (kc + uint32_t(idx)) % 3;
-            if (item_needs(it, h, it.kb0 + idx)) {
-              const uint64_t da = dQ + uint64_t((h * L::Q_TILE) >> 4);
-              const uint64_t db = dK + uint64_t((st * L::KV_BYTES) >> 4);
+      // ---------------------------------------------------------------- S = Q K^T
+      // The whole warp waits and steps; one lane issues.
+      const uint32_t id_s = idesc_bf16_f32(BQ, BKV);
+      const uint64_t dQ = sdesc_kmajor_sw128(sQ), dK = sdesc_kmajor_sw128(sK);
+      const uint32_t hi = uint32_t(dQ >> 32);
+      uint32_t kc = 0;  // K tiles of the items before
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int r = item_index(n, cta, G);
+        if (r >= num_items) break;
+        const Item it = make_item(p, entries, r);
+        if (!mbar_wait_warp(q_full, uint32_t(n) & 1, wc, 12)) break;
+        for (int idx = 0; ok && idx < it.U; ++idx) {
+          const uint32_t g = kc + uint32_t(idx), st = g % 3;
+          if (!mbar_wait_warp(k_full0 + 8 * st, (g / 3) & 1, wc, 14)) {
+            ok = false;
+            break;
+          }
+          const uint32_t k = uint32_t(dK) + st * uint32_t(L::KV_BYTES >> 4);
 #pragma unroll
-              for (int kk = 0; kk < DH / 16; ++kk) {
-                const uint64_t off = uint64_t(((kk >> 2) * BOX) >> 4) + 2 * (kk & 3);
-                mma_f16kind_ss(tmem_base + uint32_t(h * BKV), da + off, db + off, id_s,
-                               kk > 0 ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            // the other tile's softmax has read the S before: phases 2 step + h
+            if (!mbar_wait_warp(s_free, uint32_t(h ^ 1), wc, 22)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              if (item_needs(it, h, it.kb0 + idx)) {  // nothing where the tile does not need it
+                const uint32_t q = uint32_t(dQ) + uint32_t((h * L::Q_TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk) {
+                  const uint32_t off = uint32_t(((kk >> 2) * BOX) >> 4) + 2 * (kk & 3);
+                  mma_ss(tmem_base, q + off, k + off, hi, id_s, kk > 0 ? 1u : 0u);
+                }
+              }
+              mma_commit(s_full0 + 8 * h);
+              if (h == 1) {
+                mma_commit(k_empty0 + 8 * st);  // both S products have K
+                if (idx + 1 == it.U) mma_commit(q_empty);
               }
             }
-            mma_commit(s_full0 + 8 * h);
-            if (h == 1) {
-              mma_commit(k_empty0 + 8 * st);  // both S products have K
-              if (idx + 1 == it.U) mma_commit(q_empty);
-            }
-          };
-          if (!mbar_wait(q_full, uint32_t(n) & 1, wc, 12) ||
-              !mbar_wait(k_full0 + 8 * (kc % 3), (kc / 3) & 1, wc, 14))
-            break;
-          tc_fence_after();
-          issue_s(0, 0);
-          issue_s(1, 0);
-          uint32_t pv_started = 0;  // bit h: O_h holds this item's partial sum
-          for (int idx = 0; ok && idx < it.U; ++idx) {
-            const int j = it.kb0 + idx;
-            const uint32_t gv = vc + uint32_t(idx);
-            const uint64_t dv = dV + uint64_t(((gv & 1) * L::KV_BYTES) >> 4);
+            __syncwarp();
+          }
+        }
+        kc += uint32_t(it.U);
+      }
+      if (elect_one()) mma_commit(drain0);
+      mbar_wait_drain(drain0, 0, drain_ns);
+      __syncwarp();
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- O += P V
+      constexpr uint32_t T_P = 128, T_O = 256;
+      const uint32_t id_o = idesc_f32acc(BQ, DH, false, false, true);
+      const uint64_t dV = sdesc_mnmajor_sw128(sV, BOX);
+      const uint32_t hi = uint32_t(dV >> 32);
+      uint32_t vc = 0;  // V tiles (steps) of the items before
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int r = item_index(n, cta, G);
+        if (r >= num_items) break;
+        const Item it = make_item(p, entries, r);
+        for (int idx = 0; ok && idx < it.U; ++idx) {
+          const uint32_t g = vc + uint32_t(idx);
+          const uint32_t v = uint32_t(dV) + (g & 1) * uint32_t(L::KV_BYTES >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // P_0's phase also says that V tile gv and the next K tile have landed (warp 2)
-              if (!mbar_wait(p_full0 + 8 * h, (tb + uint32_t(idx)) & 1, wc, 13)) {
+          for (int h = 0; h < 2; ++h) {
+            const bool need = item_needs(it, h, it.kb0 + idx);
+            const uint32_t on = it.kb0 + idx > (h ? it.kb1 : it.kb0) ? 1u : 0u;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              // P_0's first phase also says that V tile g has landed (warp 2)
+              if (!mbar_wait_warp((half ? p_full0 : p_half0) + 8 * h, g & 1, wc, 13)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              if (item_needs(it, h, j)) {
-                const uint32_t t_p = tmem_base + uint32_t(h * BKV);
-                const uint32_t t_o = tmem_base + 256u + uint32_t(h * 128);
+              if (elect_one()) {
+                if (need) {
 #pragma unroll
-                for (int kk = 0; kk < BKV / 16; ++kk)  // 16 keys: two 8-row atoms of 1024 bytes
-                  mma_f16kind_ts(t_o, t_p + uint32_t(kk * 8), dv + uint64_t((kk * 2048) >> 4), id_o,
-                                 ((pv_started >> h) & 1u) | (kk > 0 ? 1u : 0u));
-                pv_started |= 1u << h;
+                  for (int kk = 4 * half; kk < 4 * half + 4; ++kk)  // 16 keys: two 8-row atoms
+                    mma_ts(tmem_base + T_O + uint32_t(h * 128),
+                           tmem_base + T_P + uint32_t(h * 64 + kk * 8),
+                           v + uint32_t((kk * 2048) >> 4), hi, id_o, kk > 0 ? 1u : on);
+                }
+                if (half) {
+                  mma_commit(o_done0 + 8 * h);
+                  if (h == 1) mma_commit(v_empty0 + 8 * (g & 1));  // both PV products have V
+                }
               }
-              if (h == 1) mma_commit(v_empty0 + 8 * (gv & 1));  // both PV products have V
-              if (idx + 1 == it.U) mma_commit(o_final0 + 8 * h);  // once an item
-              if (idx + 1 < it.U) issue_s(h, idx + 1);
+              __syncwarp();
             }
+            if (!ok) break;
           }
-          kc += uint32_t(it.U);
-          vc += uint32_t(it.U);
-          tb += uint32_t(it.U);
         }
-        mma_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0, drain_ns);
+        vc += uint32_t(it.U);
       }
+      if (elect_one()) mma_commit(drain0 + 8);
+      mbar_wait_drain(drain0 + 8, 0, drain_ns);
       __syncwarp();
-    } else if (warp == 2) {
-      // ---------------------------------------------------------------- landings
-      // Waits for the V tile of each step and the K tile of the next one, writes zeros over V's
-      // rows behind the sequence, and arrives on row tile 0's P barrier. A stage cannot be
-      // refilled before that phase completes: the products read it only afterwards.
-      uint32_t kc = 0, vc = 0, tb = 0;
+    } else {
+      // ---------------------------------------------------------------- V's landings
+      // Waits for the V tile of each step, writes zeros over its rows behind the sequence, and
+      // arrives on row tile 0's first P barrier. The stage cannot be refilled before that phase
+      // completes: the products read it only afterwards.
+      uint32_t vc = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const int r = item_index(n, cta, G);
         if (r >= num_items) break;
         const Item it = make_item(p, entries, r);
         for (int idx = 0; idx < it.U; ++idx) {
-          const uint32_t gv = vc + uint32_t(idx), gk = kc + uint32_t(idx + 1);
-          if (!mbar_wait_warp(v_full0 + 8 * (gv & 1), (gv >> 1) & 1, wc, 17) ||
-              (idx + 1 < it.U &&
-               !mbar_wait_warp(k_full0 + 8 * (gk % 3), (gk / 3) & 1, wc, 15))) {
+          const uint32_t g = vc + uint32_t(idx);
+          if (!mbar_wait_warp(v_full0 + 8 * (g & 1), (g >> 1) & 1, wc, 17)) {
             ok = false;
             break;
           }
           const int live = it.n - (it.kb0 + idx) * BKV;  // rows of the tile in the sequence
           if (live < BKV) {
-            uint8_t* v = smem + L::V_OFF + (gv & 1) * L::KV_BYTES;
+            uint8_t* v = smem + L::V_OFF + (g & 1) * L::KV_BYTES;
 #pragma unroll 1
             for (int hb = 0; hb < DH / 64; ++hb)
 #pragma unroll 4
@@ -441,15 +526,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full0);
-          if (!mbar_wait_warp(p_full0, (tb + uint32_t(idx)) & 1, wc, 19)) {
+          if (lane == 0) mbar_arrive(p_half0);
+          if (!mbar_wait_warp(p_half0, g & 1, wc, 19)) {
             ok = false;
             break;
           }
         }
-        kc += uint32_t(it.U);
         vc += uint32_t(it.U);
-        tb += uint32_t(it.U);
       }
       __syncwarp();
     }
@@ -459,11 +542,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int h = (warp >= 8) ? 1 : 0;  // row tile of this warpgroup
     const uint32_t quad = warp & 3;
     const int row = int(quad * 32 + lane);  // = lane of tensor memory
-    const int tok = row / p.group, head = row - tok * p.group;
+    const int tok = row / p.group;
+    // the warp's first and last token
+    const int warp_tok0 = int(quad * 32) / p.group, warp_tok1 = int(quad * 32 + 31) / p.group;
     const uint32_t lane_addr = (quad * 32u) << 16;
-    const uint32_t t_s = tmem_base + lane_addr + uint32_t(h * BKV);
+    const uint32_t t_s = tmem_base + lane_addr;
+    const uint32_t t_p = tmem_base + lane_addr + 128u + uint32_t(h * 64);
     const uint32_t t_o = tmem_base + lane_addr + 256u + uint32_t(h * 128);
-    const uint32_t s_full = s_full0 + 8 * h, p_full = p_full0 + 8 * h;
+    const uint32_t s_full = s_full0 + 8 * h, p_half = p_half0 + 8 * h, p_full = p_full0 + 8 * h;
     const float c = p.scale_log2;
     uint32_t tb = 0;  // tiles of earlier items
     bool ok = true;
@@ -474,6 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int qb = it.q0 + h * p.tile_tokens;
       const int i = qb + tok;  // place in the sequence
       const int kb_h = h ? it.kb1 : it.kb0, ke_h = h ? it.ke1 : it.ke0;
+      const int warp_first = qb + warp_tok0, warp_last = qb + warp_tok1;
       float m_used = -INFINITY, l = 0.f;
       bool has_o = false;
       for (int idx = 0; idx < it.U; ++idx) {
@@ -484,6 +571,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         if (j >= kb_h && j <= ke_h) {
+          const int k0 = j * BKV;
+          if (k0 + BKV - 1 > warp_first || warp_last - k0 >= p.window) {
+            // Scores that the token does not see become -inf where they lie, in a pass of its own:
+            // as a branch on the 128 values in registers it costs every tile 260 cycles.
+#pragma unroll 1
+            for (int ch = 0; ch < BKV / 32; ++ch) {
+              const int kf = k0 + ch * 32;
+              if (kf + 31 <= warp_first && warp_last - kf < p.window) continue;  // all see these
+              uint32_t w[32];
+              tmem_ld32(t_s + uint32_t(ch * 32), w);
+              tmem_ld_wait(w);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)  // 0 <= i - k < window in one comparison
+                if (uint32_t(i - (kf + e)) >= uint32_t(p.window)) w[e] = 0xff800000u;
+              tmem_st32(t_s + uint32_t(ch * 32), w);
+            }
+            tmem_st_wait();
+          }
           uint32_t u[BKV];
 #pragma unroll
           for (int ch = 0; ch < BKV / 32; ++ch)
@@ -492,17 +597,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 32));
           tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 64));
           tmem_ld_wait_regs(*reinterpret_cast<uint32_t(*)[32]>(u + 96));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);  // the other tile's scores may overwrite these
           float s[BKV];
 #pragma unroll
           for (int e = 0; e < BKV; ++e) s[e] = __uint_as_float(u[e]);
-          const int k0 = j * BKV;
-          const bool whole =
-              (k0 + BKV - 1 <= qb) && (qb + p.tile_tokens - 1 - k0 < p.window);
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < BKV; ++e)  // 0 <= i - k < window in one comparison
-              if (uint32_t(i - (k0 + e)) >= uint32_t(p.window)) s[e] = -INFINITY;
-          }
           float mx4[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -522,8 +622,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             m_used = mxs;
           }
           const float m_eff = (m_used == -INFINITY) ? 0.f : m_used;
-          l += probs_to_tmem(s, c, m_eff, t_s);
-          tmem_st_wait();
+          uint64_t acc[4] = {0, 0, 0, 0};
+          // the product of the step before has read P and added to O
+          if (!mbar_wait_warp(o_done0 + 8 * h, (tb + uint32_t(idx) + 1) & 1, wc, 18)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          probs_to_tmem(s, 0, c, m_eff, t_p, acc);
           if (has_o && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
             for (int ch = 0; ch < DH / 32; ++ch) {
@@ -534,39 +640,66 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
               tmem_st32(t_o + uint32_t(ch * 32), w);
             }
-            tmem_st_wait();
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_half);
+          probs_to_tmem(s, 64, c, m_eff, t_p + 32u, acc);
+          const uint64_t a2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+          float a_lo, a_hi;
+          f2_split(a2, a_lo, a_hi);
+          l += a_lo + a_hi;
           has_o = true;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full);
+        } else {
+          if (!mbar_wait_warp(o_done0 + 8 * h, (tb + uint32_t(idx) + 1) & 1, wc, 18)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive(s_free);
+            mbar_arrive(p_half);
+            mbar_arrive(p_full);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
       tb += uint32_t(it.U);
-      if (has_o && !mbar_wait_warp(o_final0 + 8 * h, uint32_t(n) & 1, wc, 18)) break;
+      if (!mbar_wait_warp(o_done0 + 8 * h, (tb + 1) & 1, wc, 18)) break;
       if (has_o) {
         tc_fence_after();
         const float inv_l = 1.f / l;
-        const bool live = tok < p.tile_tokens && i < it.n;
-        __nv_bfloat16* dst =
-            p.out + int64_t(it.first + i) * p.out_ss + int64_t(it.kv * p.group + head) * p.out_hs;
+        // Four lanes exchange 16-byte pieces and store 64 bytes of one of their rows at a time: a
+        // store of one row a lane would touch 32 lines.
+        __nv_bfloat16* dst[4];  // this lane's pieces of the four rows, or null
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = int(quad * 32 + (lane & ~3u)) + q, tt = rr / p.group;
+          dst[q] = tt < p.tile_tokens && qb + tt < it.n
+                       ? p.out + int64_t(it.first + qb + tt) * p.out_ss +
+                             int64_t(it.kv * p.group + rr - tt * p.group) * p.out_hs + (lane & 3) * 8
+                       : nullptr;
+        }
 #pragma unroll
         for (int ch = 0; ch < DH / 32; ++ch) {
           uint32_t u[32];
           tmem_ld32(t_o + uint32_t(ch * 32), u);
           tmem_ld_wait(u);
-          if (live) {
+          uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float f[8];
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[2 * e]) * inv_l,
+                               __uint_as_float(u[2 * e + 1]) * inv_l);
+          transpose_pieces(w);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[8 * q + e]) * inv_l;
-              reinterpret_cast<uint4*>(dst + ch * 32)[q] =
-                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-            }
-          }
+          for (int q = 0; q < 4; ++q)
+            if (dst[q] != nullptr)
+              reinterpret_cast<uint4*>(dst[q])[ch * 4] =
+                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         }
       }
     }  // items
