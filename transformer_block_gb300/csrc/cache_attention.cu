@@ -36,12 +36,24 @@
 namespace pb {
 namespace {
 
-constexpr int THREADS = 128, BK = 64;
-constexpr int kRing = 8;          // tiles whose rows' places are known
-constexpr int kMostTree = 64;     // a bit each
-constexpr int kBlocksPerSm = 2, kMaxSms = 192;
-constexpr int kMaxBlocks = kBlocksPerSm * kMaxSms;
-constexpr int kMostRows = 64;
+constexpr int kRing = 8;       // tiles whose rows' places are known
+constexpr int kMostTree = 64;  // a bit each
+constexpr int kMaxSms = 192;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+// A block of MB query rows: its warps, the keys of its tiles, blocks an SM.
+template <int MB>
+struct Shape {
+  static constexpr int MT = MB == 64 ? 2 : 1;  // groups of 16 rows of a warp
+  static constexpr int WARPS = MB == 64 ? 8 : 4;
+  static constexpr int BK = MB == 64 ? 128 : 64;
+  static constexpr int BLOCKS = MB == 64 ? 1 : 2;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int RW = MB / (16 * MT), KW = WARPS / RW;  // warps along rows, along keys
+  static constexpr int KPW = BK / KW;                         // keys of a tile a warp takes
+  // registers do not hold 32 rows' queries too: they are read again for every tile
+  static constexpr bool Q_SHARED = MB == 64;
+};
 
 // Of one block, two pieces at most do not hold their whole item: the one that it begins with (the
 // item began in a block before) and the one that it ends with.
@@ -65,7 +77,7 @@ struct Params {
   const int *slot, *starts, *parents, *table, *lengths;
   int* status;
   Piece* pieces;  // [blocks][2]
-  float* parts;   // [blocks][2][rows][dh + 2]
+  float* parts;   // [blocks][2][rows][dh + 4]: the result, the maximum, the sum
 };
 
 struct Seq {
@@ -107,6 +119,7 @@ __device__ __forceinline__ int end_of(const Params& p, const Seq& s, int b) {
 // Key tiles [from, to) that block of rows b needs: from the first of its first row.
 template <int MB>
 __device__ __forceinline__ int2 tiles_of(const Params& p, const Seq& s, int b) {
+  constexpr int BK = Shape<MB>::BK;
   const int from = s.base + (p.parents == nullptr ? b * MB / p.group : 0);
   return make_int2(max(0, from - p.window + 1) / BK, (end_of<MB>(p, s, b) + BK - 1) / BK);
 }
@@ -151,27 +164,32 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DH>
+template <int DH, int MB>
 struct Layout {
+  using T = Shape<MB>;
+  static constexpr int TILE = T::BK * DH * 2;  // of k or v
   static constexpr int STAGES = DH == 128 ? 3 : 6;
-  static constexpr int TILE = BK * DH * 2;  // of k or v
-  static constexpr int RING_OFF = STAGES * 2 * TILE;
-  static constexpr int ROW_OFF = RING_OFF + kRing * BK * 8;  // paths of the sequence's new tokens
+  static constexpr int Q_OFF = STAGES * 2 * TILE;
+  static constexpr int RING_OFF = Q_OFF + (T::Q_SHARED ? MB * DH * 2 : 0);
+  static constexpr int ROW_OFF = RING_OFF + kRing * T::BK * 8;  // paths of the new tokens
   static constexpr int SMEM = ROW_OFF + kMostTree * (8 + 4);
-  static_assert(STAGES + 1 < kRing && SMEM <= 111 * 1024, "shared memory layout");
-  static_assert(STAGES * 2 * TILE >= 4 * 16 * (DH + 4) * 4 + 4 * 16 * 8, "merge buffer");
+  static constexpr int PITCH = DH + 4;  // of the warps' parts
+  static_assert(STAGES + 1 < kRing && SMEM <= (T::BLOCKS == 1 ? 225 : 111) * 1024, "shared memory");
+  static_assert(STAGES * 2 * TILE >= T::KW * MB * (PITCH + 2) * 4, "merge buffer");
 };
 
 template <int DH, int MB>
-__global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const Params p) {
-  using L = Layout<DH>;
+__global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
+    attention_kernel(const Params p) {
+  using L = Layout<DH, MB>;
+  using T = Shape<MB>;
   constexpr int S = L::STAGES, CH = DH / 8;  // 16-byte chunks of a row
-  constexpr int RW = MB / 16, KW = 4 / RW;   // warps along rows, along keys
-  constexpr int KPW = BK / KW;               // keys of a tile a warp takes
+  constexpr int THREADS = T::THREADS, BK = T::BK, RW = T::RW, KW = T::KW, KPW = T::KPW, MT = T::MT;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int64_t sums[4];
+  __shared__ int64_t sums[T::WARPS];
   __shared__ int64_t found_at;
-  __shared__ int found_i;
+  __shared__ Seq found;
+  __shared__ int found_i, faulted;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rw = warp % RW, kw = warp / RW;
   int64_t* ring = reinterpret_cast<int64_t*>(smem + L::RING_OFF);
@@ -182,19 +200,26 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
   pdl_wait();
   pdl_trigger();
   if (tid < 2) mine[tid].state = kNone;
-  if (tid == 0) found_i = *reinterpret_cast<volatile int*>(p.status);
-  __syncthreads();
-  if (found_i != 0) return;
 
   // -------------------------------------------------------------- the block's share of the line
-  int64_t all = 0;
-  for (int i = tid; i < p.n; i += THREADS)
+  Seq sq{};  // of sequence tid: most calls have no more sequences than a block has threads
+  int64_t own = 0, all = 0;
+  if (tid < p.n) {
+    sq = sequence(p, tid, blockIdx.x == 0);
+    own = head_tiles<MB>(p, sq) * p.kv_heads;
+  }
+  if (tid == 0) faulted = *reinterpret_cast<volatile int*>(p.status);
+  for (int i = tid + THREADS; i < p.n; i += THREADS)
     all += head_tiles<MB>(p, sequence(p, i, blockIdx.x == 0)) * p.kv_heads;
+  all += own;
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xffffffffu, all, d);
   if (lane == 0) sums[warp] = all;
   __syncthreads();
-  all = sums[0] + sums[1] + sums[2] + sums[3];
+  if (faulted != 0) return;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < T::WARPS; ++w) all += sums[w];
   const int64_t blocks = all < int64_t(gridDim.x) ? all : int64_t(gridDim.x);
   if (int64_t(blockIdx.x) >= blocks) return;
   int64_t left;  // tiles to go
@@ -205,7 +230,14 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     int64_t before = 0;
     for (int i0 = 0; i0 < p.n; i0 += THREADS) {
       const int i = i0 + tid;
-      const int64_t x = i < p.n ? head_tiles<MB>(p, sequence(p, i, false)) * p.kv_heads : 0;
+      int64_t x = own;
+      if (i0 > 0) {
+        x = 0;
+        if (i < p.n) {
+          sq = sequence(p, i, false);
+          x = head_tiles<MB>(p, sq) * p.kv_heads;
+        }
+      }
       int64_t inc = x;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -216,18 +248,21 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
       if (lane == 31) sums[warp] = inc;
       __syncthreads();
       int64_t at = before + inc - x;
-      for (int w = 0; w < warp; ++w) at += sums[w];
+      for (int w = 0; w < T::WARPS; ++w) {
+        at += w < warp ? sums[w] : 0;
+        before += sums[w];
+      }
       if (lo >= at && lo < at + x) {
+        found = sq;
         found_i = i;
         found_at = lo - at;
       }
-      before += sums[0] + sums[1] + sums[2] + sums[3];
       if (before > lo) break;  // the same for all threads
     }
     __syncthreads();
   }
   int seq_i = found_i;
-  Seq sq = sequence(p, seq_i, false);
+  sq = found;
   int kv, blk = 0, t_off;
   {
     const int64_t per = head_tiles<MB>(p, sq);
@@ -293,12 +328,13 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     };
 
     __syncthreads();  // the piece before is done with shared memory
+#pragma unroll
     for (int i = tid / BK; i < S; i += THREADS / BK)
       ring[i * BK + tid % BK] = place(entry(i, tid % BK), i, tid % BK);
     int page_ahead = tid < BK ? entry(S, tid) : 0;
-    // the rows' queries pass through the last stage's place
+    // the rows' queries; where they go on to registers, they pass through the last stage's place
+    constexpr uint32_t qs = T::Q_SHARED ? L::Q_OFF : (S - 1) * 2 * L::TILE;
     {
-      const uint32_t qs = uint32_t((S - 1) * 2 * L::TILE);
       for (int x = tid; x < MB * CH; x += THREADS) {
         const int r = x / CH, ch = x % CH, rr = row0 + r;
         uint4 val = make_uint4(0, 0, 0, 0);
@@ -333,21 +369,24 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
         depth[tid] = d;
       }
     }
-    uint32_t qf[DH / 16][4];
-#pragma unroll
-    for (int ks = 0; ks < DH / 16; ++ks) {
+    auto load_q = [&](int mt, int ks, uint32_t (&a)[4]) {
       // A: matrices (rows 0-7, k lo), (rows 8-15, k lo), (rows 0-7, k hi), (rows 8-15, k hi)
-      const int r = rw * 16 + (lane & 15), ch = ks * 2 + (lane >> 4);
-      ldsm4(s0 + uint32_t((S - 1) * 2 * L::TILE + r * DH * 2 + ((ch ^ (r & 7)) * 16)), qf[ks]);
+      const int r = (rw * MT + mt) * 16 + (lane & 15), ch = ks * 2 + (lane >> 4);
+      ldsm4(s0 + qs + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), a);
+    };
+    uint32_t qf[T::Q_SHARED ? 1 : DH / 16][4];
+    if (!T::Q_SHARED) {
+#pragma unroll
+      for (int ks = 0; ks < DH / 16; ++ks) load_q(0, ks, qf[T::Q_SHARED ? 0 : ks]);
     }
     __syncthreads();
-    // this lane's two rows: keys before the new ones from lo on, of the new ones those up to hi (a
-    // line) or those in bits (a tree)
-    int lo[2], hi[2];
-    uint64_t bits[2];
+    // this lane's rows: keys before the new ones from lo on, of the new ones those up to hi (a line)
+    // or those in bits (a tree)
+    int lo[2 * MT], hi[2 * MT];
+    uint64_t bits[2 * MT];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = row0 + rw * 16 + (lane >> 2) + 8 * e;
+    for (int e = 0; e < 2 * MT; ++e) {
+      const int rr = row0 + rw * MT * 16 + (lane >> 2) + 8 * e;
       lo[e] = INT_MAX;
       hi[e] = -1;
       bits[e] = 0;
@@ -363,12 +402,18 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     const int all_hi = p.parents == nullptr ? sq.base + row0 / p.group : sq.base - 1;
     const int all_lo = max(0, sq.len - p.window);
 
-    float o[DH / 8][4];
+    float o[MT][DH / 8][4];
 #pragma unroll
-    for (int i = 0; i < DH / 8; ++i)
+    for (int i = 0; i < MT * (DH / 8); ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      for (int e = 0; e < 4; ++e) o[i / (DH / 8)][i % (DH / 8)][e] = 0.f;
+    // the maximum that the weights refer to (log2 units), and their sum
+    float mx[2 * MT], sum[2 * MT];
+#pragma unroll
+    for (int e = 0; e < 2 * MT; ++e) {
+      mx[e] = -INFINITY;
+      sum[e] = 0.f;
+    }
 
     for (int i = 0; i < m; ++i) {
       cp_wait<S - 2>();
@@ -379,79 +424,112 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
         page_ahead = entry(i + S + 1, tid);
       }
       const uint32_t sk = s0 + uint32_t(i % S) * uint32_t(2 * L::TILE) + uint32_t(kw * KPW * DH * 2);
-      float s[KPW / 8][4];
+      float s[MT][KPW / 8][4];
 #pragma unroll
-      for (int nt = 0; nt < KPW / 8; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int nt = 0; nt < KPW / 8; ++nt)
 #pragma unroll
-      for (int ks = 0; ks < DH / 16; ++ks)
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < DH / 16; ++ks) {
+        uint32_t a[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (T::Q_SHARED) {
+            load_q(mt, ks, a[mt]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[mt][e] = qf[T::Q_SHARED ? 0 : ks][e];
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < KPW / 16; ++nt) {
           uint32_t b[4];
           const int r = nt * 16 + k_row, ch = ks * 2 + k_chunk;
           ldsm4(sk + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), b);
-          mma16816(s[2 * nt], qf[ks], b[0], b[1]);
-          mma16816(s[2 * nt + 1], qf[ks], b[2], b[3]);
-        }
-      const int k0 = (ta + i) * BK + kw * KPW;
-      const bool full = k0 + KPW - 1 <= all_hi && k0 >= all_lo;
 #pragma unroll
-      for (int nt = 0; nt < KPW / 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[nt][e] *= p.scale_log2;
-          if (!full) {
-            const int key = k0 + nt * 8 + (lane & 3) * 2 + (e & 1), w = e >> 1;
-            const int u = key - sq.base;
-            const bool see = (key >= lo[w] && key <= hi[w]) ||
-                             (u >= 0 && u < kMostTree && ((bits[w] >> u) & 1u));
-            if (!see) s[nt][e] = -INFINITY;
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(s[mt][2 * nt], a[mt], b[0], b[1]);
+            mma16816(s[mt][2 * nt + 1], a[mt], b[2], b[3]);
           }
         }
-      float ref[2], alpha[2];
+      }
+      const int k0 = (ta + i) * BK + kw * KPW;
+      if (!(k0 + KPW - 1 <= all_hi && k0 >= all_lo)) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float t = mx[w];
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < KPW / 8; ++nt) t = max3f(t, s[nt][2 * w], s[nt][2 * w + 1]);
+          for (int nt = 0; nt < KPW / 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + nt * 8 + (lane & 3) * 2 + (e & 1), w = 2 * mt + (e >> 1);
+              const int u = key - sq.base;
+              const bool see = (key >= lo[w] && key <= hi[w]) ||
+                               (u >= 0 && u < kMostTree && ((bits[w] >> u) & 1u));
+              if (!see) s[mt][nt][e] = -INFINITY;
+            }
+      }
+      // As elsewhere: the reference moves only when a row's maximum grew by more than 2^8 (from
+      // -inf, any finite one does), so O is seldom rescaled.
+      float ref[2 * MT], alpha[2 * MT];
+      bool moved = false;
+#pragma unroll
+      for (int w = 0; w < 2 * MT; ++w) {
+        float t = s[w / 2][0][2 * (w & 1)];
+#pragma unroll
+        for (int nt = 0; nt < KPW / 8; ++nt)
+          t = max3f(t, s[w / 2][nt][2 * (w & 1)], s[w / 2][nt][2 * (w & 1) + 1]);
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        ref[w] = t == -INFINITY ? 0.f : t;
-        alpha[w] = ex2_approx(mx[w] - ref[w]);
-        mx[w] = t;
-        sum[w] *= alpha[w];
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * p.scale_log2;
+        const bool grow = t > mx[w] + kRescaleThreshold;
+        alpha[w] = grow ? ex2_approx(mx[w] - t) : 1.f;
+        if (grow) mx[w] = t;
+        moved |= grow;
+        ref[w] = mx[w] == -INFINITY ? 0.f : mx[w];
       }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int j = 0; j < DH / 8; ++j) {
-          o[j][0] *= alpha[0];
-          o[j][1] *= alpha[0];
-          o[j][2] *= alpha[1];
-          o[j][3] *= alpha[1];
+        for (int w = 0; w < 2 * MT; ++w) {
+          sum[w] *= alpha[w];
+#pragma unroll
+          for (int j = 0; j < DH / 8; ++j) {
+            o[w / 2][j][2 * (w & 1)] *= alpha[w];
+            o[w / 2][j][2 * (w & 1) + 1] *= alpha[w];
+          }
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < KPW / 8; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[nt][e] = ex2_approx(s[nt][e] - ref[e >> 1]);
-          sum[e >> 1] += s[nt][e];
-        }
+        for (int nt = 0; nt < KPW / 8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int w = 2 * mt + (e >> 1);
+            s[mt][nt][e] = ex2_approx(fmaf(s[mt][nt][e], p.scale_log2, -ref[w]));
+            sum[w] += s[mt][nt][e];
+          }
       const uint32_t sv = sk + L::TILE;
 #pragma unroll
       for (int kt = 0; kt < KPW / 16; ++kt) {
-        const uint32_t a[4] = {pack_bf16x2(s[2 * kt][0], s[2 * kt][1]),
-                               pack_bf16x2(s[2 * kt][2], s[2 * kt][3]),
-                               pack_bf16x2(s[2 * kt + 1][0], s[2 * kt + 1][1]),
-                               pack_bf16x2(s[2 * kt + 1][2], s[2 * kt + 1][3])};
+        uint32_t a[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          a[mt][0] = pack_bf16x2(s[mt][2 * kt][0], s[mt][2 * kt][1]);
+          a[mt][1] = pack_bf16x2(s[mt][2 * kt][2], s[mt][2 * kt][3]);
+          a[mt][2] = pack_bf16x2(s[mt][2 * kt + 1][0], s[mt][2 * kt + 1][1]);
+          a[mt][3] = pack_bf16x2(s[mt][2 * kt + 1][2], s[mt][2 * kt + 1][3]);
+        }
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
           uint32_t b[4];
           const int r = kt * 16 + v_row, ch = j * 2 + v_chunk;
           ldsm4_t(sv + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), b);
-          mma16816(o[2 * j], a, b[0], b[1]);
-          mma16816(o[2 * j + 1], a, b[2], b[3]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(o[mt][2 * j], a[mt], b[0], b[1]);
+            mma16816(o[mt][2 * j + 1], a[mt], b[2], b[3]);
+          }
         }
       }
     }
@@ -459,25 +537,25 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     __syncthreads();  // all tiles are read: shared memory is free for the merge
 
     // ------------------------------------------------------------ the warps' parts together
-    constexpr int PITCH = DH + 4;
+    // row r's part of key warp w at (w MB + r)
+    constexpr int PITCH = L::PITCH;
     float* parts = reinterpret_cast<float*>(smem);
-    float2* stats = reinterpret_cast<float2*>(parts + 4 * 16 * PITCH);
+    float2* stats = reinterpret_cast<float2*>(parts + KW * MB * PITCH);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < 2 * MT; ++w) {
+      const int at = kw * MB + rw * MT * 16 + (lane >> 2) + 8 * w;
       sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 1);
       sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
-      if ((lane & 3) == 0) stats[warp * 16 + (lane >> 2) + 8 * w] = make_float2(mx[w], sum[w]);
+      if ((lane & 3) == 0) stats[at] = make_float2(mx[w], sum[w]);
+#pragma unroll
+      for (int j = 0; j < DH / 8; ++j)
+        *reinterpret_cast<float2*>(parts + at * PITCH + j * 8 + (lane & 3) * 2) =
+            make_float2(o[w / 2][j][2 * (w & 1)], o[w / 2][j][2 * (w & 1) + 1]);
     }
-#pragma unroll
-    for (int j = 0; j < DH / 8; ++j)
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        *reinterpret_cast<float2*>(parts + (warp * 16 + (lane >> 2) + 8 * w) * PITCH + j * 8 +
-                                   (lane & 3) * 2) = make_float2(o[j][2 * w], o[j][2 * w + 1]);
     __syncthreads();
     const bool begins = t_off == 0, ends = t_off + m == whole;
     const int side = begins ? 1 : 0;
-    float* part = p.parts + (size_t(blockIdx.x) * 2 + side) * (MB * (DH + 2));
+    float* part = p.parts + (size_t(blockIdx.x) * 2 + side) * (MB * (DH + 4));
     if (tid == 0 && !(begins && ends)) {
       mine[side].token = sq.first;
       mine[side].row0 = row0;
@@ -492,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
       float2 st[KW];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        st[w] = stats[(w * RW + r / 16) * 16 + r % 16];
+        st[w] = stats[w * MB + r];
         best = fmaxf(best, st[w].x);
       }
       const float ref = best == -INFINITY ? 0.f : best;
@@ -500,8 +578,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
       for (int w = 0; w < KW; ++w) {
         const float f = ex2_approx(st[w].x - ref);
         total += f * st[w].y;
-        const float4* src = reinterpret_cast<const float4*>(
-            parts + ((w * RW + r / 16) * 16 + r % 16) * PITCH + ch * 8);
+        const float4* src = reinterpret_cast<const float4*>(parts + (w * MB + r) * PITCH + ch * 8);
         const float4 a = src[0], b = src[1];
         acc[0] += f * a.x;
         acc[1] += f * a.y;
@@ -520,10 +597,10 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
             make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                        pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
       } else {
-        float2* dst = reinterpret_cast<float2*>(part + r * (DH + 2) + ch * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_float2(acc[2 * e], acc[2 * e + 1]);
-        if (ch == 0) *reinterpret_cast<float2*>(part + r * (DH + 2) + DH) = make_float2(best, total);
+        float4* dst = reinterpret_cast<float4*>(part + r * (DH + 4) + ch * 8);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (ch == 0) *reinterpret_cast<float2*>(part + r * (DH + 4) + DH) = make_float2(best, total);
       }
     }
 
@@ -551,11 +628,11 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   const int r = blockIdx.y * 4 + int(threadIdx.x >> 5);
   const Piece head = p.pieces[2 * b + 1];
-  if (head.state == kNone || head.row0 + r >= head.rows) return;
   // the blocks behind, up to the one in which the item ends
   int pieces = 1;
   for (int i = b + 1;; i += 32) {
     const int state = i + lane < int(gridDim.x) ? p.pieces[2 * (i + lane)].state : kNone;
+    if (head.state == kNone || head.row0 + r >= head.rows) return;
     const uint32_t m = __ballot_sync(0xffffffffu, state != kGoesOn);
     if (m != 0) {
       // no end: a block left out its share, since a fault was recorded meanwhile
@@ -565,38 +642,45 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
     }
     pieces += 32;
   }
-  constexpr int PART = MB * (DH + 2);
-  const float* first = p.parts + (size_t(b) * 2 + 1) * PART + r * (DH + 2);
-  auto piece = [&](int i) {  // piece 0: the block's second; the others: the first of their block
-    return i == 0 ? first : first + size_t(2 * i - 1) * PART;
-  };
-  float best = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) best = fmaxf(best, piece(i)[DH]);
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
-  const float ref = best == -INFINITY ? 0.f : best;
-  constexpr int V = DH / 32;
-  float acc[V], total = 0.f;
+  constexpr int PART = MB * (DH + 4), V = DH / 32, AT_ONCE = 8;
+  const float* first = p.parts + (size_t(b) * 2 + 1) * PART + r * (DH + 4);
+  float best = -INFINITY, total = 0.f, acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    float f = 0.f, t = 0.f;
-    if (i0 + lane < pieces) {
-      const float2 st = *reinterpret_cast<const float2*>(piece(i0 + lane) + DH);
-      f = ex2_approx(st.x - ref);
-      t = f * st.y;
-    }
-    const int n = min(32, pieces - i0);
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      total += __shfl_sync(0xffffffffu, t, j);
-      const float* src = piece(i0 + j) + lane * V;
+  for (int i0 = 0; i0 < pieces; i0 += AT_ONCE) {
+    float2 st[AT_ONCE], x[AT_ONCE][V / 2];
 #pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + e);
-        acc[e] += fj * x.x;
-        acc[e + 1] += fj * x.y;
+    for (int j = 0; j < AT_ONCE; ++j) {
+      // piece 0: the block's second; the others: the first of their block
+      const int i = i0 + j;
+      const float* src = i == 0 ? first : first + size_t(2 * i - 1) * PART;
+      st[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) x[j][e] = make_float2(0.f, 0.f);
+      if (i < pieces) {
+        st[j] = *reinterpret_cast<const float2*>(src + DH);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e)
+          x[j][e] = *reinterpret_cast<const float2*>(src + lane * V + 2 * e);
+      }
+    }
+    float top = best;
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) top = fmaxf(top, st[j].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float old = ex2_approx(best - ref);
+    best = top;
+    total *= old;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= old;
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const float f = ex2_approx(st[j].x - ref);
+      total += f * st[j].y;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        acc[2 * e] += f * x[j][e].x;
+        acc[2 * e + 1] += f * x[j][e].y;
       }
     }
   }
@@ -608,14 +692,20 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
   for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-constexpr size_t kPieceBytes = size_t(kMaxBlocks) * 2 * sizeof(Piece);
+constexpr size_t kPieceBytes = size_t(2 * kMaxSms) * 2 * sizeof(Piece);
+template <int MB>
+constexpr size_t part_rows() {
+  return size_t(kMaxSms) * Shape<MB>::BLOCKS * 2 * MB;
+}
 size_t scratch_need(int head_dim) {
-  return kPieceBytes + size_t(kMaxBlocks) * 2 * kMostRows * (head_dim + 2) * 4;
+  static_assert(part_rows<64>() >= part_rows<32>() && part_rows<64>() >= part_rows<16>(), "rows");
+  return kPieceBytes + part_rows<64>() * (head_dim + 4) * 4;
 }
 
 template <int DH, int MB>
 cudaError_t launch(const Params& p, cudaStream_t stream) {
-  using L = Layout<DH>;
+  using L = Layout<DH, MB>;
+  using T = Shape<MB>;
   static PerDeviceInit setup;  // per device: the shared-memory opt-in, and the number of SMs
   int sms = 0;
   cudaError_t e = per_device_init(
@@ -629,8 +719,8 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
       },
       &sms);
   if (e != cudaSuccess) return e;
-  const unsigned grid = unsigned(kBlocksPerSm * (sms < kMaxSms ? sms : kMaxSms));
-  e = launch_dependent(attention_kernel<DH, MB>, dim3(grid), dim3(THREADS), L::SMEM, 1, stream, p);
+  const unsigned grid = unsigned(T::BLOCKS * (sms < kMaxSms ? sms : kMaxSms));
+  e = launch_dependent(attention_kernel<DH, MB>, dim3(grid), dim3(T::THREADS), L::SMEM, 1, stream, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(join_kernel<DH, MB>, dim3(grid, MB / 4), dim3(128), 0, 1, stream, p);
 }

@@ -1129,9 +1129,9 @@ class Cache:
                            out, scratch)
         tokens, heads, d = q.shape
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if scratch is None:
-            scratch = torch.empty(self.attention_scratch_bytes, dtype=torch.uint8, device=q.device)
+            out = q.new_empty(q.shape)
+        if scratch is None:  # in the values' type: new_empty is the quickest way to memory
+            scratch = self.k.new_empty(self.attention_scratch_bytes // 2)
         _here(self.k, q, slots, starts, parents, out, scratch)
         n = slots.numel()
         args = _pack_cache_attention(
@@ -1141,7 +1141,8 @@ class Cache:
             _ints(starts, n + 1, "starts"),
             0 if parents is None else _ints(parents, tokens, "parents"))
         _check("pb_cache_attention", lib().pb_cache_attention(
-            self._plan, args, _ptr(scratch), scratch.numel(), _stream(None)))
+            self._plan, args, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
+            _stream(None)))
         return out
 
 
