@@ -110,17 +110,23 @@ __device__ __forceinline__ Seq sequence(const Params& p, int i, bool report) {
   return s;
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where both fit.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 // The end of the keys that block of rows b sees.
 template <int MB>
 __device__ __forceinline__ int end_of(const Params& p, const Seq& s, int b) {
-  return p.parents != nullptr ? s.len
-                              : s.base + min(s.count, ((b + 1) * MB - 1) / p.group + 1);
+  return p.parents != nullptr || s.count * p.group <= (b + 1) * MB
+             ? s.len
+             : s.base + ((b + 1) * MB - 1) / p.group + 1;
 }
 // Key tiles [from, to) that block of rows b needs: from the first of its first row.
 template <int MB>
 __device__ __forceinline__ int2 tiles_of(const Params& p, const Seq& s, int b) {
   constexpr int BK = Shape<MB>::BK;
-  const int from = s.base + (p.parents == nullptr ? b * MB / p.group : 0);
+  const int from = s.base + (p.parents == nullptr && b > 0 ? b * MB / p.group : 0);
   return make_int2(max(0, from - p.window + 1) / BK, (end_of<MB>(p, s, b) + BK - 1) / BK);
 }
 template <int MB>
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
   constexpr int THREADS = T::THREADS, BK = T::BK, RW = T::RW, KW = T::KW, KPW = T::KPW, MT = T::MT;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t sums[T::WARPS];
-  __shared__ int64_t found_at;
+  __shared__ int64_t found_tile;
   __shared__ Seq found;
   __shared__ int found_i, faulted;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -202,32 +208,62 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
   if (tid < 2) mine[tid].state = kNone;
 
   // -------------------------------------------------------------- the block's share of the line
-  Seq sq{};  // of sequence tid: most calls have no more sequences than a block has threads
-  int64_t own = 0, all = 0;
-  if (tid < p.n) {
-    sq = sequence(p, tid, blockIdx.x == 0);
-    own = head_tiles<MB>(p, sq) * p.kv_heads;
-  }
-  if (tid == 0) faulted = *reinterpret_cast<volatile int*>(p.status);
-  for (int i = tid + THREADS; i < p.n; i += THREADS)
-    all += head_tiles<MB>(p, sequence(p, i, blockIdx.x == 0)) * p.kv_heads;
-  all += own;
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xffffffffu, all, d);
-  if (lane == 0) sums[warp] = all;
-  __syncthreads();
-  if (faulted != 0) return;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < T::WARPS; ++w) all += sums[w];
-  const int64_t blocks = all < int64_t(gridDim.x) ? all : int64_t(gridDim.x);
-  if (int64_t(blockIdx.x) >= blocks) return;
-  int64_t left;  // tiles to go
-  {
-    const int64_t each = all / blocks, more = all % blocks, b = blockIdx.x;
-    const int64_t lo = each * b + (b < more ? b : more);
+  int status = 0;
+  if (lane == 0) status = *reinterpret_cast<volatile int*>(p.status);
+  Seq sq{};             // the sequence at which the share begins
+  int seq_i = 0;        // its place in the list
+  int64_t found_at = 0; // tiles before the share's first in it
+  int64_t left = 0;     // tiles to go
+  // The share of `all` tiles: its first tile; false where there are fewer tiles than blocks.
+  auto share = [&](int64_t all, int64_t* first) {
+    const int64_t blocks = all < int64_t(gridDim.x) ? all : int64_t(gridDim.x), b = blockIdx.x;
+    if (b >= blocks) return false;
+    const int64_t each = divide(all, blocks), more = all - each * blocks;
+    *first = each * b + (b < more ? b : more);
     left = each + (b < more ? 1 : 0);
-    int64_t before = 0;
+    return true;
+  };
+  auto scan = [&](int64_t x) {  // inclusive sums over the warp
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  if (p.n <= 32) {  // a lane a sequence, every warp for itself
+    int64_t x = 0, first = 0;
+    if (lane < p.n) {
+      sq = sequence(p, lane, blockIdx.x == 0);
+      x = head_tiles<MB>(p, sq) * p.kv_heads;
+    }
+    const int64_t to = scan(x);
+    if (__shfl_sync(0xffffffffu, status, 0) != 0) return;
+    if (!share(__shfl_sync(0xffffffffu, to, 31), &first)) return;
+    seq_i = __ffs(int(__ballot_sync(0xffffffffu, first < to))) - 1;
+    found_at = first - __shfl_sync(0xffffffffu, to - x, seq_i);
+    sq.slot = __shfl_sync(0xffffffffu, sq.slot, seq_i);
+    sq.first = __shfl_sync(0xffffffffu, sq.first, seq_i);
+    sq.count = __shfl_sync(0xffffffffu, sq.count, seq_i);
+    sq.base = __shfl_sync(0xffffffffu, sq.base, seq_i);
+    sq.len = __shfl_sync(0xffffffffu, sq.len, seq_i);
+  } else {  // a thread a sequence
+    int64_t own = 0, all = 0, first = 0, before = 0;
+    if (tid < p.n) {
+      sq = sequence(p, tid, blockIdx.x == 0);
+      own = head_tiles<MB>(p, sq) * p.kv_heads;
+    }
+    for (int i = tid + THREADS; i < p.n; i += THREADS)
+      all += head_tiles<MB>(p, sequence(p, i, blockIdx.x == 0)) * p.kv_heads;
+    all = scan(all + own);
+    if (lane == 31) sums[warp] = all;
+    if (tid == 0) faulted = status;
+    __syncthreads();
+    if (faulted != 0) return;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < T::WARPS; ++w) all += sums[w];
+    if (!share(all, &first)) return;
     for (int i0 = 0; i0 < p.n; i0 += THREADS) {
       const int i = i0 + tid;
       int64_t x = own;
@@ -238,35 +274,31 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
           x = head_tiles<MB>(p, sq) * p.kv_heads;
         }
       }
-      int64_t inc = x;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
+      const int64_t to = scan(x);
       __syncthreads();
-      if (lane == 31) sums[warp] = inc;
+      if (lane == 31) sums[warp] = to;
       __syncthreads();
-      int64_t at = before + inc - x;
+      int64_t at = before + to - x;
       for (int w = 0; w < T::WARPS; ++w) {
         at += w < warp ? sums[w] : 0;
         before += sums[w];
       }
-      if (lo >= at && lo < at + x) {
+      if (first >= at && first < at + x) {
         found = sq;
         found_i = i;
-        found_at = lo - at;
+        found_tile = first - at;
       }
-      if (before > lo) break;  // the same for all threads
+      if (before > first) break;  // the same for all threads
     }
     __syncthreads();
+    seq_i = found_i;
+    sq = found;
+    found_at = found_tile;
   }
-  int seq_i = found_i;
-  sq = found;
   int kv, blk = 0, t_off;
   {
     const int64_t per = head_tiles<MB>(p, sq);
-    kv = int(found_at / per);
+    kv = int(divide(found_at, per));
     int64_t off = found_at - kv * per;
     int2 t = tiles_of<MB>(p, sq, 0);
     while (off >= t.y - t.x) {
@@ -327,28 +359,46 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
       cp_commit();
     };
 
-    __syncthreads();  // the piece before is done with shared memory
+    // What the piece needs from memory first, all on its way at once: pages of the first tiles, the
+    // rows' queries, the new tokens' parents.
+    constexpr int PLACES = (S * BK + THREADS - 1) / THREADS;
+    int first_pages[PLACES];
 #pragma unroll
-    for (int i = tid / BK; i < S; i += THREADS / BK)
-      ring[i * BK + tid % BK] = place(entry(i, tid % BK), i, tid % BK);
+    for (int x = 0; x < PLACES; ++x) {
+      const int at = tid + x * THREADS;
+      first_pages[x] = at < S * BK ? entry(at / BK, at % BK) : 0;
+    }
     int page_ahead = tid < BK ? entry(S, tid) : 0;
-    // the rows' queries; where they go on to registers, they pass through the last stage's place
-    constexpr uint32_t qs = T::Q_SHARED ? L::Q_OFF : (S - 1) * 2 * L::TILE;
-    {
-      for (int x = tid; x < MB * CH; x += THREADS) {
-        const int r = x / CH, ch = x % CH, rr = row0 + r;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (rr < rows) {
-          const int t = rr / p.group, h = rr - t * p.group;
-          val = *reinterpret_cast<const uint4*>(p.q + int64_t(sq.first + t) * p.q_token +
-                                                int64_t(kv * p.group + h) * p.q_head + ch * 8);
-        }
-        *reinterpret_cast<uint4*>(smem + qs + r * DH * 2 + ((ch ^ (r & 7)) * 16)) = val;
+    constexpr int QUERIES = MB * CH / THREADS;
+    uint4 queries[QUERIES];
+#pragma unroll
+    for (int x = 0; x < QUERIES; ++x) {
+      const int r = (tid + x * THREADS) / CH, ch = tid % CH, rr = row0 + r;
+      queries[x] = make_uint4(0, 0, 0, 0);
+      if (rr < rows) {
+        const int t = rr / p.group, h = rr - t * p.group;
+        queries[x] = *reinterpret_cast<const uint4*>(p.q + int64_t(sq.first + t) * p.q_token +
+                                                     int64_t(kv * p.group + h) * p.q_head + ch * 8);
       }
     }
-    if (p.parents != nullptr && tid < sq.count) depth[tid] = p.parents[sq.first + tid];
-    __syncthreads();
+    int parent = -1;
+    if (p.parents != nullptr && tid < sq.count) parent = p.parents[sq.first + tid];
+    __syncthreads();  // the piece before is done with shared memory
 #pragma unroll
+    for (int x = 0; x < PLACES; ++x) {
+      const int at = tid + x * THREADS;
+      if (at < S * BK) ring[at] = place(first_pages[x], at / BK, at % BK);
+    }
+    // where the queries go on to registers, they pass through the last stage's place
+    constexpr uint32_t qs = T::Q_SHARED ? L::Q_OFF : (S - 1) * 2 * L::TILE;
+#pragma unroll
+    for (int x = 0; x < QUERIES; ++x) {
+      const int r = (tid + x * THREADS) / CH, ch = tid % CH;
+      *reinterpret_cast<uint4*>(smem + qs + r * DH * 2 + ((ch ^ (r & 7)) * 16)) = queries[x];
+    }
+    if (p.parents != nullptr && tid < sq.count) depth[tid] = parent;
+    __syncthreads();
+#pragma unroll 1  // one copy of the code: cold instructions cost more than the loop
     for (int i = 0; i < S - 1; ++i) load(i);
     if (p.parents != nullptr) {
       // walk to the root: 64 steps at most, since a parent comes before its child
@@ -563,8 +613,9 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
       mine[side].kv = kv;
       mine[side].state = ends ? kEnds : kGoesOn;
     }
-    for (int x = tid; x < MB * (DH / 8); x += THREADS) {
-      const int r = x / (DH / 8), ch = x % (DH / 8), rr = row0 + r;
+#pragma unroll
+    for (int x0 = 0; x0 < MB * CH; x0 += THREADS) {
+      const int r = (x0 + tid) / CH, ch = tid % CH, rr = row0 + r;
       if (rr >= rows) continue;
       float best = -INFINITY, total = 0.f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       float2 st[KW];
