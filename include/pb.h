@@ -679,7 +679,7 @@ typedef struct pb_cache {
   int32_t page_size; /* tokens of a page */
   int32_t kv_heads;
   int32_t head_dim;   /* 64 or 128 */
-  int32_t slots;      /* sequences, 2^18 at most */
+  int32_t slots;      /* sequences, 2^16 at most */
   int32_t slot_pages; /* pages of a sequence at most; slot_pages * page_size <= 2^30 */
   void* k;            /* bf16 [layers, pages, kv_heads, page_size, head_dim], 16-byte aligned */
   void* v;
@@ -706,7 +706,7 @@ pb_status pb_cache_extend(const pb_cache* cache, int32_t n, const int32_t* slots
 /* Writes k and v of the last starts[i + 1] - starts[i] tokens of every sequence (those that
  * pb_cache_extend made room for), into `layers` layers from `layer` on. k, v: bf16 views [layers,
  * tokens, kv_heads, head_dim] (batch_stride is the layers' stride). Rows in no sequence are not
- * read. */
+ * used. */
 pb_status pb_cache_write(const pb_cache* cache, int32_t layer, int32_t layers, int32_t n,
                          const int32_t* slots, const int32_t* starts, int32_t tokens,
                          const pb_heads* k, const pb_heads* v, void* stream);

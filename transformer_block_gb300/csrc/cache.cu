@@ -6,11 +6,12 @@
 // host, and can be a captured graph.
 //
 // Bookkeeping is small (a few thousand words): one block checks a whole call, so that a call at fault
-// changes nothing, and does it, a warp a sequence. Free pages are those whose count is zero, found
-// in rising order by a scan (one block scan for 4096 pages): their numbers depend on nothing but the
-// counts, whatever the order in which sequences came and went, and there is no list that could
-// disagree with them. A fork copies rows of the table, which a block a sequence does, in two launches
-// (read all, then write), since a slot may be read and written in one call.
+// changes nothing, and does it. It waits for memory, so it takes few steps that depend on one
+// another: a thread a sequence for its words, then 16 lanes a sequence for its pages. Free pages are
+// those whose count is zero, found in rising order by a scan (one block scan for 4096 pages): their
+// numbers depend on nothing but the counts, whatever the order in which sequences came and went, and
+// there is no list that could disagree with them. A fork reads all its sources' rows of the table
+// before it writes one, since a slot may be read and written in one call.
 //
 // Data moves by 16-byte accesses, a row of a head (128 or 256 bytes) by 8 or 16 lanes: bound by
 // memory for many sequences and by the launch for few.
@@ -23,17 +24,16 @@
 namespace pb {
 namespace {
 
-struct Info {  // of a listed sequence, for the launch that moves data
-  int base;    // keep: tokens before the new ones; extend: rank of its first new page; fork: length
-  int count;   // keep: tokens to keep; extend: 1 where its last page is copied
-  int copy;    // extend: place in the list of copies
-  int pad;
+struct Job {  // a listed sequence
+  int slot;   // -1: none, or at fault
+  int len;    // its length
+  int a, b, c, d;  // by the call
 };
 struct Copy {
   int from, to, rows, pad;
 };
 
-// Scratch: header, Info [slots], Copy [slots], free pages [pages] or rows of the table [slots,
+// Scratch: header, Job [slots], Copy [slots], free pages [pages] or rows of the table [slots,
 // slot_pages].
 struct Header {
   int go;      // the call is sound
@@ -46,14 +46,14 @@ struct Cache {
   __nv_bfloat16 *k, *v;
   int *table, *lengths, *refs, *status;
   Header* header;
-  Info* info;
+  Job* jobs;
   Copy* copies;
   int* list;
 };
 
 size_t scratch_need(const pb_cache& c) {
   const size_t list = size_t(c.slots) * c.slot_pages;
-  return kHeaderBytes + size_t(c.slots) * (sizeof(Info) + sizeof(Copy)) +
+  return kHeaderBytes + size_t(c.slots) * (sizeof(Job) + sizeof(Copy)) +
          4 * (list > size_t(c.pages) ? list : size_t(c.pages));
 }
 
@@ -64,18 +64,22 @@ Cache device_view(const pb_cache& c, void* scratch) {
           c.table,   c.lengths, c.refs,      c.status,   nullptr,    nullptr, nullptr, nullptr};
   if (s != nullptr) {
     d.header = reinterpret_cast<Header*>(s);
-    d.info = reinterpret_cast<Info*>(s + kHeaderBytes);
-    d.copies = reinterpret_cast<Copy*>(d.info + c.slots);
-    d.list = reinterpret_cast<int*>(d.copies + c.slots);
+    d.copies = reinterpret_cast<Copy*>(s + kHeaderBytes);
+    d.jobs = reinterpret_cast<Job*>(d.copies + c.slots);
+    d.list = reinterpret_cast<int*>(d.jobs + c.slots);
   }
   return d;
 }
 
 constexpr int BLOCK = 1024, WARPS = BLOCK / 32;
+constexpr int LANES = 16, GROUPS = BLOCK / LANES;  // lanes of a sequence
+constexpr int kListed = 2048;                      // free pages listed in shared memory
 
 struct Shared {
   uint32_t seen[kMaxSlots / 32];  // slots listed
+  Job job[BLOCK];                 // of the 1024 sequences at work
   int sums[WARPS];
+  int list[kListed];
   int fault;
 };
 
@@ -109,7 +113,8 @@ __device__ int block_scan(int x, Shared& sh, int* total) {
   return before + inc - x;
 }
 
-// Clears the bits of the slots and tells whether the cache is free of faults (all threads).
+// Clears the bits of the slots and tells whether the cache is free of faults (all threads). What a
+// thread has read from memory before is on its way meanwhile.
 __device__ bool begin(const Cache& c, Shared& sh) {
   for (int i = threadIdx.x; i < (c.slots + 31) / 32; i += BLOCK) sh.seen[i] = 0;
   if (threadIdx.x == 0) {
@@ -138,72 +143,119 @@ __device__ __forceinline__ bool good_length(const Cache& c, int len) {
 __device__ __forceinline__ bool good_page(const Cache& c, int page) {
   return page >= 0 && page < c.pages;
 }
-// A slot of the list: whether it may be used.
-__device__ bool check_slot(const Cache& c, Shared& sh, int slot) {
+// A slot of the list, which must not come again: whether it may be used, and its length.
+__device__ bool check_slot(const Cache& c, Shared& sh, int slot, int* len) {
   if (slot < 0 || slot >= c.slots ||
       ((atomicOr(&sh.seen[slot >> 5], 1u << (slot & 31)) >> (slot & 31)) & 1u) != 0) {
     set_fault(sh, kFaultSlot);
     return false;
   }
-  if (!good_length(c, c.lengths[slot])) {
+  *len = c.lengths[slot];
+  if (!good_length(c, *len)) {
     set_fault(sh, kFaultTable);
     return false;
   }
   return true;
 }
-// The pages [a, z) of a slot lose a user; one warp.
-__device__ void release(const Cache& c, int slot, int a, int z) {
+// The pages [a, z) of a slot lose a user; LANES lanes.
+__device__ __forceinline__ void release(const Cache& c, int slot, int a, int z) {
   const int* row = c.table + int64_t(slot) * c.slot_pages;
-  for (int i = a + int(threadIdx.x & 31); i < z; i += 32) atomicSub(&c.refs[row[i]], 1);
+#pragma unroll 4
+  for (int i = a + int(threadIdx.x % LANES); i < z; i += LANES) atomicSub(&c.refs[row[i]], 1);
 }
-// Whether the pages [a, z) of a slot are pages; one warp, its lanes together.
-__device__ void check_pages(const Cache& c, Shared& sh, int slot, int a, int z) {
+// Whether the pages [a, z) of a slot are pages; LANES lanes.
+__device__ __forceinline__ void check_pages(const Cache& c, Shared& sh, int slot, int a, int z) {
   const int* row = c.table + int64_t(slot) * c.slot_pages;
-  for (int i = a + int(threadIdx.x & 31); i < z; i += 32)
-    if (!good_page(c, row[i])) set_fault(sh, kFaultTable);
+  bool sound = true;
+#pragma unroll 4
+  for (int i = a + int(threadIdx.x % LANES); i < z; i += LANES) sound &= good_page(c, row[i]);
+  if (!sound) set_fault(sh, kFaultTable);
+}
+// For every sequence of the list, 1024 at a time: a thread fills its job, kept in scratch too where
+// there are more, or where the launch behind reads it; or (filled) the jobs are those of before. Then
+// LANES lanes work on each.
+template <class Fill, class Work>
+__device__ __forceinline__ void each(const Cache& c, Shared& sh, int n, bool keep, Fill&& fill,
+                                     Work&& work) {
+  const int tid = threadIdx.x;
+  for (int i0 = 0; i0 < n; i0 += BLOCK) {
+    __syncthreads();
+    Job job{-1, 0, 0, 0, 0, 0};
+    if (i0 + tid < n) fill(i0 + tid, job);
+    sh.job[tid] = job;
+    if ((keep || n > BLOCK) && i0 + tid < n) c.jobs[i0 + tid] = job;
+    __syncthreads();
+    for (int g = tid / LANES; g < min(BLOCK, n - i0); g += GROUPS)
+      if (sh.job[g].slot >= 0) work(i0 + g, sh.job[g]);
+  }
+}
+template <class Work>
+__device__ __forceinline__ void each_again(const Cache& c, Shared& sh, int n, Work&& work) {
+  const int tid = threadIdx.x;
+  for (int i0 = 0; i0 < n; i0 += BLOCK) {
+    if (n > BLOCK) {
+      __syncthreads();
+      if (i0 + tid < n) sh.job[tid] = c.jobs[i0 + tid];
+      __syncthreads();
+    }
+    for (int g = tid / LANES; g < min(BLOCK, n - i0); g += GROUPS) work(i0 + g, sh.job[g]);
+  }
 }
 
 // ------------------------------------------------------------------ extend
 
 __global__ void __launch_bounds__(BLOCK) extend_kernel(const Cache c, int n, const int* slots,
                                                        const int* starts) {
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  const int tid = threadIdx.x, lane = tid % LANES;
   pdl_wait();
   pdl_trigger();
+  // the first pages' counts: whether they are free is needed last
+  int ahead[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ahead[e] = 4 * tid + e < c.pages ? c.refs[4 * tid + e] : 1;
+  const int slot0 = tid < n ? slots[tid] : 0;
+  const int start0 = tid < n ? starts[tid] : 0, start1 = tid < n ? starts[tid + 1] : 0;
   if (!begin(c, sh)) return;
   int need_all = 0, copies = 0;
+  // job: a: tokens more, b: rank of the first new page, c: whether the last page is copied, d: place
+  // in the list of copies
   for (int i0 = 0; i0 < n; i0 += BLOCK) {
     const int i = i0 + tid;
-    int need = 0, copy = 0;
+    Job job{-1, 0, 0, 0, 0, 0};
+    int need = 0;
     if (i < n) {
-      const int slot = slots[i];
-      const int64_t count = int64_t(starts[i + 1]) - starts[i];
-      if (check_slot(c, sh, slot)) {
-        const int len = c.lengths[slot];
+      const int slot = i0 == 0 ? slot0 : slots[i];
+      const int64_t count =
+          i0 == 0 ? int64_t(start1) - start0 : int64_t(starts[i + 1]) - starts[i];
+      if (check_slot(c, sh, slot, &job.len)) {
         if (count < 0) {
           set_fault(sh, kFaultCounts);
-        } else if (len + count > int64_t(c.slot_pages) * c.page_size) {
+        } else if (job.len + count > int64_t(c.slot_pages) * c.page_size) {
           set_fault(sh, kFaultRow);
         } else {
-          if (count > 0 && len % c.page_size != 0) {
-            const int page = c.table[int64_t(slot) * c.slot_pages + len / c.page_size];
+          if (count > 0 && job.len % c.page_size != 0) {
+            const int page = c.table[int64_t(slot) * c.slot_pages + job.len / c.page_size];
             if (!good_page(c, page))
               set_fault(sh, kFaultTable);
             else
-              copy = c.refs[page] > 1;
+              job.c = c.refs[page] > 1;
           }
-          need = pages_of(c, int(len + count)) - pages_of(c, len) + copy;
+          job.slot = slot;
+          job.a = int(count);
+          need = pages_of(c, int(job.len + count)) - pages_of(c, job.len) + job.c;
         }
       }
     }
     // a page more than there are is as many as any: 1024 of them stay below 2^31
     int total, ctotal;
-    const int first = block_scan(min(need, c.pages + 1), sh, &total);
-    const int cfirst = block_scan(copy, sh, &ctotal);
-    if (i < n) c.info[i] = Info{need_all + first, copy, copies + cfirst, 0};
-    copies += ctotal;
+    job.b = need_all + block_scan(min(need, c.pages + 1), sh, &total);
+    job.d = copies + block_scan(job.c, sh, &ctotal);
+    sh.job[tid] = job;
+    if (n > BLOCK && i < n) c.jobs[i] = job;
     need_all += total;
+    copies += ctotal;
     if (need_all > c.pages) {
       set_fault(sh, kFaultPages);
       break;  // the same for all threads
@@ -211,6 +263,7 @@ __global__ void __launch_bounds__(BLOCK) extend_kernel(const Cache c, int n, con
   }
   __syncthreads();
   // the need_all free pages of lowest number
+  const bool listed = need_all <= kListed;
   if (sh.fault == 0) {
     int found = 0;
     for (int p0 = 0; p0 < c.pages && found < need_all; p0 += 4 * BLOCK) {
@@ -218,7 +271,7 @@ __global__ void __launch_bounds__(BLOCK) extend_kernel(const Cache c, int n, con
       int used[4], zeros = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        used[e] = p + e < c.pages ? c.refs[p + e] : 1;
+        used[e] = p0 == 0 ? ahead[e] : p + e < c.pages ? c.refs[p + e] : 1;
         zeros += used[e] == 0;
       }
       int total;
@@ -226,7 +279,7 @@ __global__ void __launch_bounds__(BLOCK) extend_kernel(const Cache c, int n, con
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (used[e] == 0) {
-          if (rank < need_all) c.list[rank] = p + e;
+          if (rank < need_all) (listed ? sh.list : c.list)[rank] = p + e;
           ++rank;
         }
       found += total;
@@ -235,29 +288,26 @@ __global__ void __launch_bounds__(BLOCK) extend_kernel(const Cache c, int n, con
     if (found < need_all && tid == 0) set_fault(sh, kFaultPages);
   }
   if (!decide(c, sh, copies)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int slot = slots[i], count = starts[i + 1] - starts[i];
-    const int len = c.lengths[slot];
-    const Info f = c.info[i];
-    int* row = c.table + int64_t(slot) * c.slot_pages;
-    const int have = pages_of(c, len), more = pages_of(c, len + count) - have;
-    for (int j = lane; j < more; j += 32) {
-      const int page = c.list[f.base + f.count + j];
+  const int* list = listed ? sh.list : c.list;
+  each_again(c, sh, n, [&](int, const Job& job) {
+    int* row = c.table + int64_t(job.slot) * c.slot_pages;
+    const int have = pages_of(c, job.len), more = pages_of(c, job.len + job.a) - have;
+    for (int j = lane; j < more; j += LANES) {
+      const int page = list[job.b + job.c + j];
       row[have + j] = page;
       c.refs[page] = 1;
     }
-    __syncwarp();  // all lanes have read the length
     if (lane == 0) {
-      if (f.count != 0) {
-        const int at = len / c.page_size, old = row[at], page = c.list[f.base];
-        c.copies[f.copy] = Copy{old, page, len % c.page_size, 0};
+      if (job.c != 0) {
+        const int at = job.len / c.page_size, old = row[at], page = list[job.b];
+        c.copies[job.d] = Copy{old, page, job.len % c.page_size, 0};
         row[at] = page;
         c.refs[page] = 1;
         atomicSub(&c.refs[old], 1);
       }
-      c.lengths[slot] = len + count;
+      c.lengths[job.slot] = job.len + job.a;
     }
-  }
+  });
 }
 
 // Copies the rows of the listed pages, a head of a layer of k or v at a time.
@@ -308,6 +358,22 @@ __global__ void __launch_bounds__(256) write_kernel(const Cache c, int layer0, i
   for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units;
        u += int64_t(gridDim.x) * 8) {
     const int t = int(u / layers), layer = int(u % layers);
+    // the rows are on their way while their place is found
+    const int per = c.head_dim / 8, chunks = c.kv_heads * per;
+    const __nv_bfloat16* const ks = k.p + layer * k.layer + t * k.token;
+    const __nv_bfloat16* const vs = v.p + layer * v.layer + t * v.token;
+    uint4 x[2][4];
+    auto fetch = [&](int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = i + 32 * e, h = j / per, d = (j - h * per) * 8;
+        if (j < chunks) {
+          x[0][e] = *reinterpret_cast<const uint4*>(ks + h * k.head + d);
+          x[1][e] = *reinterpret_cast<const uint4*>(vs + h * v.head + d);
+        }
+      }
+    };
+    fetch(lane);
     if (t < starts[0] || t >= starts[n]) continue;
     // the last i with starts[i] <= t, 32 candidates at a time (starts that fall find any): it is
     // among lo .. lo + span - 1
@@ -342,21 +408,11 @@ __global__ void __launch_bounds__(256) write_kernel(const Cache c, int layer0, i
       if (lane == 0) cache_fault(c.status, kFaultTable);
       continue;
     }
-    const int per = c.head_dim / 8;
     const int64_t plane = int64_t(c.page_size) * c.head_dim;
     const int64_t dst0 =
         (int64_t(layer0 + layer) * c.pages + page) * c.kv_heads * plane + int64_t(row) * c.head_dim;
-    const int chunks = c.kv_heads * per;
     for (int i = lane; i < chunks; i += 128) {
-      uint4 x[2][4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = i + 32 * e, h = j / per, d = (j - h * per) * 8;
-        if (j < chunks) {
-          x[0][e] = *reinterpret_cast<const uint4*>(k.p + layer * k.layer + t * k.token + h * k.head + d);
-          x[1][e] = *reinterpret_cast<const uint4*>(v.p + layer * v.layer + t * v.token + h * v.head + d);
-        }
-      }
+      if (i != lane) fetch(i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = i + 32 * e, h = j / per, d = (j - h * per) * 8;
@@ -376,53 +432,53 @@ __global__ void __launch_bounds__(256) write_kernel(const Cache c, int layer0, i
 __global__ void __launch_bounds__(BLOCK) keep_kernel(const Cache c, int n, const int* slots,
                                                      const int* starts, int tokens,
                                                      const int* path, const int* kept) {
-  __shared__ Shared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  const int lane = threadIdx.x % LANES;
   pdl_wait();
   pdl_trigger();
   if (!begin(c, sh)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int slot = slots[i], first = starts[i], a = kept[i];
-    const int64_t count = int64_t(starts[i + 1]) - first;
-    int sound = 0;
-    if (lane == 0 && check_slot(c, sh, slot)) {
-      if (count < 0 || first < 0 || first + count > tokens || count > c.lengths[slot])
-        set_fault(sh, kFaultCounts);
-      else if (a < 0 || a > count)
-        set_fault(sh, kFaultPath);
-      else
-        sound = 1;
-    }
-    if (__shfl_sync(0xffffffffu, sound, 0) == 0) continue;
-    const int len = c.lengths[slot], base = len - int(count);
-    check_pages(c, sh, slot, base / c.page_size, pages_of(c, len));
-    bool moved = false;
-    for (int j = lane; j < a; j += 32) {
-      const int at = path[first + j], before = j > 0 ? path[first + j - 1] : -1;
-      if (at <= before || at >= count) set_fault(sh, kFaultPath);
-      moved |= at != j;
-    }
-    if (__any_sync(0xffffffffu, moved)) {
-      const int* row = c.table + int64_t(slot) * c.slot_pages;
-      for (int q = base / c.page_size + lane; q < pages_of(c, base + a); q += 32)
-        if (good_page(c, row[q]) && c.refs[row[q]] != 1) set_fault(sh, kFaultShared);
-    }
-    if (lane == 0) c.info[i] = Info{base, a, 0, 0};
-  }
+  // job: a: tokens before the new ones, b: new ones, c: those kept, d: the first one's row
+  each(
+      c, sh, n, true,
+      [&](int i, Job& job) {
+        const int slot = slots[i], first = starts[i], a = kept[i];
+        const int64_t count = int64_t(starts[i + 1]) - first;
+        if (!check_slot(c, sh, slot, &job.len)) return;
+        if (count < 0 || first < 0 || first + count > tokens || count > job.len) {
+          set_fault(sh, kFaultCounts);
+        } else if (a < 0 || a > count) {
+          set_fault(sh, kFaultPath);
+        } else {
+          job = Job{slot, job.len, job.len - int(count), int(count), a, first};
+        }
+      },
+      [&](int, const Job& job) {
+        const int* row = c.table + int64_t(job.slot) * c.slot_pages;
+        check_pages(c, sh, job.slot, job.a / c.page_size, pages_of(c, job.len));
+        bool rises = true, moved = false;
+        for (int j = lane; j < job.c; j += LANES) {
+          const int at = path[job.d + j], before = j > 0 ? path[job.d + j - 1] : -1;
+          rises &= at > before && at < job.b;
+          moved |= at != j;
+        }
+        if (!rises) set_fault(sh, kFaultPath);
+        // the lanes of this sequence among the warp's that are here
+        const uint32_t group = 0xffffu << (threadIdx.x & 16);
+        if (__any_sync(group, moved))
+          for (int q = job.a / c.page_size + lane; q < pages_of(c, job.a + job.c); q += LANES)
+            if (good_page(c, row[q]) && c.refs[row[q]] != 1) set_fault(sh, kFaultShared);
+      });
   if (!decide(c, sh, 0)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int slot = slots[i];
-    const Info f = c.info[i];
-    release(c, slot, pages_of(c, f.base + f.count), pages_of(c, c.lengths[slot]));
-    __syncwarp();
-    if (lane == 0) c.lengths[slot] = f.base + f.count;
-  }
+  each_again(c, sh, n, [&](int, const Job& job) {
+    release(c, job.slot, pages_of(c, job.a + job.c), pages_of(c, job.len));
+    if (lane == 0) c.lengths[job.slot] = job.a + job.c;
+  });
 }
 
 // A group of head_dim / 8 lanes a head of a layer of k or v of a sequence: rows move forward or stay,
 // in rising order, so a row is read before anything is written over it, eight at a time too.
-__global__ void __launch_bounds__(256) move_kernel(const Cache c, int n, const int* slots,
-                                                   const int* starts, const int* path) {
+__global__ void __launch_bounds__(256) move_kernel(const Cache c, int n, const int* path) {
   pdl_wait();
   pdl_trigger();
   if (c.header->go == 0) return;
@@ -435,9 +491,9 @@ __global__ void __launch_bounds__(256) move_kernel(const Cache c, int n, const i
     const int h = int(u % c.kv_heads);
     const int64_t w = u / c.kv_heads;
     const int which = int(w & 1), layer = int((w >> 1) % c.layers), i = int((w >> 1) / c.layers);
-    const Info f = c.info[i];
-    const int* row = c.table + int64_t(slots[i]) * c.slot_pages;
-    const int* from = path + starts[i];
+    const Job f = c.jobs[i];
+    const int* row = c.table + int64_t(f.slot) * c.slot_pages;
+    const int* from = path + f.d;
     __nv_bfloat16* pool = (which ? c.v : c.k) +
                           (int64_t(layer) * c.pages * c.kv_heads + h) * plane + lane * 8;
     auto place = [&](int t) {
@@ -445,59 +501,88 @@ __global__ void __launch_bounds__(256) move_kernel(const Cache c, int n, const i
       return reinterpret_cast<uint4*>(pool + int64_t(row[at]) * c.kv_heads * plane +
                                       int64_t(t - at * c.page_size) * c.head_dim);
     };
-    for (int j = 0; j < f.count; j += 8) {
+    for (int j = 0; j < f.c; j += 8) {
       uint4 x[8];
       uint32_t move = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (j + e < f.count && from[j + e] != j + e) {
-          x[e] = *place(f.base + from[j + e]);
+        if (j + e < f.c && from[j + e] != j + e) {
+          x[e] = *place(f.a + from[j + e]);
           move |= 1u << e;
         }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if ((move >> e) & 1u) *place(f.base + j + e) = x[e];
+        if ((move >> e) & 1u) *place(f.a + j + e) = x[e];
     }
   }
 }
 
 // ------------------------------------------------------------------ fork
 
-__global__ void __launch_bounds__(BLOCK) fork_check_kernel(const Cache c, int n, const int* from,
-                                                           const int* to) {
-  __shared__ Shared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// A call's sources and targets checked. ALL: the whole call in this one block; else the launches
+// behind go on.
+template <bool ALL>
+__global__ void __launch_bounds__(BLOCK) fork_kernel(const Cache c, int n, const int* from,
+                                                     const int* to) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  const int lane = threadIdx.x % LANES;
   pdl_wait();
   pdl_trigger();
   if (!begin(c, sh)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int src = from[i], dst = to[i];
-    int sound = 0;
-    if (lane == 0 && check_slot(c, sh, dst)) {
-      if (src < 0 || src >= c.slots)
-        set_fault(sh, kFaultSlot);
-      else if (!good_length(c, c.lengths[src]))
-        set_fault(sh, kFaultTable);
-      else
-        sound = 1;
+  // job: slot, len: the target and what it holds; a: the source, b: its length
+  each(
+      c, sh, n, true,
+      [&](int i, Job& job) {
+        const int src = from[i], dst = to[i];
+        if (!check_slot(c, sh, dst, &job.len)) return;
+        if (src < 0 || src >= c.slots) {
+          set_fault(sh, kFaultSlot);
+          return;
+        }
+        job.a = src;
+        job.b = c.lengths[src];
+        if (good_length(c, job.b))
+          job.slot = dst;
+        else
+          set_fault(sh, kFaultTable);
+      },
+      [&](int, const Job& job) {
+        check_pages(c, sh, job.a, 0, pages_of(c, job.b));
+        check_pages(c, sh, job.slot, 0, pages_of(c, job.len));
+      });
+  if (!decide(c, sh, 0) || !ALL) return;
+  each_again(c, sh, n, [&](int i, const Job& job) {
+    const int* row = c.table + int64_t(job.a) * c.slot_pages;
+    const int m = pages_of(c, job.b);
+#pragma unroll 4
+    for (int j = lane; j < m; j += LANES) {
+      const int page = row[j];
+      c.list[int64_t(i) * c.slot_pages + j] = page;
+      atomicAdd(&c.refs[page], 1);
     }
-    if (__shfl_sync(0xffffffffu, sound, 0) == 0) continue;
-    check_pages(c, sh, src, 0, pages_of(c, c.lengths[src]));
-    check_pages(c, sh, dst, 0, pages_of(c, c.lengths[dst]));
-    if (lane == 0) c.info[i] = Info{c.lengths[src], 0, 0, 0};
-  }
-  decide(c, sh, 0);
+  });
+  __syncthreads();
+  each_again(c, sh, n, [&](int i, const Job& job) {
+    int* row = c.table + int64_t(job.slot) * c.slot_pages;
+    release(c, job.slot, 0, pages_of(c, job.len));
+    __syncwarp(0xffffu << (threadIdx.x & 16));  // the old pages are read
+    const int m = pages_of(c, job.b);
+#pragma unroll 4
+    for (int j = lane; j < m; j += LANES) row[j] = c.list[int64_t(i) * c.slot_pages + j];
+    if (lane == 0) c.lengths[job.slot] = job.b;
+  });
 }
 
 // The sources' rows into scratch; their pages get a user more.
-__global__ void __launch_bounds__(256) fork_read_kernel(const Cache c, const int* from) {
+__global__ void __launch_bounds__(256) fork_read_kernel(const Cache c) {
   pdl_wait();
   pdl_trigger();
   if (c.header->go == 0) return;
-  const int i = blockIdx.x;
-  const int* row = c.table + int64_t(from[i]) * c.slot_pages;
-  int* save = c.list + int64_t(i) * c.slot_pages;
-  const int m = pages_of(c, c.info[i].base);
+  const Job job = c.jobs[blockIdx.x];
+  const int* row = c.table + int64_t(job.a) * c.slot_pages;
+  int* save = c.list + int64_t(blockIdx.x) * c.slot_pages;
+  const int m = pages_of(c, job.b);
   for (int j = threadIdx.x; j < m; j += 256) {
     const int page = row[j];
     save[j] = page;
@@ -505,45 +590,47 @@ __global__ void __launch_bounds__(256) fork_read_kernel(const Cache c, const int
   }
 }
 
-__global__ void __launch_bounds__(256) fork_write_kernel(const Cache c, const int* to) {
+__global__ void __launch_bounds__(256) fork_write_kernel(const Cache c) {
   pdl_wait();
   pdl_trigger();
   if (c.header->go == 0) return;
-  const int i = blockIdx.x, slot = to[i];
-  int* row = c.table + int64_t(slot) * c.slot_pages;
-  const int* save = c.list + int64_t(i) * c.slot_pages;
-  const int m = pages_of(c, c.info[i].base), old = pages_of(c, c.lengths[slot]);
+  const Job job = c.jobs[blockIdx.x];
+  int* row = c.table + int64_t(job.slot) * c.slot_pages;
+  const int* save = c.list + int64_t(blockIdx.x) * c.slot_pages;
+  const int m = pages_of(c, job.b), old = pages_of(c, job.len);
   for (int j = threadIdx.x; j < max(m, old); j += 256) {
     if (j < old) atomicSub(&c.refs[row[j]], 1);
     if (j < m) row[j] = save[j];
   }
-  __syncthreads();  // every thread has read the length
-  if (threadIdx.x == 0) c.lengths[slot] = c.info[i].base;
+  if (threadIdx.x == 0) c.lengths[job.slot] = job.b;
 }
 
 // ------------------------------------------------------------------ truncate
 
 __global__ void __launch_bounds__(BLOCK) truncate_kernel(const Cache c, int n, const int* slots,
                                                          const int* lengths) {
-  __shared__ Shared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared& sh = *reinterpret_cast<Shared*>(raw);
+  const int lane = threadIdx.x % LANES;
   pdl_wait();
   pdl_trigger();
   if (!begin(c, sh)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int slot = slots[i];
-    const int sound = lane == 0 ? int(check_slot(c, sh, slot)) : 0;
-    if (__shfl_sync(0xffffffffu, sound, 0) == 0) continue;
-    const int len = c.lengths[slot], to = min(len, max(0, lengths[i]));
-    check_pages(c, sh, slot, pages_of(c, to), pages_of(c, len));
-  }
+  each(
+      c, sh, n, false,
+      [&](int i, Job& job) {  // a: the new length
+        const int slot = slots[i], to = lengths[i];
+        if (!check_slot(c, sh, slot, &job.len)) return;
+        job.slot = slot;
+        job.a = min(job.len, max(0, to));
+      },
+      [&](int, const Job& job) {
+        check_pages(c, sh, job.slot, pages_of(c, job.a), pages_of(c, job.len));
+      });
   if (!decide(c, sh, 0)) return;
-  for (int i = warp; i < n; i += WARPS) {
-    const int slot = slots[i], len = c.lengths[slot], to = min(len, max(0, lengths[i]));
-    release(c, slot, pages_of(c, to), pages_of(c, len));
-    __syncwarp();
-    if (lane == 0) c.lengths[slot] = to;
-  }
+  each_again(c, sh, n, [&](int, const Job& job) {
+    release(c, job.slot, pages_of(c, job.a), pages_of(c, job.len));
+    if (lane == 0) c.lengths[job.slot] = job.a;
+  });
 }
 
 // ------------------------------------------------------------------ arguments
@@ -593,6 +680,17 @@ pb_status sm_count(int* sms) {
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "cudaDeviceGetAttribute");
 }
 
+// A bookkeeping launch: one block.
+template <class... P, class... A>
+cudaError_t launch_one(void (*kernel)(P...), cudaStream_t st, const A&... args) {
+  return launch_dependent(kernel, dim3(1), dim3(BLOCK), sizeof(Shared), 1, st, args...);
+}
+static_assert(sizeof(Shared) <= 48 * 1024, "no opt-in");
+
+// A fork of at most this many entries of the table is one block's work. 64 sequences of 64 pages:
+// FORK_FIGURES
+constexpr int64_t kForkOne = 16384;
+
 unsigned blocks_for(int64_t units, int64_t per_block, int64_t most) {
   const int64_t b = (units + per_block - 1) / per_block;
   return unsigned(b < most ? b : most);
@@ -624,7 +722,7 @@ pb_status pb_cache_extend(const pb_cache* cache, int32_t n, const int32_t* slots
   if (s != PB_OK) return s;
   const Cache c = device_view(*cache, scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dependent(extend_kernel, dim3(1), dim3(BLOCK), 0, 1, st, c, n, slots, starts);
+  cudaError_t e = launch_one(extend_kernel, st, c, n, slots, starts);
   // few blocks an SM: most calls copy nothing, and then these only look
   const unsigned grid = blocks_for(int64_t(n) * c.layers * 2 * c.kv_heads, 1, 4 * sms);
   if (e == cudaSuccess) e = launch_dependent(copy_kernel, dim3(grid), dim3(256), 0, 1, st, c);
@@ -684,12 +782,11 @@ pb_status pb_cache_keep(const pb_cache* cache, int32_t n, const int32_t* slots,
   if (s != PB_OK) return s;
   const Cache c = device_view(*cache, scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dependent(keep_kernel, dim3(1), dim3(BLOCK), 0, 1, st, c, n, slots, starts,
-                                   tokens, path, kept);
+  cudaError_t e = launch_one(keep_kernel, st, c, n, slots, starts, tokens, path, kept);
   const unsigned grid =
       blocks_for(int64_t(n) * c.layers * 2 * c.kv_heads, 256 / (c.head_dim / 8), 8 * sms);
   if (e == cudaSuccess)
-    e = launch_dependent(move_kernel, dim3(grid), dim3(256), 0, 1, st, c, n, slots, starts, path);
+    e = launch_dependent(move_kernel, dim3(grid), dim3(256), 0, 1, st, c, n, path);
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "cache keep launch");
 }
 
@@ -700,11 +797,15 @@ pb_status pb_cache_fork(const pb_cache* cache, int32_t n, const int32_t* from, c
   if (s != PB_OK || n == 0) return s;
   const Cache c = device_view(*cache, scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dependent(fork_check_kernel, dim3(1), dim3(BLOCK), 0, 1, st, c, n, from, to);
+  if (int64_t(n) * c.slot_pages <= kForkOne) {
+    const cudaError_t one = launch_one(fork_kernel<true>, st, c, n, from, to);
+    return one == cudaSuccess ? PB_OK : cuda_failed(one, "cache fork launch");
+  }
+  cudaError_t e = launch_one(fork_kernel<false>, st, c, n, from, to);
   if (e == cudaSuccess)
-    e = launch_dependent(fork_read_kernel, dim3(unsigned(n)), dim3(256), 0, 1, st, c, from);
+    e = launch_dependent(fork_read_kernel, dim3(unsigned(n)), dim3(256), 0, 1, st, c);
   if (e == cudaSuccess)
-    e = launch_dependent(fork_write_kernel, dim3(unsigned(n)), dim3(256), 0, 1, st, c, to);
+    e = launch_dependent(fork_write_kernel, dim3(unsigned(n)), dim3(256), 0, 1, st, c);
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "cache fork launch");
 }
 
@@ -715,8 +816,8 @@ pb_status pb_cache_truncate(const pb_cache* cache, int32_t n, const int32_t* slo
   const pb_status s = check_call(cache, n, w, scratch, scratch_bytes, true);
   if (s != PB_OK || n == 0) return s;
   const Cache c = device_view(*cache, scratch);
-  const cudaError_t e = launch_dependent(truncate_kernel, dim3(1), dim3(BLOCK), 0, 1,
-                                         static_cast<cudaStream_t>(stream), c, n, slots, lengths);
+  const cudaError_t e = launch_one(truncate_kernel, static_cast<cudaStream_t>(stream), c, n, slots,
+                                   lengths);
   return e == cudaSuccess ? PB_OK : cuda_failed(e, "cache truncate launch");
 }
 

@@ -18,7 +18,7 @@ enum CacheFault : int {
   kFaultPath = 6,    // a kept path that does not rise, or leaves the new tokens
   kFaultShared = 7,  // kept tokens would move into a page that another sequence uses too
 };
-constexpr int kMaxSlots = 1 << 18;  // a bit each in shared memory
+constexpr int kMaxSlots = 1 << 16;  // a bit each in shared memory
 constexpr int kMaxPages = 1 << 20;  // 1024 times as many are counted in 32 bits
 
 inline int64_t page_values(const pb_cache& c) {  // of k or v in one page of one layer
@@ -36,7 +36,7 @@ inline pb_status check_cache_sizes(const pb_cache* c) {
     return record_error(PB_ERR_INVALID_ARG, "cache: every size must be >= 1");
   if (c->head_dim != 64 && c->head_dim != 128)
     return record_error(PB_ERR_UNSUPPORTED, "cache: head_dim must be 64 or 128");
-  if (c->slots > kMaxSlots) return record_error(PB_ERR_UNSUPPORTED, "cache: more than 2^18 slots");
+  if (c->slots > kMaxSlots) return record_error(PB_ERR_UNSUPPORTED, "cache: more than 2^16 slots");
   if (c->pages > kMaxPages || int64_t(c->slot_pages) * c->page_size > (1 << 30))
     return record_error(PB_ERR_UNSUPPORTED,
                         "cache: more than 2^20 pages, or 2^30 tokens in a row of the table");
