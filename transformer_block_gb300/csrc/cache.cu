@@ -347,7 +347,7 @@ struct Rows {
 };
 
 // A warp a token and layer: finds the token's sequence, then copies its heads of k and v.
-__global__ void __launch_bounds__(256) write_kernel(const Cache c, int layer0, int layers, int n,
+__global__ void __launch_bounds__(256, 4) write_kernel(const Cache c, int layer0, int layers, int n,
                                                     const int* slots, const int* starts,
                                                     int tokens, const Rows k, const Rows v) {
   pdl_wait();

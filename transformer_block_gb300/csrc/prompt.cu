@@ -49,6 +49,8 @@ constexpr int BOX = 128 * 64 * 2;          // 128 rows x 64 columns of 16 bits
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint64_t kLimitNs = 2000000000ull;
 constexpr int kBuckets = 2048;
+constexpr int kOwnItems = 64;       // items that a block lists for itself
+constexpr int kOwnSequences = 128;  // of at most so many sequences
 
 // Scratch: the number of entries, then the entries: a pair of tiles of a sequence (every key head
 // has one item for it).
@@ -67,6 +69,7 @@ struct Params {
   float scale_log2;
   int shift;      // bucket = pair index >> shift
   int capacity;   // entries that scratch holds
+  bool own_list;  // blocks list their items themselves
   const int* starts;  // or null: one sequence
   __nv_bfloat16* out;
   int64_t out_ss, out_hs;
@@ -209,6 +212,63 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       : "memory");
 }
 
+__device__ __forceinline__ int item_index(int n, int c, int G) {
+  return n * G + ((n & 1) ? G - 1 - c : c);
+}
+
+// The same order of pairs, later ones of a sequence first and equal ones by sequence, found by every
+// block for its own items alone: no launch before. A lane holds every 32nd sequence's pairs, and the
+// pairs behind level L are sum_s max(0, pairs_s - L - 1). Returns the number of all pairs.
+__device__ __forceinline__ int list_own(const Params& p, Entry* own, int warp, int lane,
+                                        int* status) {
+  constexpr int PER = kOwnSequences / 32;
+  const int pair_tokens = 2 * p.tile_tokens;
+  int2 q[PER];
+  int pairs[PER], all = 0, most = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    q[k] = lane + 32 * k < p.sequences ? sequence(p, lane + 32 * k) : make_int2(0, 0);
+    pairs[k] = (q[k].y + pair_tokens - 1) / pair_tokens;
+    all += pairs[k];
+    most = max(most, pairs[k]);
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (all > p.capacity) {  // falling starts: sequences that overlap, more pairs than tokens allow
+    if (lane == 0 && status != nullptr) atomicCAS(status, 0, int(PB_ERR_INVALID_ARG));
+    all = p.capacity;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  const int items = all * p.kv_heads, G = int(gridDim.x);
+  for (int n = warp; n < kOwnItems; n += THREADS / 32) {
+    const int r = item_index(n, int(blockIdx.x), G);
+    if (r >= items) break;
+    const int e = r / p.kv_heads;
+    auto behind = [&](int level) {
+      int sum = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) sum += max(0, pairs[k] - level - 1);
+      return int(__reduce_add_sync(0xffffffffu, sum));
+    };
+    int lo = 0, hi = most - 1;  // the lowest level with at most e pairs behind it
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (behind(mid) <= e)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    int j = e - behind(lo);  // the j-th sequence that has this level
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, pairs[k] > lo);
+      if (pairs[k] > lo && __popc(m & ((1u << lane) - 1)) == j)
+        own[n] = Entry{q[k].x, q[k].y, lo * pair_tokens, 0};
+      j -= __popc(m);  // below zero behind the one that is meant
+    }
+  }
+  return all;
+}
+
 template <int DH>
 struct Layout {
   static constexpr int Q_TILE = BQ * DH * 2;
@@ -218,7 +278,8 @@ struct Layout {
   static constexpr int V_OFF = K_OFF + K_STAGES * KV_BYTES;
   static constexpr int BAR_OFF = V_OFF + V_STAGES * KV_BYTES;
   static constexpr int NUM_BARS = 23;
-  static constexpr size_t NEED = size_t(BAR_OFF) + NUM_BARS * 8 + 16 + 1024;
+  static constexpr int OWN_OFF = BAR_OFF + (NUM_BARS * 8 + 16 + 15) / 16 * 16;
+  static constexpr size_t NEED = size_t(OWN_OFF) + kOwnItems * sizeof(Entry) + 1024;
   // so much that one block fits an SM: it takes all 512 columns of tensor memory
   static constexpr size_t SMEM = NEED > 200 * 1024 ? NEED : 200 * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory layout");
@@ -231,11 +292,12 @@ struct Item {
   int U;                   // tiles from kb0 to the last one
 };
 
-__device__ __forceinline__ Item make_item(const Params& p, const Entry* entries, int r) {
+// Item r of all, the block's n-th.
+__device__ __forceinline__ Item make_item(const Params& p, const Entry* entries, int r, int n) {
   Item it;
   const int e = r / p.kv_heads;
   it.kv = r - e * p.kv_heads;
-  const int4 v = *reinterpret_cast<const int4*>(entries + e);
+  const int4 v = *reinterpret_cast<const int4*>(entries + (p.own_list ? n : e));
   it.first = v.x;
   it.n = v.y;
   it.q0 = v.z;
@@ -258,15 +320,11 @@ __device__ __forceinline__ bool item_needs(const Item& it, int h, int j) {
   return h ? (j >= it.kb1 && j <= it.ke1) : (j >= it.kb0 && j <= it.ke0);
 }
 
-__device__ __forceinline__ int item_index(int n, int c, int G) {
-  return n * G + ((n & 1) ? G - 1 - c : c);
-}
-
 template <int DH>
 __global__ void __launch_bounds__(THREADS, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p, const int* count,
-                  const Entry* entries, int* status) {
+                  const Entry* entries0, int* status) {
   using L = Layout<DH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -319,12 +377,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();  // what the launches before wrote is there, the list too where one of them made it
+  Entry* const own = reinterpret_cast<Entry*>(smem + L::OWN_OFF);
+  const Entry* const entries = p.own_list ? own : entries0;
+  const int num_items =
+      (p.own_list ? list_own(p, own, int(warp), int(lane), status) : *count) * p.kv_heads;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();  // the list is written, and what the launches before it wrote
-  const int num_items = *count * p.kv_heads;
   const WaitCtl wc{abort_flag, status, kLimitNs};
   const uint64_t drain_ns = kLimitNs > kDrainFloorNs ? kLimitNs : kDrainFloorNs;
   const uint32_t sQ = smem_u32(smem);
@@ -345,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int n = 0; ok; ++n) {
           const int r = item_index(n, cta, G);
           if (r >= num_items) break;
-          const Item it = make_item(p, entries, r);
+          const Item it = make_item(p, entries, r, n);
           // the Q tiles of the previous item are free once its last S products completed
           if (!mbar_wait(q_empty, (n & 1) ^ 1, wc, 20)) break;
           mbar_arrive_expect_tx(q_full, q_bytes);
@@ -408,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int n = 0; ok; ++n) {
         const int r = item_index(n, cta, G);
         if (r >= num_items) break;
-        const Item it = make_item(p, entries, r);
+        const Item it = make_item(p, entries, r, n);
         if (!mbar_wait_warp(q_full, uint32_t(n) & 1, wc, 12)) break;
         for (int idx = 0; ok && idx < it.U; ++idx) {
           const uint32_t g = kc + uint32_t(idx), st = g % 3;
@@ -459,7 +520,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int n = 0; ok; ++n) {
         const int r = item_index(n, cta, G);
         if (r >= num_items) break;
-        const Item it = make_item(p, entries, r);
+        const Item it = make_item(p, entries, r, n);
         for (int idx = 0; ok && idx < it.U; ++idx) {
           const uint32_t g = vc + uint32_t(idx);
           const uint32_t v = uint32_t(dV) + (g & 1) * uint32_t(L::KV_BYTES >> 4);
@@ -508,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int n = 0; ok; ++n) {
         const int r = item_index(n, cta, G);
         if (r >= num_items) break;
-        const Item it = make_item(p, entries, r);
+        const Item it = make_item(p, entries, r, n);
         for (int idx = 0; idx < it.U; ++idx) {
           const uint32_t g = vc + uint32_t(idx);
           if (!mbar_wait_warp(v_full0 + 8 * (g & 1), (g >> 1) & 1, wc, 17)) {
@@ -556,7 +617,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int n = 0; ok; ++n) {
       const int ri = item_index(n, cta, G);
       if (ri >= num_items) break;
-      const Item it = make_item(p, entries, ri);
+      const Item it = make_item(p, entries, ri, n);
       const int qb = it.q0 + h * p.tile_tokens;
       const int i = qb + tok;  // place in the sequence
       const int kb_h = h ? it.kb1 : it.kb0, ke_h = h ? it.ke1 : it.ke0;
@@ -736,11 +797,16 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   if (e != cudaSuccess) return e;
   int* count = static_cast<int*>(scratch);
   Entry* entries = reinterpret_cast<Entry*>(static_cast<uint8_t*>(scratch) + kHeaderBytes);
-  e = launch_dependent(list_kernel, dim3(1), dim3(1024), 0, 1, stream, p, count, entries, status);
-  if (e != cudaSuccess) return e;
   const int64_t items = int64_t(p.capacity) * p.kv_heads;
+  // Few sequences and items: each block lists its own (LIST_FIGURES).
+  Params mine = p;
+  mine.own_list = p.sequences <= kOwnSequences && items <= int64_t(kOwnItems) * sms;
+  if (!mine.own_list) {
+    e = launch_dependent(list_kernel, dim3(1), dim3(1024), 0, 1, stream, p, count, entries, status);
+    if (e != cudaSuccess) return e;
+  }
   return launch_dependent(prompt_kernel<DH>, dim3(unsigned(items < sms ? items : sms)),
-                          dim3(THREADS), L::SMEM, 1, stream, tmQ, tmK, tmV, p,
+                          dim3(THREADS), L::SMEM, 1, stream, tmQ, tmK, tmV, mine,
                           static_cast<const int*>(count), static_cast<const Entry*>(entries), status);
 }
 

@@ -247,9 +247,22 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_cuda_ready = False
+
+
+def _device() -> int:
+    """The current device: ``torch.cuda.current_device()`` without its checks after the first call."""
+    global _cuda_ready
+    if _cuda_ready:
+        return torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
+    _cuda_ready = True
+    return dev
+
+
 def _stream(stream):
     if stream is None:  # the raw handle: no Stream object for every call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -633,7 +646,7 @@ def wait_probe(limit_ns: int, status: torch.Tensor, stream=None):
 
 def _here(*tensors):
     """Every given tensor is a CUDA tensor on the current device."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
@@ -982,7 +995,7 @@ def prompt_attention(q, k, v, starts=None, window=None, scale=None, out=None, sc
     tokens, _, d = q.shape
     n = 1 if starts is None else _sequences(starts)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if scratch is None:
         scratch = torch.empty(prompt_attention_scratch_bytes(tokens, n), dtype=torch.uint8,
                               device=q.device)
@@ -1007,7 +1020,7 @@ assert struct.calcsize(_CACHE_ATTENTION_FORMAT) == ctypes.sizeof(pb_cache_attent
 
 def _ints(t, n: int, what: str):
     """A contiguous int32 [n]; returns its address."""
-    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 [{n}]")
     return t.data_ptr()
 
@@ -1045,6 +1058,9 @@ class Cache:
         self.attention_scratch_bytes = self._bytes("pb_cache_attention_scratch_bytes")
         # of the calls that change the cache, which run one after another
         self.scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=k.device)
+        self._scratch = self.scratch.data_ptr()
+        self._made_on = _stream(None) if k.is_cuda else None
+        self._attention_scratch = None
 
     @classmethod
     def empty(cls, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, slots: int,
@@ -1074,7 +1090,7 @@ class Cache:
         _here(self.k, slots, starts)
         n = slots.numel()
         self._call("pb_cache_extend", n, _ints(slots, n, "slots"), _ints(starts, n + 1, "starts"),
-                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+                   self._scratch, self.scratch_bytes, stream=stream)
 
     def write(self, k, v, slots, starts, layer: int = 0, stream=None):
         """``pb_cache_write``: ``k`` and ``v`` of the sequences' last tokens, [tokens, kv_heads,
@@ -1099,7 +1115,7 @@ class Cache:
         _here(self.k, slots, starts, path, kept)
         n, tokens = slots.numel(), path.numel()
         self._call("pb_cache_keep", n, _ints(slots, n, "slots"), _ints(starts, n + 1, "starts"),
-                   tokens, _ints(path, tokens, "path"), _ints(kept, n, "kept"), _ptr(self.scratch),
+                   tokens, _ints(path, tokens, "path"), _ints(kept, n, "kept"), self._scratch,
                    self.scratch_bytes, stream=stream)
 
     def fork(self, src, dst, stream=None):
@@ -1107,14 +1123,14 @@ class Cache:
         _here(self.k, src, dst)
         n = dst.numel()
         self._call("pb_cache_fork", n, _ints(src, n, "src"), _ints(dst, n, "dst"),
-                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+                   self._scratch, self.scratch_bytes, stream=stream)
 
     def truncate(self, slots, lengths, stream=None):
         """``pb_cache_truncate``: sequences cut to ``lengths`` tokens (0 frees their slots)."""
         _here(self.k, slots, lengths)
         n = slots.numel()
         self._call("pb_cache_truncate", n, _ints(slots, n, "slots"), _ints(lengths, n, "lengths"),
-                   _ptr(self.scratch), self.scratch_bytes, stream=stream)
+                   self._scratch, self.scratch_bytes, stream=stream)
 
     def attention(self, q, slots, starts, parents=None, layer: int = 0, window=None, scale=None,
                   out=None, scratch=None, stream=None):
@@ -1122,16 +1138,25 @@ class Cache:
         head_dim] (a bf16 view), over the cache. ``parents`` (int32 [tokens]): the new tokens of a
         sequence are a tree, parents[t] the number of the one that t follows, -1 for the token before
         them (None: each follows the one before). ``window`` and ``scale`` as in
-        ``prompt_attention``. ``scratch`` (a uint8 CUDA tensor of ``attention_scratch_bytes``) is
-        allocated unless given. Rows of ``out`` in no sequence stay as they are."""
+        ``prompt_attention``. ``scratch``: a uint8 CUDA tensor of ``attention_scratch_bytes`` (found
+        unless given). Rows of ``out`` in no sequence stay as they are."""
         if stream is not None:
             return _run_on(stream, self.attention, q, slots, starts, parents, layer, window, scale,
                            out, scratch)
         tokens, heads, d = q.shape
         if out is None:
-            out = q.new_empty(q.shape)
-        if scratch is None:  # in the values' type: new_empty is the quickest way to memory
-            scratch = self.k.new_empty(self.attention_scratch_bytes // 2)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if scratch is None:
+            # On the stream that the cache was made on, calls follow one another and may share a
+            # buffer; elsewhere, and in a captured graph, each has its own.
+            if self._made_on == _stream(None) and not torch._C._cuda_isCurrentStreamCapturing():
+                if self._attention_scratch is None:
+                    self._attention_scratch = torch.empty(
+                        self.attention_scratch_bytes, dtype=torch.uint8, device=self.k.device)
+                scratch = self._attention_scratch
+            else:
+                scratch = torch.empty(self.attention_scratch_bytes, dtype=torch.uint8,
+                                      device=self.k.device)
         _here(self.k, q, slots, starts, parents, out, scratch)
         n = slots.numel()
         args = _pack_cache_attention(
@@ -1141,8 +1166,7 @@ class Cache:
             _ints(starts, n + 1, "starts"),
             0 if parents is None else _ints(parents, tokens, "parents"))
         _check("pb_cache_attention", lib().pb_cache_attention(
-            self._plan, args, scratch.data_ptr(), scratch.numel() * scratch.element_size(),
-            _stream(None)))
+            self._plan, args, scratch.data_ptr(), scratch.numel(), _stream(None)))
         return out
 
 
