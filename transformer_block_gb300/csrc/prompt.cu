@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                              int64_t(it.kv * p.group + rr - tt * p.group) * p.out_hs + (lane & 3) * 8
                        : nullptr;
         }
-#pragma unroll
+#pragma unroll 1  // once an item: cold instructions cost more than the loop
         for (int ch = 0; ch < DH / 32; ++ch) {
           uint32_t u[32];
           tmem_ld32(t_o + uint32_t(ch * 32), u);
