@@ -407,16 +407,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int r = item_index(n, cta, G);
           if (r >= num_items) break;
           const Item it = make_item(p, entries, r, n);
-          // the Q tiles of the previous item are free once its last S products completed
-          if (!mbar_wait(q_empty, (n & 1) ^ 1, wc, 20)) break;
-          mbar_arrive_expect_tx(q_full, q_bytes);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int hb = 0; hb < DH / 64; ++hb)
-              tma_load_3d(sQ + h * L::Q_TILE + hb * BOX, &tmQ, q_full, hb * 64, it.kv * p.group,
-                          it.first + it.q0 + h * p.tile_tokens);
-          n_done = n + 1;
           auto load_k = [&](int idx) -> bool {
             const uint32_t g = kc + uint32_t(idx);
             const uint32_t st = g % 3, par = (g / 3) & 1;
@@ -444,7 +434,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             return true;
           };
           // K runs one tile ahead of V: S runs ahead of P V
-          ok = load_k(0);
+          ok = load_k(0);  // before Q: its stage is free sooner
+          // the Q tiles of the previous item are free once its last S products completed
+          if (!ok || !mbar_wait(q_empty, (n & 1) ^ 1, wc, 20)) break;
+          mbar_arrive_expect_tx(q_full, q_bytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int hb = 0; hb < DH / 64; ++hb)
+              tma_load_3d(sQ + h * L::Q_TILE + hb * BOX, &tmQ, q_full, hb * 64, it.kv * p.group,
+                          it.first + it.q0 + h * p.tile_tokens);
+          n_done = n + 1;
           for (int idx = 0; ok && idx < it.U; ++idx) {
             if (idx + 1 < it.U) ok = load_k(idx + 1);
             if (ok) ok = load_v(idx);
