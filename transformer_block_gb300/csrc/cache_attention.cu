@@ -41,18 +41,13 @@ constexpr int kMostTree = 64;  // a bit each
 constexpr int kMaxSms = 192;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-// A block of MB query rows: its warps, the keys of its tiles, blocks an SM.
+constexpr int THREADS = 128, BK = 64, kBlocksPerSm = 2;
+
+// A block of MB query rows.
 template <int MB>
 struct Shape {
-  static constexpr int MT = MB == 64 ? 2 : 1;  // groups of 16 rows of a warp
-  static constexpr int WARPS = MB == 64 ? 8 : 4;
-  static constexpr int BK = MB == 64 ? 128 : 64;
-  static constexpr int BLOCKS = MB == 64 ? 1 : 2;
-  static constexpr int THREADS = 32 * WARPS;
-  static constexpr int RW = MB / (16 * MT), KW = WARPS / RW;  // warps along rows, along keys
-  static constexpr int KPW = BK / KW;                         // keys of a tile a warp takes
-  // registers do not hold 32 rows' queries too: they are read again for every tile
-  static constexpr bool Q_SHARED = MB == 64;
+  static constexpr int RW = MB / 16, KW = 4 / RW;  // warps along rows, along keys
+  static constexpr int KPW = BK / KW;              // keys of a tile a warp takes
 };
 
 // Of one block, two pieces at most do not hold their whole item: the one that it begins with (the
@@ -125,7 +120,6 @@ __device__ __forceinline__ int end_of(const Params& p, const Seq& s, int b) {
 // Key tiles [from, to) that block of rows b needs: from the first of its first row.
 template <int MB>
 __device__ __forceinline__ int2 tiles_of(const Params& p, const Seq& s, int b) {
-  constexpr int BK = Shape<MB>::BK;
   const int from = s.base + (p.parents == nullptr && b > 0 ? b * MB / p.group : 0);
   return make_int2(max(0, from - p.window + 1) / BK, (end_of<MB>(p, s, b) + BK - 1) / BK);
 }
@@ -172,27 +166,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 template <int DH, int MB>
 struct Layout {
-  using T = Shape<MB>;
-  static constexpr int TILE = T::BK * DH * 2;  // of k or v
+  static constexpr int TILE = BK * DH * 2;  // of k or v
   static constexpr int STAGES = DH == 128 ? 3 : 6;
-  static constexpr int Q_OFF = STAGES * 2 * TILE;
-  static constexpr int RING_OFF = Q_OFF + (T::Q_SHARED ? MB * DH * 2 : 0);
-  static constexpr int ROW_OFF = RING_OFF + kRing * T::BK * 8;  // paths of the new tokens
+  static constexpr int RING_OFF = STAGES * 2 * TILE;
+  static constexpr int ROW_OFF = RING_OFF + kRing * BK * 8;  // paths of the new tokens
   static constexpr int SMEM = ROW_OFF + kMostTree * (8 + 4);
   static constexpr int PITCH = DH + 4;  // of the warps' parts
-  static_assert(STAGES + 1 < kRing && SMEM <= (T::BLOCKS == 1 ? 225 : 111) * 1024, "shared memory");
-  static_assert(STAGES * 2 * TILE >= T::KW * MB * (PITCH + 2) * 4, "merge buffer");
+  static_assert(STAGES + 1 < kRing && SMEM <= 111 * 1024, "shared memory");
+  static_assert(RING_OFF >= Shape<MB>::KW * MB * (PITCH + 2) * 4, "merge buffer");
 };
 
 template <int DH, int MB>
-__global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
-    attention_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const Params p) {
   using L = Layout<DH, MB>;
   using T = Shape<MB>;
   constexpr int S = L::STAGES, CH = DH / 8;  // 16-byte chunks of a row
-  constexpr int THREADS = T::THREADS, BK = T::BK, RW = T::RW, KW = T::KW, KPW = T::KPW, MT = T::MT;
+  constexpr int RW = T::RW, KW = T::KW, KPW = T::KPW;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int64_t sums[T::WARPS];
+  __shared__ int64_t sums[4];
   __shared__ int64_t found_tile;
   __shared__ Seq found;
   __shared__ int found_i, faulted;
@@ -262,7 +253,7 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
     if (faulted != 0) return;
     all = 0;
 #pragma unroll
-    for (int w = 0; w < T::WARPS; ++w) all += sums[w];
+    for (int w = 0; w < 4; ++w) all += sums[w];
     if (!share(all, &first)) return;
     for (int i0 = 0; i0 < p.n; i0 += THREADS) {
       const int i = i0 + tid;
@@ -279,7 +270,7 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
       if (lane == 31) sums[warp] = to;
       __syncthreads();
       int64_t at = before + to - x;
-      for (int w = 0; w < T::WARPS; ++w) {
+      for (int w = 0; w < 4; ++w) {
         at += w < warp ? sums[w] : 0;
         before += sums[w];
       }
@@ -389,8 +380,8 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
       const int at = tid + x * THREADS;
       if (at < S * BK) ring[at] = place(first_pages[x], at / BK, at % BK);
     }
-    // where the queries go on to registers, they pass through the last stage's place
-    constexpr uint32_t qs = T::Q_SHARED ? L::Q_OFF : (S - 1) * 2 * L::TILE;
+    // the queries pass through the last stage's place on to registers
+    constexpr uint32_t qs = (S - 1) * 2 * L::TILE;
 #pragma unroll
     for (int x = 0; x < QUERIES; ++x) {
       const int r = (tid + x * THREADS) / CH, ch = tid % CH;
@@ -419,24 +410,21 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
         depth[tid] = d;
       }
     }
-    auto load_q = [&](int mt, int ks, uint32_t (&a)[4]) {
-      // A: matrices (rows 0-7, k lo), (rows 8-15, k lo), (rows 0-7, k hi), (rows 8-15, k hi)
-      const int r = (rw * MT + mt) * 16 + (lane & 15), ch = ks * 2 + (lane >> 4);
-      ldsm4(s0 + qs + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), a);
-    };
-    uint32_t qf[T::Q_SHARED ? 1 : DH / 16][4];
-    if (!T::Q_SHARED) {
+    uint32_t qf[DH / 16][4];
 #pragma unroll
-      for (int ks = 0; ks < DH / 16; ++ks) load_q(0, ks, qf[T::Q_SHARED ? 0 : ks]);
+    for (int ks = 0; ks < DH / 16; ++ks) {
+      // A: matrices (rows 0-7, k lo), (rows 8-15, k lo), (rows 0-7, k hi), (rows 8-15, k hi)
+      const int r = rw * 16 + (lane & 15), ch = ks * 2 + (lane >> 4);
+      ldsm4(s0 + qs + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), qf[ks]);
     }
     __syncthreads();
-    // this lane's rows: keys before the new ones from lo on, of the new ones those up to hi (a line)
-    // or those in bits (a tree)
-    int lo[2 * MT], hi[2 * MT];
-    uint64_t bits[2 * MT];
+    // this lane's two rows: keys before the new ones from lo on, of the new ones those up to hi (a
+    // line) or those in bits (a tree)
+    int lo[2], hi[2];
+    uint64_t bits[2];
 #pragma unroll
-    for (int e = 0; e < 2 * MT; ++e) {
-      const int rr = row0 + rw * MT * 16 + (lane >> 2) + 8 * e;
+    for (int e = 0; e < 2; ++e) {
+      const int rr = row0 + rw * 16 + (lane >> 2) + 8 * e;
       lo[e] = INT_MAX;
       hi[e] = -1;
       bits[e] = 0;
@@ -452,15 +440,15 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
     const int all_hi = p.parents == nullptr ? sq.base + row0 / p.group : sq.base - 1;
     const int all_lo = max(0, sq.len - p.window);
 
-    float o[MT][DH / 8][4];
+    float o[DH / 8][4];
 #pragma unroll
-    for (int i = 0; i < MT * (DH / 8); ++i)
+    for (int i = 0; i < DH / 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i / (DH / 8)][i % (DH / 8)][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     // the maximum that the weights refer to (log2 units), and their sum
-    float mx[2 * MT], sum[2 * MT];
+    float mx[2], sum[2];
 #pragma unroll
-    for (int e = 0; e < 2 * MT; ++e) {
+    for (int e = 0; e < 2; ++e) {
       mx[e] = -INFINITY;
       sum[e] = 0.f;
     }
@@ -474,62 +462,43 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
         page_ahead = entry(i + S + 1, tid);
       }
       const uint32_t sk = s0 + uint32_t(i % S) * uint32_t(2 * L::TILE) + uint32_t(kw * KPW * DH * 2);
-      float s[MT][KPW / 8][4];
+      float s[KPW / 8][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < KPW / 8; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < KPW / 8; ++nt)
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < DH / 16; ++ks) {
-        uint32_t a[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if (T::Q_SHARED) {
-            load_q(mt, ks, a[mt]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[mt][e] = qf[T::Q_SHARED ? 0 : ks][e];
-          }
-        }
+      for (int ks = 0; ks < DH / 16; ++ks)
 #pragma unroll
         for (int nt = 0; nt < KPW / 16; ++nt) {
           uint32_t b[4];
           const int r = nt * 16 + k_row, ch = ks * 2 + k_chunk;
           ldsm4(sk + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), b);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(s[mt][2 * nt], a[mt], b[0], b[1]);
-            mma16816(s[mt][2 * nt + 1], a[mt], b[2], b[3]);
-          }
+          mma16816(s[2 * nt], qf[ks], b[0], b[1]);
+          mma16816(s[2 * nt + 1], qf[ks], b[2], b[3]);
         }
-      }
       const int k0 = (ta + i) * BK + kw * KPW;
       if (!(k0 + KPW - 1 <= all_hi && k0 >= all_lo)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < KPW / 8; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < KPW / 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = k0 + nt * 8 + (lane & 3) * 2 + (e & 1), w = 2 * mt + (e >> 1);
-              const int u = key - sq.base;
-              const bool see = (key >= lo[w] && key <= hi[w]) ||
-                               (u >= 0 && u < kMostTree && ((bits[w] >> u) & 1u));
-              if (!see) s[mt][nt][e] = -INFINITY;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int key = k0 + nt * 8 + (lane & 3) * 2 + (e & 1), w = e >> 1;
+            const int u = key - sq.base;
+            const bool see = (key >= lo[w] && key <= hi[w]) ||
+                             (u >= 0 && u < kMostTree && ((bits[w] >> u) & 1u));
+            if (!see) s[nt][e] = -INFINITY;
+          }
       }
       // As elsewhere: the reference moves only when a row's maximum grew by more than 2^8 (from
       // -inf, any finite one does), so O is seldom rescaled.
-      float ref[2 * MT], alpha[2 * MT];
+      float ref[2], alpha[2];
       bool moved = false;
 #pragma unroll
-      for (int w = 0; w < 2 * MT; ++w) {
-        float t = s[w / 2][0][2 * (w & 1)];
+      for (int w = 0; w < 2; ++w) {
+        float t = s[0][2 * w];
 #pragma unroll
-        for (int nt = 0; nt < KPW / 8; ++nt)
-          t = max3f(t, s[w / 2][nt][2 * (w & 1)], s[w / 2][nt][2 * (w & 1) + 1]);
+        for (int nt = 0; nt < KPW / 8; ++nt) t = max3f(t, s[nt][2 * w], s[nt][2 * w + 1]);
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * p.scale_log2;
         const bool grow = t > mx[w] + kRescaleThreshold;
@@ -540,46 +509,36 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
       }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int w = 0; w < 2 * MT; ++w) {
+        for (int w = 0; w < 2; ++w) {
           sum[w] *= alpha[w];
 #pragma unroll
           for (int j = 0; j < DH / 8; ++j) {
-            o[w / 2][j][2 * (w & 1)] *= alpha[w];
-            o[w / 2][j][2 * (w & 1) + 1] *= alpha[w];
+            o[j][2 * w] *= alpha[w];
+            o[j][2 * w + 1] *= alpha[w];
           }
         }
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < KPW / 8; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < KPW / 8; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int w = 2 * mt + (e >> 1);
-            s[mt][nt][e] = ex2_approx(fmaf(s[mt][nt][e], p.scale_log2, -ref[w]));
-            sum[w] += s[mt][nt][e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          s[nt][e] = ex2_approx(fmaf(s[nt][e], p.scale_log2, -ref[e >> 1]));
+          sum[e >> 1] += s[nt][e];
+        }
       const uint32_t sv = sk + L::TILE;
 #pragma unroll
       for (int kt = 0; kt < KPW / 16; ++kt) {
-        uint32_t a[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          a[mt][0] = pack_bf16x2(s[mt][2 * kt][0], s[mt][2 * kt][1]);
-          a[mt][1] = pack_bf16x2(s[mt][2 * kt][2], s[mt][2 * kt][3]);
-          a[mt][2] = pack_bf16x2(s[mt][2 * kt + 1][0], s[mt][2 * kt + 1][1]);
-          a[mt][3] = pack_bf16x2(s[mt][2 * kt + 1][2], s[mt][2 * kt + 1][3]);
-        }
+        const uint32_t a[4] = {pack_bf16x2(s[2 * kt][0], s[2 * kt][1]),
+                               pack_bf16x2(s[2 * kt][2], s[2 * kt][3]),
+                               pack_bf16x2(s[2 * kt + 1][0], s[2 * kt + 1][1]),
+                               pack_bf16x2(s[2 * kt + 1][2], s[2 * kt + 1][3])};
 #pragma unroll
         for (int j = 0; j < DH / 16; ++j) {
           uint32_t b[4];
           const int r = kt * 16 + v_row, ch = j * 2 + v_chunk;
           ldsm4_t(sv + uint32_t(r * DH * 2 + ((ch ^ (r & 7)) * 16)), b);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * j], a[mt], b[0], b[1]);
-            mma16816(o[mt][2 * j + 1], a[mt], b[2], b[3]);
-          }
+          mma16816(o[2 * j], a, b[0], b[1]);
+          mma16816(o[2 * j + 1], a, b[2], b[3]);
         }
       }
     }
@@ -592,15 +551,15 @@ __global__ void __launch_bounds__(Shape<MB>::THREADS, Shape<MB>::BLOCKS)
     float* parts = reinterpret_cast<float*>(smem);
     float2* stats = reinterpret_cast<float2*>(parts + KW * MB * PITCH);
 #pragma unroll
-    for (int w = 0; w < 2 * MT; ++w) {
-      const int at = kw * MB + rw * MT * 16 + (lane >> 2) + 8 * w;
+    for (int w = 0; w < 2; ++w) {
+      const int at = kw * MB + rw * 16 + (lane >> 2) + 8 * w;
       sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 1);
       sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], 2);
       if ((lane & 3) == 0) stats[at] = make_float2(mx[w], sum[w]);
 #pragma unroll
       for (int j = 0; j < DH / 8; ++j)
         *reinterpret_cast<float2*>(parts + at * PITCH + j * 8 + (lane & 3) * 2) =
-            make_float2(o[w / 2][j][2 * (w & 1)], o[w / 2][j][2 * (w & 1) + 1]);
+            make_float2(o[j][2 * w], o[j][2 * w + 1]);
     }
     __syncthreads();
     const bool begins = t_off == 0, ends = t_off + m == whole;
@@ -743,20 +702,13 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
   for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-constexpr size_t kPieceBytes = size_t(2 * kMaxSms) * 2 * sizeof(Piece);
-template <int MB>
-constexpr size_t part_rows() {
-  return size_t(kMaxSms) * Shape<MB>::BLOCKS * 2 * MB;
-}
-size_t scratch_need(int head_dim) {
-  static_assert(part_rows<64>() >= part_rows<32>() && part_rows<64>() >= part_rows<16>(), "rows");
-  return kPieceBytes + part_rows<64>() * (head_dim + 4) * 4;
-}
+constexpr size_t kMaxBlocks = size_t(kBlocksPerSm) * kMaxSms;
+constexpr size_t kPieceBytes = kMaxBlocks * 2 * sizeof(Piece);
+size_t scratch_need(int head_dim) { return kPieceBytes + kMaxBlocks * 2 * 64 * (head_dim + 4) * 4; }
 
 template <int DH, int MB>
 cudaError_t launch(const Params& p, cudaStream_t stream) {
   using L = Layout<DH, MB>;
-  using T = Shape<MB>;
   static PerDeviceInit setup;  // per device: the shared-memory opt-in, and the number of SMs
   int sms = 0;
   cudaError_t e = per_device_init(
@@ -770,8 +722,8 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
       },
       &sms);
   if (e != cudaSuccess) return e;
-  const unsigned grid = unsigned(T::BLOCKS * (sms < kMaxSms ? sms : kMaxSms));
-  e = launch_dependent(attention_kernel<DH, MB>, dim3(grid), dim3(T::THREADS), L::SMEM, 1, stream, p);
+  const unsigned grid = unsigned(kBlocksPerSm * (sms < kMaxSms ? sms : kMaxSms));
+  e = launch_dependent(attention_kernel<DH, MB>, dim3(grid), dim3(THREADS), L::SMEM, 1, stream, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(join_kernel<DH, MB>, dim3(grid, MB / 4), dim3(128), 0, 1, stream, p);
 }
