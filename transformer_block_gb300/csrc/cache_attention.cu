@@ -7,11 +7,13 @@
 // included) with d(t) - d(u) < w. Query head h reads key head h / g.
 //
 // For few query rows the work is reading k and v once: 4 dh bytes a key and key head for 4 dh g c
-// operations (g heads, c new tokens), so that up to about 64 rows (g c) a product by mma.sync keeps
-// up with memory. A block of 4 warps takes MB = 16, 32 or 64 rows (row r: head r mod g of token r / g)
-// of one key head, and tiles of 64 keys. With 64 rows each warp has 16 rows and all keys of a tile;
-// with 32 two warps, with 16 four warps share the rows and split the keys, each with a softmax of
-// its own, merged in shared memory at the end.
+// operations (g heads, c new tokens). A block of 4 warps takes MB = 16, 32 or 64 rows (row r: head r
+// mod g of token r / g) of one key head, and tiles of 64 keys, two blocks an SM; products by mma.sync,
+// whose rate (1024 multiplications a cycle and SM) a block of 64 rows would need 2/3 of at the rate
+// of memory. With 64 rows each warp has 16 rows and all keys of a tile; with 32 two warps, with 16 four
+// warps share the rows and split the keys, each with a softmax of its own, merged in shared memory at
+// the end. (64 rows as one block an SM of 8 or 16 warps and tiles of 128 keys: 61 to 70 us where this
+// takes 58.)
 //
 // Split. All tiles of all (sequence, key head, block of rows) form one line, of which every block
 // takes an equal share, whatever it cuts: one long sequence fills the GPU as well as many, and
@@ -24,6 +26,11 @@
 // row r at place c ^ (r mod 8), which ldmatrix reads without conflicts. Rows behind the sequence (a
 // last page's rest) arrive as zeros: what the pool holds there reaches nothing. Weights are rounded
 // to bf16 for the product with v; scores, maximum, sums and results are fp32.
+//
+// Measured (in a graph): 64 sequences of 500 to 8192 tokens, 32 heads over 8 of 128, 182 us (6.6 TB/s,
+// 99 % of a plain copy); one of 131072 tokens 86 us (6.2 TB/s); 8 sequences with 16 drafts each, 58 us
+// (3.6 TB/s: bound by latency inside the tiles and 6 us of start, cold instructions among it); one
+// token over 500, 4 heads of 64, 6.7 us: five accesses that depend on one another, twice a launch.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -728,6 +735,9 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   return launch_dependent(join_kernel<DH, MB>, dim3(grid, MB / 4), dim3(128), 0, 1, stream, p);
 }
 
+// The block that holds a sequence's rows, from 8 sequences of 2 to 16 thousand tokens, 8 key heads:
+// 16 rows 41.5 us by blocks of 16, 42.7 by 32; 32 rows 57 (16, the cache read twice), 45.9 (32), 54
+// (64); 36 rows 58.4 (32), 53.9 (64); 64 rows 68 (32), 58 (64).
 template <int DH>
 cudaError_t launch_rows(int64_t rows, const Params& p, cudaStream_t stream) {
   return rows <= 16   ? launch<DH, 16>(p, stream)

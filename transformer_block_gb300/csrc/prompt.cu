@@ -10,23 +10,38 @@
 // token, whatever g is, and a short prompt fills its rows with heads instead of padding.
 //
 // Items. An item is two such tiles that follow one another in a sequence (2 T tokens) and share
-// every key and value tile. How many items there are is known on the device only (starts): a first
-// launch lists them, longest first (by the first token's place in its sequence, counted into
-// buckets), and the main launch, one block an SM, deals the list out in rounds of alternating
-// direction. The second launch's set-up runs beside the first.
+// every key and value tile. How many items there are is known on the device only (starts). They are
+// dealt out longest first (by the first token's place in its sequence), in rounds of alternating
+// direction, to one block an SM. Up to 128 sequences every block finds its own items in that order by
+// itself; more are listed by a launch before (counted into buckets by length), beside which the main
+// launch sets up.
 //
-// Inside a block, as in swa.cu: warp 0 loads by TMA (K 3 stages, V 2), warp 1's first thread issues
-// the products in the order S0, S1, then O0 += P0 V, S0 of the next tile, O1 += P1 V, S1 of the next
-// tile; warp 2 folds the landings of V and of the next K into P0's barrier; two groups of four warps
-// take the softmax, a row a thread. P (bf16, as all attention of the library; its error averages
-// over the keys) lies over S in tensor memory. The softmax's maximum, its sum and O are fp32; O is
-// rescaled only where a maximum grows by more than 2^8. V comes as it is stored, [keys, head_dim]: the
-// product reads it as an MN-major operand, so no transposed copy is made.
+// Inside a block. Warp 0 loads by TMA (K 3 stages, V 2). Warp 1 issues S = Q K^T, warp 3 O += P V,
+// each product by one elected lane of the converged warp: issuing from one diverged lane, or all from
+// one warp, takes longer than the products (a step of 256 rows x 128 keys: 2048 cycles of products;
+// issued by one lane 3960 to 5500 cycles, by one warp 3080, by two 2870). Warp 2 waits for V. Two
+// groups of four warps take the softmax, a row a thread. Tensor memory (512 columns) holds
+//   S (128) | P0 (64) | P1 (64) | O0 (128) | O1 (128)
+// One S serves both row tiles in turn: it is free as soon as the softmax has it in registers, so the
+// next tile's scores are computed during this one's softmax. With an S of each tile's own, over which
+// its P is written, a tile's S, softmax and P V follow one another (3330 cycles a step). Steps of 64
+// keys with two S for each tile need twice the products' starts (16384 tokens: 2277 us, this form
+// 1365). P (bf16, as all attention of the library; its error averages over the keys) is handed over in
+// two halves. The softmax's maximum, its sum and O are fp32; O is rescaled only where a maximum grows by
+// more than 2^8. V comes as it is stored, [keys, head_dim]: the product reads it as an MN-major
+// operand, so no transposed copy is made.
 //
 // A key tile at a sequence's end holds rows of the next sequence, or of nothing. Their scores are
 // replaced, not added to; their values would still meet P = 0, and 0 x NaN is NaN, so warp 2 writes
 // zeros over those rows of V before the product reads them. Nothing of another sequence reaches a
 // result.
+//
+// Measured (in a graph): 16384 tokens, 32 heads over 8, 1365 us (1.61 PFLOP/s, 81 % of the library's
+// product rate; tensor pipe 67 % busy; called over and over the power limit makes it 1500); 15 prompts of
+// 1 to 2049 tokens, 8096 in all, the same heads, 93 us (890 TFLOP/s of the pairs that are seen); 4 x
+// 2048 tokens, 16 heads, window 512, 55 us; 128 tokens 6 us. What is left of the short ones is the start
+// and end of an item, about 6500 cycles: its first softmax and last P V have nothing beside them, and
+// its result leaves by plain stores.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -81,7 +96,8 @@ __device__ __forceinline__ int2 sequence(const Params& p, int s) {
   return make_int2(a, max(min(max(p.starts[s + 1], 0), p.tokens) - a, 0));
 }
 
-// Lists the pairs of all sequences, later ones of a sequence (more keys) first.
+// Lists the pairs of all sequences, later ones of a sequence (more keys) first. The order of equal
+// ones, which atomics decide, changes no result.
 __global__ void __launch_bounds__(1024) list_kernel(const Params p, int* count, Entry* entries,
                                                     int* status) {
   __shared__ int at[kBuckets];
@@ -798,7 +814,8 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   int* count = static_cast<int*>(scratch);
   Entry* entries = reinterpret_cast<Entry*>(static_cast<uint8_t*>(scratch) + kHeaderBytes);
   const int64_t items = int64_t(p.capacity) * p.kv_heads;
-  // Few sequences and items: each block lists its own (LIST_FIGURES).
+  // Few sequences and items: each block lists its own. With a launch for the list 128 tokens take 7.1
+  // us instead of 5.9, the ragged 8096 tokens 96 instead of 92.
   Params mine = p;
   mine.own_list = p.sequences <= kOwnSequences && items <= int64_t(kOwnItems) * sms;
   if (!mine.own_list) {
