@@ -671,8 +671,10 @@ pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t 
  * 3 a slot that is none or listed twice, 4 starts that fall or leave the call's tokens, or more
  * tokens than the sequence has, 5 a page or a length that is none, 6 a path that does not rise within
  * the new tokens, 7 kept tokens to be moved in a page that several sequences use. From then on calls
- * on the cache do nothing, until the caller writes 0 to status. Calls on one cache must not overlap
- * on the GPU, but for pb_cache_attention calls among themselves. */
+ * on the cache do nothing, until the caller writes 0 to status. Reason 3 for a slot listed twice comes
+ * from the four; pb_cache_attention takes one as two sequences, and pb_cache_write leaves the rows of
+ * either. Rows of out of a sequence with reason 5 for a page have no defined value. Calls on one cache
+ * must not overlap on the GPU, but for pb_cache_attention calls among themselves. */
 typedef struct pb_cache {
   int32_t layers;
   int32_t pages;     /* 2^20 at most */
@@ -706,7 +708,8 @@ pb_status pb_cache_extend(const pb_cache* cache, int32_t n, const int32_t* slots
 /* Writes k and v of the last starts[i + 1] - starts[i] tokens of every sequence (those that
  * pb_cache_extend made room for), into `layers` layers from `layer` on. k, v: bf16 views [layers,
  * tokens, kv_heads, head_dim] (batch_stride is the layers' stride). Rows in no sequence are not
- * used. */
+ * used. Where sequences share the page of such a token (a fork after the extension) it is written for
+ * all of them. */
 pb_status pb_cache_write(const pb_cache* cache, int32_t layer, int32_t layers, int32_t n,
                          const int32_t* slots, const int32_t* starts, int32_t tokens,
                          const pb_heads* k, const pb_heads* v, void* stream);

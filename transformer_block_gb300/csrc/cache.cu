@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(256, 4) write_kernel(const Cache c, int layer0
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t units = int64_t(tokens) * layers;
-  if (*reinterpret_cast<volatile int*>(c.status) != 0) return;
+  // the warp as a whole: another may record a fault meanwhile
+  if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(c.status) != 0)) return;
   for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units;
        u += int64_t(gridDim.x) * 8) {
     int layer;

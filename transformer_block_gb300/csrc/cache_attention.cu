@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
 
   // -------------------------------------------------------------- the block's share of the line
   int status = 0;
-  if (lane == 0) status = *reinterpret_cast<volatile int*>(p.status);
+  if (tid == 0) status = *reinterpret_cast<volatile int*>(p.status);
   Seq sq{};             // the sequence at which the share begins
   int seq_i = 0;        // its place in the list
   int64_t found_at = 0; // tiles before the share's first in it
@@ -236,7 +236,6 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
       x = head_tiles<MB>(p, sq) * p.kv_heads;
     }
     const int64_t to = scan(x);
-    if (__shfl_sync(0xffffffffu, status, 0) != 0) return;
     if (!share(__shfl_sync(0xffffffffu, to, 31), &first)) return;
     seq_i = __ffs(int(__ballot_sync(0xffffffffu, first < to))) - 1;
     found_at = first - __shfl_sync(0xffffffffu, to - x, seq_i);
@@ -255,9 +254,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
       all += head_tiles<MB>(p, sequence(p, i, blockIdx.x == 0)) * p.kv_heads;
     all = scan(all + own);
     if (lane == 31) sums[warp] = all;
-    if (tid == 0) faulted = status;
     __syncthreads();
-    if (faulted != 0) return;
     all = 0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) all += sums[w];
@@ -293,6 +290,10 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     sq = found;
     found_at = found_tile;
   }
+  // A fault may be recorded while the block's warps read the word: one thread's reading counts for
+  // all, and is looked at behind the first barrier that the block comes to anyway. What is read before
+  // lies within the tables and tensors, whatever they hold.
+  if (tid == 0) faulted = status;
   int kv, blk = 0, t_off;
   {
     const int64_t per = head_tiles<MB>(p, sq);
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(THREADS, kBlocksPerSm) attention_kernel(const 
     int parent = -1;
     if (p.parents != nullptr && tid < sq.count) parent = p.parents[sq.first + tid];
     __syncthreads();  // the piece before is done with shared memory
+    if (faulted != 0) return;
 #pragma unroll
     for (int x = 0; x < PLACES; ++x) {
       const int at = tid + x * THREADS;
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
     if (head.state == kNone || head.row0 + r >= head.rows) return;
     const uint32_t m = __ballot_sync(0xffffffffu, state != kGoesOn);
     if (m != 0) {
-      // no end: a block left out its share, since a fault was recorded meanwhile
+      // no end: a block left out its share, since a fault was recorded before it looked
       if (__shfl_sync(0xffffffffu, state, __ffs(int(m)) - 1) != kEnds) return;
       pieces += __ffs(int(m));
       break;
