@@ -635,7 +635,8 @@ pb_status pb_activation_backward(int64_t rows, int64_t cols, int32_t dtype, int3
  * rounded once. Rows of out in no sequence are left as they were, and what q, k and v hold there, or
  * in another sequence, reaches no result. Within a sequence a v that is not finite makes results of
  * earlier tokens NaN too (those that share a tile of 128 keys with it). A start outside [0, tokens] is
- * moved to the nearest end; starts that fall give some rows of out no defined value.
+ * moved to the nearest end. Where starts fall the call does nothing and records PB_ERR_INVALID_ARG in
+ * *status.
  * head_dim 64 or 128. Strides of q, k and v of dimensions beyond 1: head_dim at least, below 2^38.
  * out overlaps nothing else. tokens or sequences 0 does nothing. */
 typedef struct pb_prompt_args {

@@ -62,6 +62,28 @@ def test_falling_starts_stay_inside(n):
     assert bool((scratch[nbytes:] == 77).all())
 
 
+@pytest.mark.parametrize("n,t,group", [(128, 300, 2), (2 ** 20, 8192, 128)])
+def test_falling_starts_do_nothing(n, t, group):
+    # the second: more than 2^31 pairs of tiles, were they taken one by one
+    q, k, v = pa.randn(1, t, group, 64), pa.randn(2, t, 1, 64), pa.randn(3, t, 1, 64)
+    st = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    st[1::2] = t
+    out = torch.full_like(q, 3.0)
+    nbytes = pb.prompt_attention_scratch_bytes(t, n)
+    scratch = torch.full((4096 + nbytes + 4096,), 77, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pb.prompt_attention(q, k, v, st, out=out, scratch=scratch[4096:-4096], status=status)
+    assert status.item() == 1
+    assert bool((out == 3).all())
+    assert bool((scratch[:4096] == 77).all()) and bool((scratch[-4096:] == 77).all())
+    # and the same scratch serves a sound call
+    st[:] = t
+    st[0] = 0
+    pb.prompt_attention(q[:300], k[:300], v[:300], st[:2].clamp(max=300), out=out[:300],
+                        scratch=scratch[4096:-4096])
+    pa.check(out[:300], q[:300], k[:300], v[:300], [0, 300])
+
+
 @pytest.mark.parametrize("n", [8, 40])
 def test_faults_while_blocks_begin(n):
     # a fault is recorded while blocks of the same call look at the status word: each goes on as a whole

@@ -83,13 +83,18 @@ struct Params {
   int window;  // at least 1
   float scale_log2;
   int shift;      // bucket = pair index >> shift
-  int capacity;   // entries that scratch holds
+  int capacity;   // the most pairs that sequences of so many tokens have: entries in scratch
   bool own_list;  // blocks list their items themselves
   const int* starts;  // or null: one sequence
   __nv_bfloat16* out;
   int64_t out_ss, out_hs;
 };
 
+// Whether sequence s ends before it begins. Where starts fall, sequences may overlap, and there is no
+// bound on their pairs: such a call does nothing.
+__device__ __forceinline__ bool falls(const Params& p, int s) {
+  return p.starts != nullptr && p.starts[s + 1] < p.starts[s];
+}
 __device__ __forceinline__ int2 sequence(const Params& p, int s) {
   if (p.starts == nullptr) return make_int2(0, p.tokens);
   const int a = min(max(p.starts[s], 0), p.tokens);
@@ -106,7 +111,15 @@ __global__ void __launch_bounds__(1024) list_kernel(const Params p, int* count, 
   pdl_wait();
   pdl_trigger();
   for (int b = tid; b < kBuckets; b += 1024) at[b] = 0;
-  __syncthreads();
+  bool fall = false;
+  for (int s = tid; s < p.sequences; s += 1024) fall |= falls(p, s);
+  if (__syncthreads_or(fall)) {
+    if (tid == 0) {
+      *count = 0;
+      if (status != nullptr) atomicCAS(status, 0, int(PB_ERR_INVALID_ARG));
+    }
+    return;
+  }
   const int pair_tokens = 2 * p.tile_tokens;
   for (int s = warp; s < p.sequences; s += 32) {
     const int pairs = (sequence(p, s).y + pair_tokens - 1) / pair_tokens;
@@ -129,18 +142,14 @@ __global__ void __launch_bounds__(1024) list_kernel(const Params p, int* count, 
   x += before;
   at[b1] = x - n1 - n0;
   at[b0] = x - n0;
-  if (tid == 1023) {
-    *count = min(x, p.capacity);
-    // falling starts: sequences that overlap, more pairs than tokens allow
-    if (x > p.capacity && status != nullptr) atomicCAS(status, 0, int(PB_ERR_INVALID_ARG));
-  }
+  if (tid == 1023) *count = x;
   __syncthreads();
   for (int s = warp; s < p.sequences; s += 32) {
     const int2 q = sequence(p, s);
     const int pairs = (q.y + pair_tokens - 1) / pair_tokens;
     for (int i = lane; i < pairs; i += 32) {
       const int e = atomicAdd(&at[i >> p.shift], 1);
-      if (e < p.capacity) entries[e] = Entry{q.x, q.y, i * pair_tokens, 0};
+      entries[e] = Entry{q.x, q.y, i * pair_tokens, 0};
     }
   }
 }
@@ -241,17 +250,19 @@ __device__ __forceinline__ int list_own(const Params& p, Entry* own, int warp, i
   const int pair_tokens = 2 * p.tile_tokens;
   int2 q[PER];
   int pairs[PER], all = 0, most = 0;
+  bool fall = false;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     q[k] = lane + 32 * k < p.sequences ? sequence(p, lane + 32 * k) : make_int2(0, 0);
+    fall |= lane + 32 * k < p.sequences && falls(p, lane + 32 * k);
     pairs[k] = (q[k].y + pair_tokens - 1) / pair_tokens;
     all += pairs[k];
     most = max(most, pairs[k]);
   }
   all = __reduce_add_sync(0xffffffffu, all);
-  if (all > p.capacity) {  // falling starts: sequences that overlap, more pairs than tokens allow
+  if (__any_sync(0xffffffffu, fall)) {
     if (lane == 0 && status != nullptr) atomicCAS(status, 0, int(PB_ERR_INVALID_ARG));
-    all = p.capacity;
+    return 0;
   }
   most = __reduce_max_sync(0xffffffffu, most);
   const int items = all * p.kv_heads, G = int(gridDim.x);
