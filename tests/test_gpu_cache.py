@@ -229,6 +229,26 @@ def test_fork_onto_its_own_sources():
         m.check(c)
 
 
+def test_keep_beside_a_shared_page():
+    # pages of 16: tokens 20 to 31 share a page with the fork and stay where they are, those behind move
+    c, m = make()
+    counts = [45]
+    st = ints(starts_of(counts))
+    k, v = (torch.randn(2, 45, 3, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    c.extend(ints([0]), st)
+    m.extend([0], counts)
+    c.write(k, v, ints([0]), st)
+    m.write([0], counts, k.cpu(), v.cpu())
+    c.fork(ints([0]), ints([1]))
+    m.fork([0], [1])
+    c.truncate(ints([1]), ints([32]))
+    m.truncate([1], [32])
+    path = list(range(12)) + [13, 17, 24]
+    c.keep(ints([0]), ints([0, 25]), ints(path + [0] * 10), ints([15]))
+    m.keep([0], [25], [path])
+    m.check(c)
+
+
 def test_layers_apart_and_views():
     c, m = make(layers=3, heads=4)
     counts = [17, 3]

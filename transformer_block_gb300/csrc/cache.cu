@@ -477,17 +477,19 @@ __global__ void __launch_bounds__(BLOCK) keep_kernel(const Cache c, int n, const
       [&](int, const Job& job) {
         const int* row = c.table + int64_t(job.slot) * c.slot_pages;
         check_pages(c, sh, job.slot, job.a / c.page_size, pages_of(c, job.len));
-        bool rises = true, moved = false;
+        bool rises = true;
+        int moved = job.c;  // the first that moves: all behind it do
         for (int j = lane; j < job.c; j += LANES) {
           const int at = path[job.d + j], before = j > 0 ? path[job.d + j - 1] : -1;
           rises &= at > before && at < job.b;
-          moved |= at != j;
+          if (at != j) moved = min(moved, j);
         }
         if (!rises) set_fault(sh, kFaultPath);
         // the lanes of this sequence among the warp's that are here
-        const uint32_t group = 0xffffu << (threadIdx.x & 16);
-        if (__any_sync(group, moved))
-          for (int q = job.a / c.page_size + lane; q < pages_of(c, job.a + job.c); q += LANES)
+        moved = __reduce_min_sync(0xffffu << (threadIdx.x & 16), moved);
+        if (moved < job.c)
+          for (int q = (job.a + moved) / c.page_size + lane; q < pages_of(c, job.a + job.c);
+               q += LANES)
             if (good_page(c, row[q]) && c.refs[row[q]] != 1) set_fault(sh, kFaultShared);
       });
   if (!decide(c, sh, 0)) return;
