@@ -644,7 +644,7 @@ typedef struct pb_prompt_args {
   int32_t sequences;
   int32_t head_dim;
   int32_t window; /* 0: all earlier tokens */
-  float scale;    /* 0: 1 / sqrt(head_dim) */
+  float scale;    /* 0: 1 / sqrt(head_dim); 2^127 at most */
   pb_heads q;
   pb_heads k;
   pb_heads v;
@@ -752,7 +752,7 @@ typedef struct pb_cache_attention_args {
   int32_t sequences;
   int32_t tokens;
   int32_t window; /* 0: all */
-  float scale;    /* 0: 1 / sqrt(head_dim) */
+  float scale;    /* 0: 1 / sqrt(head_dim); 2^127 at most */
   pb_heads q;
   pb_heads out;
   const int32_t* slots;

@@ -43,7 +43,7 @@ def prompt(lib, scratch=P + 64 * MB, nbytes=None, status=None, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(tokens=-1), 1), (dict(sequences=-1), 1), (dict(head_dim=96), 2), (dict(head_dim=256), 2),
     (dict(window=-1), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
-    (dict(scale=float("inf")), 1), (dict(tokens=2 ** 31 - 1000, nbytes=2 ** 60), 2),
+    (dict(scale=float("inf")), 1), (dict(scale=3e38), 1), (dict(tokens=2 ** 31 - 1000, nbytes=2 ** 60), 2),
     (dict(sequences=2 ** 24 + 1, nbytes=2 ** 60), 2), (dict(starts=None), 1),
     (dict(starts=P + 4 * MB + 2), 1), (dict(q=heads(None, 8)), 1), (dict(k=heads(P + MB + 8, 2)), 1),
     (dict(v=heads(P + 2 * MB, 2, stride=260)), 1), (dict(v=heads(P + 2 * MB, 2, stride=-256)), 1),
@@ -249,6 +249,10 @@ def test_binding_refuses():
             pb._window(bad)
         with pytest.raises(ValueError):
             pb._scale(bad)
+    for bad in (float("nan"), float("inf"), 2.0 ** -127, 1e-300, 2.0 ** 127.5):
+        with pytest.raises(ValueError):
+            pb._scale(bad)
+    assert pb._scale(None) == 0 and pb._scale(2.0 ** -126) > 0
     assert pb._window(None) == 0 and pb._window(2 ** 40) == 2 ** 31 - 1
     i32 = dict(dtype=torch.int32)
     k = torch.zeros(1, 4, 2, 16, 64, dtype=torch.bfloat16)

@@ -776,8 +776,8 @@ pb_status pb_cache_attention(const pb_cache* cache, const pb_cache_attention_arg
   if (a.tokens < 0 || a.tokens > (1 << 30))
     return record_error(PB_ERR_INVALID_ARG, "tokens must be between 0 and 2^30");
   if (a.window < 0) return record_error(PB_ERR_INVALID_ARG, "window must be >= 0");
-  if (!(a.scale >= 0.f && std::isfinite(a.scale)))
-    return record_error(PB_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (!(a.scale >= 0.f && a.scale <= 0x1p127f))  // log2(e) times it is finite
+    return record_error(PB_ERR_INVALID_ARG, "scale must be between 0 and 2^127");
   if (a.sequences == 0 || a.tokens == 0) return PB_OK;
   s = check_view(&a.q, "q", 1, a.tokens, c.head_dim, false);
   if (s == PB_OK) s = check_view(&a.out, "out", 1, a.tokens, c.head_dim, true);

@@ -862,8 +862,8 @@ pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t 
   if (a.head_dim != 64 && a.head_dim != 128)
     return record_error(PB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   if (a.window < 0) return record_error(PB_ERR_INVALID_ARG, "window must be >= 0");
-  if (!(a.scale >= 0.f && std::isfinite(a.scale)))
-    return record_error(PB_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (!(a.scale >= 0.f && a.scale <= 0x1p127f))  // log2(e) times it is finite
+    return record_error(PB_ERR_INVALID_ARG, "scale must be between 0 and 2^127");
   if (a.tokens > 0x7fffffff - 1024)  // tiles end up to 256 rows behind the last token
     return record_error(PB_ERR_UNSUPPORTED, "more than 2^31 - 1025 tokens");
   if (a.sequences > (1 << 24))

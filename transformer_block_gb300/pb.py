@@ -978,7 +978,9 @@ def _window(window) -> int:
 
 
 def _scale(scale) -> float:
-    _is(scale is None or scale > 0, "scale must be positive, or None")
+    # below 2^-126 it may become 0 in 32 bits, which stands for None
+    _is(scale is None or 2.0 ** -126 <= scale <= 2.0 ** 127,
+        "scale must be between 2^-126 and 2^127, or None")
     return 0.0 if scale is None else float(scale)
 
 
