@@ -234,6 +234,32 @@ def test_several_host_threads():
     assert not errors, errors
 
 
+def test_host_threads_on_one_stream():
+    # two launches a call: those of two threads may come in any order on the stream
+    c, data = ca.fill([9000, 70, 4555], 4, 128, 32)
+    sl, st = ints([0, 1, 2]), ints([0, 1, 2, 3])
+    qs = [ca.randn(i, 3, 16, 128) for i in range(4)]
+    want = [c.attention(q, sl, st).clone() for q in qs]
+    torch.cuda.synchronize()
+    wrong, done = [], []
+
+    def work(i):
+        torch.cuda.set_device(0)
+        for _ in range(20):
+            outs = [c.attention(qs[i], sl, st) for _ in range(50)]
+            wrong.extend(i for o in outs if not torch.equal(o, want[i]))
+        done.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(1, 4)]
+    for t in threads:
+        t.start()
+    work(0)
+    for t in threads:
+        t.join()
+    assert not wrong and len(done) == 4
+    assert c.fault() == 0
+
+
 def test_first_calls_inside_a_capture_and_two_graphs():
     # every kind of call captured; two graphs of one cache's attention replayed at once
     c, data = ca.fill([3000, 70, 555], 4, 128, 32)

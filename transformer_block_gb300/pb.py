@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 import torch
 
@@ -1034,7 +1035,8 @@ class Cache:
     ``Cache.empty`` makes them. ``slots`` in a call is an int32 tensor of different sequences, and
     ``starts`` an int32 [len(slots) + 1]: sequence i has the rows starts[i] to starts[i + 1] of the
     call's tensors. What is wrong in them shows in ``status`` when the call runs (see
-    ``pb_cache``): ``fault()`` reads it. Calls on one cache run one after another."""
+    ``pb_cache``): ``fault()`` reads it. Calls on one cache run one after another, and a cache lives
+    until they have run."""
 
     def __init__(self, k, v, table, lengths, refs, status=None):
         _is(k.dim() == 5 and v.shape == k.shape, "k and v must be [layers, pages, kv_heads, "
@@ -1062,6 +1064,7 @@ class Cache:
         self.scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=k.device)
         self._scratch = self.scratch.data_ptr()
         self._made_on = _stream(None) if k.is_cuda else None
+        self._made_by = threading.get_ident()
         self._attention_scratch = None
 
     @classmethod
@@ -1149,9 +1152,10 @@ class Cache:
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if scratch is None:
-            # On the stream that the cache was made on, calls follow one another and may share a
-            # buffer; elsewhere, and in a captured graph, each has its own.
-            if self._made_on == _stream(None) and not torch._C._cuda_isCurrentStreamCapturing():
+            # On the stream and the host thread that the cache was made on, calls follow one another
+            # and may share a buffer; elsewhere, and in a captured graph, each has its own.
+            if self._made_on == _stream(None) and self._made_by == threading.get_ident() \
+                    and not torch._C._cuda_isCurrentStreamCapturing():
                 if self._attention_scratch is None:
                     self._attention_scratch = torch.empty(
                         self.attention_scratch_bytes, dtype=torch.uint8, device=self.k.device)
