@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(FewGeo<NT, KN, NARROW>::THREADS, 1)
       }
       // The stage's reads are done, not only issued, when the producer may load over it: without the
       // fence a warp's last reads could meet the next tile's values while other work keeps the SM
-      // busy (three of a thousand calls of 32 rows, beside three other streams; no cost).
+      // busy (one in a thousand products of 32 rows was off beside three other streams; no cost).
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8 * stage);
