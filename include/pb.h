@@ -654,7 +654,8 @@ typedef struct pb_prompt_args {
 
 /* `scratch` (device, 256-byte aligned, >= pb_prompt_attention_scratch_bytes of the call's tokens
  * and sequences) needs no preparation and must not be used by another call that may run
- * concurrently. `status` as in pb_gemm_bf16. */
+ * concurrently, or that another host thread enqueues at the same time (a call may be two launches,
+ * here and in pb_cache_attention). `status` as in pb_gemm_bf16. */
 pb_status pb_prompt_attention_scratch_bytes(int32_t tokens, int32_t sequences, size_t* bytes);
 pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t scratch_bytes,
                               int* status, void* stream);
@@ -675,7 +676,11 @@ pb_status pb_prompt_attention(const pb_prompt_args* args, void* scratch, size_t 
  * on the cache do nothing, until the caller writes 0 to status. Reason 3 for a slot listed twice comes
  * from the four; pb_cache_attention takes one as two sequences, and pb_cache_write leaves the rows of
  * either. Rows of out of a sequence with reason 5 for a page have no defined value. Calls on one cache
- * must not overlap on the GPU, but for pb_cache_attention calls among themselves. */
+ * must not overlap on the GPU, but for pb_cache_attention calls among themselves. Nor may a host thread
+ * be in a call that changes a cache while another is in one, on the same stream either: extend, keep
+ * and fork are several launches that hand one another lists in scratch, and a call whose launches
+ * come between them puts its own lists there (rows are then not copied or moved, or a path is read
+ * behind its end). The caller takes a lock around such calls. */
 typedef struct pb_cache {
   int32_t layers;
   int32_t pages;     /* 2^20 at most */
@@ -695,7 +700,8 @@ typedef struct pb_cache {
 /* The calls below take n sequences, slots[n] (device int32, all different; n <= cache->slots), and
  * for their new tokens starts[n + 1] (device int32): sequence i has the rows starts[i] <= t <
  * starts[i + 1] of the call's tensors. `scratch` (device, 256-byte aligned, >= the bytes given here)
- * needs no preparation and must not be used by another call that may run concurrently. */
+ * needs no preparation and must not be used by another call that may run concurrently, or that
+ * another host thread enqueues at the same time. */
 pb_status pb_cache_scratch_bytes(const pb_cache* cache, size_t* bytes);
 
 /* Room for starts[i + 1] - starts[i] more tokens of every sequence, whose lengths grow by them: the

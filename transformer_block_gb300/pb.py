@@ -1036,7 +1036,8 @@ class Cache:
     ``starts`` an int32 [len(slots) + 1]: sequence i has the rows starts[i] to starts[i + 1] of the
     call's tensors. What is wrong in them shows in ``status`` when the call runs (see
     ``pb_cache``): ``fault()`` reads it. Calls on one cache run one after another, and a cache lives
-    until they have run."""
+    until they have run. Several host threads may change one cache on one stream through the same
+    ``Cache`` (through two of the same tensors only one after the other)."""
 
     def __init__(self, k, v, table, lengths, refs, status=None):
         _is(k.dim() == 5 and v.shape == k.shape, "k and v must be [layers, pages, kv_heads, "
@@ -1063,6 +1064,7 @@ class Cache:
         # of the calls that change the cache, which run one after another
         self.scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=k.device)
         self._scratch = self.scratch.data_ptr()
+        self._changing = threading.Lock()
         self._made_on = _stream(None) if k.is_cuda else None
         self._made_by = threading.get_ident()
         self._attention_scratch = None
@@ -1084,7 +1086,12 @@ class Cache:
         return n.value
 
     def _call(self, name: str, *args, stream=None):
-        _check(name, getattr(lib(), name)(self._plan, *args, _stream(stream)))
+        # extend, keep and fork are several launches that hand one another lists in the scratch:
+        # between them no other host thread's call (ctypes gives up the interpreter's lock)
+        call = getattr(lib(), name)
+        with self._changing:
+            status = call(self._plan, *args, _stream(stream))
+        _check(name, status)
 
     def fault(self) -> int:
         """0, or what a call recorded: ``PB_ERR_CACHE`` + 256 x the reason. Waits for the GPU."""
