@@ -633,10 +633,13 @@ pb_status pb_activation_backward(int64_t rows, int64_t cols, int32_t dtype, int3
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j.
  * Scores, softmax and sums in fp32, its weights rounded to bf16 for the product with v, out
  * rounded once. Rows of out in no sequence are left as they were, and what q, k and v hold there, or
- * in another sequence, reaches no result. Within a sequence a v that is not finite makes results of
- * earlier tokens NaN too (those that share a tile of 128 keys with it). A start outside [0, tokens] is
- * moved to the nearest end. Where starts fall the call does nothing and records PB_ERR_INVALID_ARG in
- * *status.
+ * in another sequence, reaches no result. Within a sequence a v that is not finite may make results of
+ * tokens NaN that do not see it: 128 / (q.heads / k.heads) tokens (rounded down) are computed together,
+ * and where one of them sees a key of the value's 128 (both counted from the sequence's first token),
+ * the weights of 0 of the others meet it too. So it reaches earlier tokens, and with a window later
+ * ones that have left it behind. A k that is not finite reaches the tokens that see it. A start outside
+ * [0, tokens] is moved to the nearest end. Where starts fall the call does nothing and records
+ * PB_ERR_INVALID_ARG in *status.
  * head_dim 64 or 128. Strides of q, k and v of dimensions beyond 1: head_dim at least, below 2^38.
  * out overlaps nothing else. tokens or sequences 0 does nothing. */
 typedef struct pb_prompt_args {
@@ -750,8 +753,9 @@ pb_status pb_cache_truncate(const pb_cache* cache, int32_t n, const int32_t* slo
  * Places count along the path: of those a token sees the last `window` (0: all). Query heads and key
  * heads, scale, and the roundings as in pb_prompt_attention. Rows of out in no sequence are left as
  * they were; rows of the cache behind a sequence reach no result. Within a sequence a v that is
- * not finite may make results of tokens NaN that do not see it, by a tile of 64 keys. Any number of
- * new tokens, without parents; from about 64 / (q heads / kv_heads) on a sequence's cache is read
+ * not finite may make results of tokens NaN that do not see it: a tile of 64 keys is read for up to 64
+ * rows (new tokens x heads) together. A k that is not finite reaches the tokens that see it. Any number
+ * of new tokens, without parents; from about 64 / (q heads / kv_heads) on a sequence's cache is read
  * several times. */
 typedef struct pb_cache_attention_args {
   int32_t layer;
