@@ -992,7 +992,10 @@ def prompt_attention(q, k, v, starts=None, window=None, scale=None, out=None, sc
     the first token of each sequence and the end of the last (None: one sequence). A token sees
     ``window`` tokens, itself included (None: all before it); ``scale`` is 1 / sqrt(head_dim) unless
     given. Rows of ``out`` in no sequence stay as they are: give ``out`` where there are such rows
-    (a new one holds anything there)."""
+    (a new one holds anything there). ``starts`` that fall are found when the call runs: it then
+    leaves all of ``out`` as it is (a new one holds anything) and records ``PB_ERR_INVALID_ARG`` (1)
+    in ``status``, an int32 [1] CUDA tensor that is zero before and is read when it suits the caller,
+    as ``Cache.fault()`` is; without ``status`` nothing tells."""
     if stream is not None:
         return _run_on(stream, prompt_attention, q, k, v, starts, window, scale, out, scratch, status)
     tokens, _, d = q.shape
@@ -1151,7 +1154,8 @@ class Cache:
         sequence are a tree, parents[t] the number of the one that t follows, -1 for the token before
         them (None: each follows the one before). ``window`` and ``scale`` as in
         ``prompt_attention``. ``scratch``: a uint8 CUDA tensor of ``attention_scratch_bytes`` (found
-        unless given). Rows of ``out`` in no sequence stay as they are."""
+        unless given). Rows of ``out`` in no sequence stay as they are, and any rows where
+        ``fault()`` is not 0 (a new ``out`` holds anything there)."""
         if stream is not None:
             return _run_on(stream, self.attention, q, slots, starts, parents, layer, window, scale,
                            out, scratch)
