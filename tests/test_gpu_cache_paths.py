@@ -38,14 +38,13 @@ def filled(seed, lengths, pages, page, slot_pages, heads=1, dh=64, layers=1):
 
 
 def test_fork_of_many_entries():
-    # 40 rows of 600 pages: sources read and targets written by launches of their own
+    # rows of 600 pages: sources read and targets written by launches of their own
     slots, slot_pages, page = 40, 600, 4
     rng = random.Random(7)
     lengths = [rng.choice([0, 1, page, rng.randint(1, 900), slot_pages * page]) for _ in range(slots)]
     c, m, rng = filled(1, lengths, 40 * 600, page, slot_pages)
     m.check(c)
     for n in (28, 40, 40, 35):
-        assert n * slot_pages > 16384
         dst = rng.sample(range(slots), n)
         src = [rng.randrange(slots) for _ in dst]  # targets among them, some more than once
         c.fork(ints(src), ints(dst))
@@ -69,6 +68,26 @@ def test_fork_of_many_entries():
         c.fork(ints(src), ints(dst))
         m.fork(src, dst)
         m.check(c)
+
+
+@pytest.mark.parametrize("n,slot_pages", [(64, 128), (64, 129), (63, 128), (65, 64), (65, 65), (128, 64),
+                                          (128, 65), (129, 8), (129, 64), (1, 128), (1, 129)])
+def test_forks_by_one_launch_and_by_three(n, slot_pages):
+    page = 4
+    rng = random.Random(n)
+    lengths = [rng.choice([0, rng.randint(1, slot_pages * page), slot_pages * page])
+               for _ in range(n + 1)]
+    c, m, rng = filled(n, lengths, (n + 1) * slot_pages, page, slot_pages)
+    for _ in range(3):
+        dst = rng.sample(range(n + 1), n)
+        src = [rng.randrange(n + 1) for _ in dst]
+        c.fork(ints(src), ints(dst))
+        m.fork(src, dst)
+        m.check(c)
+    before = state(c)
+    c.fork(ints(src), ints(dst[:-1] + [n + 1]))
+    assert c.fault() == pb.PB_ERR_CACHE + 256 * 3
+    assert same(before, state(c))
 
 
 def test_faulty_forks_of_many_entries_change_nothing():
@@ -99,7 +118,7 @@ def test_faulty_forks_of_many_entries_change_nothing():
     m.check(c)
 
 
-@pytest.mark.parametrize("slot_pages", [8, 12])  # a fork of 12000 entries, and of 18000
+@pytest.mark.parametrize("slot_pages", [8, 12])
 def test_lists_of_more_than_1024(slot_pages):
     slots, page = 1500, 4
     rng = random.Random(slot_pages)

@@ -710,10 +710,13 @@ cudaError_t launch_one(void (*kernel)(P...), cudaStream_t st, const A&... args) 
 }
 static_assert(sizeof(Shared) <= 48 * 1024, "no opt-in");
 
-// A fork of at most this many entries of the table is one block's work: a call of 64 sequences of up
-// to 66 pages, with what goes before and behind, takes 35.3 us so and 36.4 in three launches, whose
-// blocks read more at once where there are more.
-constexpr int64_t kForkOne = 16384;
+// A fork is one block's work for up to 128 sequences if no lane group of it has more than 128 entries
+// of the table, and three launches beyond. In a graph, pages of 16, all rows full (one launch, three):
+// 8 x 128 entries 5.0 and 6.4 us, 64 x 64 5.7 and 6.7, 64 x 96 7.1 and 7.4, 64 x 128 7.7 and 7.3, 64 x 160
+// 9.0 and 8.2, 64 x 256 14.2 and 8.6, 128 x 48 8.1 and 8.9, 128 x 64 8.6 and 7.7, 256 x 16 10.4 and 9.5, 2 x
+// 8192 204 and 66. With short sequences, whose entries the host does not know, 64 x 128 takes 4.9 and 6.8,
+// 128 x 64 7.2 and 7.9, 256 x 32 11.0 and 9.5. (Few long rows would do up to 256: 8 x 256 6.2 and 7.9.)
+constexpr int kForkRows = 128, kForkEntries = 128;
 
 unsigned blocks_for(int64_t units, int64_t per_block, int64_t most) {
   const int64_t b = (units + per_block - 1) / per_block;
@@ -822,7 +825,7 @@ pb_status pb_cache_fork(const pb_cache* cache, int32_t n, const int32_t* from, c
   if (s != PB_OK || n == 0) return s;
   const Cache c = device_view(*cache, scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (int64_t(n) * c.slot_pages <= kForkOne) {
+  if (n <= kForkRows && int64_t((n + GROUPS - 1) / GROUPS) * c.slot_pages <= kForkEntries) {
     const cudaError_t one = launch_one(fork_kernel<true>, st, c, n, from, to);
     return one == cudaSuccess ? PB_OK : cuda_failed(one, "cache fork launch");
   }
