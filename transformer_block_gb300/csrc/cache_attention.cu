@@ -27,10 +27,12 @@
 // last page's rest) arrive as zeros: what the pool holds there reaches nothing. Weights are rounded
 // to bf16 for the product with v; scores, maximum, sums and results are fp32.
 //
-// Measured (in a graph): 64 sequences of 500 to 8192 tokens, 32 heads over 8 of 128, 182 us (6.6 TB/s,
-// 99 % of a plain copy); one of 131072 tokens 86 us (6.2 TB/s); 8 sequences with 16 drafts each, 58 us
+// Measured (in a graph): 64 sequences of 500 to 8192 tokens, 32 heads over 8 of 128, 183 us (6.6 TB/s,
+// 98 % of a plain copy); one of 131072 tokens 87 us (6.1 TB/s); 8 sequences with 16 drafts each, 58 us
 // (3.6 TB/s: bound by latency inside the tiles and 6 us of start, cold instructions among it); one
-// token over 500, 4 heads of 64, 6.7 us: five accesses that depend on one another, twice a launch.
+// token over 500, 4 heads of 64, 6.3 us: five accesses that depend on one another, twice a launch. Many
+// tokens in a line read the cache once for 64 rows: the last 512 of 16384, 32 heads over 8, 406 us, the
+// last 4096 of 20480 3.5 ms (330 and 350 TFLOP/s).
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -740,6 +742,11 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
 // The block that holds a sequence's rows, from 8 sequences of 2 to 16 thousand tokens, 8 key heads:
 // 16 rows 41.5 us by blocks of 16, 42.7 by 32; 32 rows 57 (16, the cache read twice), 45.9 (32), 54
 // (64); 36 rows 58.4 (32), 53.9 (64); 64 rows 68 (32), 58 (64).
+// `rows` is the mean of the call's sequences, since their own numbers are on the device only. Where
+// they differ much the choice fits the many, and the few with more rows read their cache once for
+// every block of theirs: 255 sequences of 2048 tokens with one new token and one of 16384 with 512,
+// 4 heads a key head, take 1080 us by blocks of 16 rows (what the mean says) and 801 by 64; 256 with
+// one new token each 315 and 411; 15 of 8192 with one and one of 16384 with 16 114 and 120.
 template <int DH>
 cudaError_t launch_rows(int64_t rows, const Params& p, cudaStream_t stream) {
   return rows <= 16   ? launch<DH, 16>(p, stream)
@@ -845,7 +852,7 @@ pb_status pb_cache_attention(const pb_cache* cache, const pb_cache_attention_arg
   p.status = c.status;
   p.pieces = static_cast<Piece*>(scratch);
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + kPieceBytes);
-  // rows of an ordinary sequence of the call (padding counts: it only chooses the kernel)
+  // the mean rows of a sequence (padding counts): any choice is right, not all are as fast
   const int64_t rows = (int64_t(a.tokens) + a.sequences - 1) / a.sequences * group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = c.head_dim == 128 ? launch_rows<128>(rows, p, st) : launch_rows<64>(rows, p, st);

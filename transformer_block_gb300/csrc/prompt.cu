@@ -36,12 +36,14 @@
 // zeros over those rows of V before the product reads them. Nothing of another sequence reaches a
 // result.
 //
-// Measured (in a graph): 16384 tokens, 32 heads over 8, 1365 us (1.61 PFLOP/s, 81 % of the library's
-// product rate; tensor pipe 67 % busy; called over and over the power limit makes it 1500); 15 prompts of
-// 1 to 2049 tokens, 8096 in all, the same heads, 93 us (890 TFLOP/s of the pairs that are seen); 4 x
-// 2048 tokens, 16 heads, window 512, 55 us; 128 tokens 6 us. What is left of the short ones is the start
-// and end of an item, about 6500 cycles: its first softmax and last P V have nothing beside them, and
-// its result leaves by plain stores.
+// Measured (in a graph): 16384 tokens, 32 heads over 8, 1365 to 1416 us on two boxes (1.55 to 1.61
+// PFLOP/s, 80 to 83 % of the library's product rate; tensor pipe 67 % busy; called over and over the
+// power limit makes it 1480 to 1530); 15 prompts of 1 to 2049 tokens, 8096 in all, the same heads, 94 us
+// (870 TFLOP/s of the pairs that are seen); 4 x 2048 tokens, 16 heads, window 512, 55 us; 128 tokens 6
+// us. What is left of the short ones is the start and end of an item, about 6500 cycles: its first
+// softmax and last P V have nothing beside them, and its result leaves by plain stores. 168 registers a
+// thread, the most that 384 threads may be compiled with, spill 44 bytes of stores and 308 of loads
+// (96/200, 104/192 or 120/184 registers a warpgroup; 88/208: 40 and 284).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -825,8 +827,11 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   int* count = static_cast<int*>(scratch);
   Entry* entries = reinterpret_cast<Entry*>(static_cast<uint8_t*>(scratch) + kHeaderBytes);
   const int64_t items = int64_t(p.capacity) * p.kv_heads;
-  // Few sequences and items: each block lists its own. With a launch for the list 128 tokens take 7.1
-  // us instead of 5.9, the ragged 8096 tokens 96 instead of 92.
+  // Few sequences and items: each block lists its own. With a launch for the list 128 tokens take 7.8
+  // us instead of 6.3, the ragged 8096 tokens 96 instead of 94, 128 sequences of 64 tokens 50.0 instead
+  // of 45.9 (129, listed by the launch: 50.4), 128 of one token 39 instead of 35. Near 64 items an SM the
+  // launch is as good or better, by 2 % at most: 8192 tokens, window 64, 296 heads over 148 (9620 items)
+  // 399 us instead of 408, 148 over 148 255 instead of 257, 8 x 1024 with 128 heads 209 instead of 212.
   Params mine = p;
   mine.own_list = p.sequences <= kOwnSequences && items <= int64_t(kOwnItems) * sms;
   if (!mine.own_list) {

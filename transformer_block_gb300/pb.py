@@ -1154,8 +1154,8 @@ class Cache:
         sequence are a tree, parents[t] the number of the one that t follows, -1 for the token before
         them (None: each follows the one before). ``window`` and ``scale`` as in
         ``prompt_attention``. ``scratch``: a uint8 CUDA tensor of ``attention_scratch_bytes`` (found
-        unless given). Rows of ``out`` in no sequence stay as they are, and any rows where
-        ``fault()`` is not 0 (a new ``out`` holds anything there)."""
+        unless given). Rows of ``out`` in no sequence stay as they are; where ``fault()`` is not 0
+        any may (a new ``out`` holds anything there)."""
         if stream is not None:
             return _run_on(stream, self.attention, q, slots, starts, parents, layer, window, scale,
                            out, scratch)
