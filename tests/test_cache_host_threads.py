@@ -111,3 +111,19 @@ def test_caches_are_independent(counting):
         free.start()
         free.join(20)
         assert not free.is_alive()
+
+
+def test_what_runs_inside_a_call_may_change_the_cache(counting, monkeypatch):
+    # a finalizer or a signal's handler runs on the thread that is in a call, and frees a slot
+    c = small()
+
+    def freeing(stream):
+        monkeypatch.setattr(pb, "_stream", lambda stream: None)
+        c.truncate(ints(1), ints(0))
+
+    monkeypatch.setattr(pb, "_stream", freeing)
+    done = threading.Thread(target=c.extend, args=(ints(0), ints(0, 1)), daemon=True)
+    done.start()
+    done.join(20)
+    assert not done.is_alive()
+    assert counting.calls == ["pb_cache_truncate", "pb_cache_extend"]

@@ -1067,7 +1067,9 @@ class Cache:
         # of the calls that change the cache, which run one after another
         self.scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=k.device)
         self._scratch = self.scratch.data_ptr()
-        self._changing = threading.Lock()
+        # taken again by what runs while it is held, on the same thread: a finalizer that frees a slot,
+        # a signal's handler (they come between calls of the library, not inside one)
+        self._changing = threading.RLock()
         self._made_on = _stream(None) if k.is_cuda else None
         self._made_by = threading.get_ident()
         self._attention_scratch = None
