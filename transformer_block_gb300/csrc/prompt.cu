@@ -36,7 +36,7 @@
 // zeros over those rows of V before the product reads them. Nothing of another sequence reaches a
 // result.
 //
-// Measured (in a graph): 16384 tokens, 32 heads over 8, 1365 to 1416 us on two boxes (1.55 to 1.61
+// Measured (in a graph): 16384 tokens, 32 heads over 8, 1365 to 1416 us on two GPUs (1.55 to 1.61
 // PFLOP/s, 80 to 83 % of the library's product rate; tensor pipe 67 % busy; called over and over the
 // power limit makes it 1480 to 1530); 15 prompts of 1 to 2049 tokens, 8096 in all, the same heads, 94 us
 // (870 TFLOP/s of the pairs that are seen); 4 x 2048 tokens, 16 heads, window 512, 55 us; 128 tokens 6
